@@ -21,6 +21,7 @@ OK, EINVAL, ESHAPE, EALIGN, EHIP, ENOTIMPL = range(6)
 F32, BF16 = 0, 1
 E4M3FN, E5M2 = 0, 1
 GRAN_TENSOR, GRAN_1x128, GRAN_128x128 = 0, 1, 2
+ACT_SILU, ACT_GELU = 0, 1
 MAX_FINITE = {E4M3FN: 448.0, E5M2: 57344.0}
 
 # every exported symbol declared in include/fp8q.h
@@ -46,6 +47,14 @@ SYMBOLS = (
     "fp8q_quantize_tensor_dq",
     "fp8q_quantize_tensor_delayed",
     "fp8q_gemm_blockscaled_qt",
+    "fp8q_rmsnorm_1x128",
+    "fp8q_rmsnorm_bwd_workspace",
+    "fp8q_rmsnorm_bwd",
+    "fp8q_glu_blockscaled",
+    "fp8q_glu_blockscaled_fast",
+    "fp8q_glu_blockscaled_q",
+    "fp8q_glu_bwd_q",
+    "fp8q_gemm_blockscaled_few",
 )
 
 
@@ -108,6 +117,20 @@ def lib() -> ctypes.CDLL:
                                                vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp]),
             "fp8q_gemm_blockscaled_q": (i32, [vp, i32, i64, vp, i64, i64, vp, i32, i64, vp, i32, i64, i64, i32, f32,
                                               vp, i64, vp, i64, i64, i64, i64, vp]),
+            "fp8q_rmsnorm_1x128": (i32, [vp, i32, i64, vp, i64, vp, i32, i64, i64, f32, vp, i64, vp, i64, i32, f32, vp,
+                                         i64, vp, i64, vp, vp]),
+            "fp8q_rmsnorm_bwd_workspace": (i64, [i64, i64]),
+            "fp8q_rmsnorm_bwd": (i32, [vp, i32, i64, vp, i64, vp, i32, vp, vp, i64, i64, i64, vp, i64, vp, vp, i64, vp]),
+            "fp8q_glu_blockscaled": (i32, [vp, i32, i64, vp, i64, i64, vp, vp, i32, i64, vp, vp, i64, i64, i32, vp, i32,
+                                           i64, vp, i64, i64, i64, i64, vp]),
+            "fp8q_glu_blockscaled_fast": (i32, [vp, i32, i64, vp, i64, i64, vp, vp, i32, i64, vp, vp, i64, i64, i32, vp,
+                                                i32, i64, vp, i64, i64, i64, i64, vp]),
+            "fp8q_glu_blockscaled_q": (i32, [vp, i32, i64, vp, i64, i64, vp, vp, i32, i64, vp, vp, i64, i64, i32, i32,
+                                             f32, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp]),
+            "fp8q_glu_bwd_q": (i32, [vp, i32, i64, vp, i64, i32, i32, f32, vp, i64, vp, i64, vp, i64, vp, i64, i32, vp,
+                                     i64, vp, i64, i64, i64, vp]),
+            "fp8q_gemm_blockscaled_few": (i32, [vp, i32, i64, vp, i64, i64, vp, i32, i64, vp, i32, i64, i64, vp, i32,
+                                                i64, i64, i64, i64, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -247,3 +270,63 @@ def fp8q_gemm_blockscaled_qt(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, gb, 
     _check(lib().fp8q_gemm_blockscaled_qt(_ptr(A), fa, lda, _ptr(sA), sA_sm, sA_skb, _ptr(B), fb, ldb, _ptr(sB), gb,
                                           sB_sn, sB_skb, fc, eps, _ptr(Cqt), ldcqt, _ptr(Cst), ld_cst, _ptr(Cq), ldcq,
                                           _ptr(Cs), ld_cs, M, N, K, _stream(stream, A)))
+
+
+def _same_dt(t, *others) -> int:
+    """The element type of t, which the tensors among `others` must share."""
+    for o in others:
+        if o is not None and not isinstance(o, int) and o.dtype != t.dtype:
+            raise TypeError(f"these operands share one dtype, got {t.dtype} and {o.dtype}")
+    return _dt(t)
+
+
+def fp8q_rmsnorm_1x128(x, ldx, res, ldr, w, rows, cols, norm_eps, z, ldz, y, ldy, f, eps, q, ldq, scales, ld_s,
+                       rstd=None, stream=None) -> None:
+    _check(lib().fp8q_rmsnorm_1x128(_ptr(x), _same_dt(x, res, z, y), ldx, _ptr(res), ldr, _ptr(w), _dt(w), rows, cols,
+                                    norm_eps, _ptr(z), ldz, _ptr(y), ldy, f, eps, _ptr(q), ldq, _ptr(scales), ld_s,
+                                    _ptr(rstd), _stream(stream, x)))
+
+
+def fp8q_rmsnorm_bwd_workspace(rows, cols) -> int:
+    return lib().fp8q_rmsnorm_bwd_workspace(rows, cols)
+
+
+def fp8q_rmsnorm_bwd(dy, lddy, z, ldz, w, rstd, dres, lddr, rows, cols, dx, lddx, dw=None, ws=None, ws_bytes=0,
+                     stream=None) -> None:
+    _check(lib().fp8q_rmsnorm_bwd(_ptr(dy), _same_dt(dy, z, dres, dx), lddy, _ptr(z), ldz, _ptr(w), _dt(w), _ptr(rstd),
+                                  _ptr(dres), lddr, rows, cols, _ptr(dx), lddx, _ptr(dw), _ptr(ws), ws_bytes,
+                                  _stream(stream, dy)))
+
+
+def fp8q_glu_blockscaled(A, fa, lda, sA, sA_sm, sA_skb, Bg, Bu, fb, ldb, sBg, sBu, sB_sn, sB_skb, act, H, ldh, gu, ldgu,
+                         M, F, K, stream=None) -> None:
+    _check(lib().fp8q_glu_blockscaled(_ptr(A), fa, lda, _ptr(sA), sA_sm, sA_skb, _ptr(Bg), _ptr(Bu), fb, ldb, _ptr(sBg),
+                                      _ptr(sBu), sB_sn, sB_skb, act, _ptr(H), _dt(H), ldh, _ptr(gu), ldgu, M, F, K,
+                                      _stream(stream, A)))
+
+
+def fp8q_glu_blockscaled_fast(A, fa, lda, sA, sA_sm, sA_skb, Bg, Bu, fb, ldb, sBg, sBu, sB_sn, sB_skb, act, H, ldh, gu,
+                              ldgu, M, F, K, stream=None) -> None:
+    _check(lib().fp8q_glu_blockscaled_fast(_ptr(A), fa, lda, _ptr(sA), sA_sm, sA_skb, _ptr(Bg), _ptr(Bu), fb, ldb,
+                                           _ptr(sBg), _ptr(sBu), sB_sn, sB_skb, act, _ptr(H), _dt(H), ldh, _ptr(gu),
+                                           ldgu, M, F, K, _stream(stream, A)))
+
+
+def fp8q_glu_blockscaled_q(A, fa, lda, sA, sA_sm, sA_skb, Bg, Bu, fb, ldb, sBg, sBu, sB_sn, sB_skb, act, fc, eps, Hq,
+                           ldhq, Hs, ld_hs, gu, ldgu, M, F, K, stream=None) -> None:
+    _check(lib().fp8q_glu_blockscaled_q(_ptr(A), fa, lda, _ptr(sA), sA_sm, sA_skb, _ptr(Bg), _ptr(Bu), fb, ldb,
+                                        _ptr(sBg), _ptr(sBu), sB_sn, sB_skb, act, fc, eps, _ptr(Hq), ldhq, _ptr(Hs),
+                                        ld_hs, _ptr(gu), ldgu, M, F, K, _stream(stream, A)))
+
+
+def fp8q_glu_bwd_q(dH, lddh, gu, ldgu, act, fc, eps, Dq, lddq, Ds, ld_ds, Dt, lddt, Dst, ld_dst, fh, Ht, ldht, Hst,
+                   ld_hst, M, F, stream=None) -> None:
+    _check(lib().fp8q_glu_bwd_q(_ptr(dH), _dt(dH), lddh, _ptr(gu), ldgu, act, fc, eps, _ptr(Dq), lddq, _ptr(Ds), ld_ds,
+                                _ptr(Dt), lddt, _ptr(Dst), ld_dst, fh, _ptr(Ht), ldht, _ptr(Hst), ld_hst, M, F,
+                                _stream(stream, dH)))
+
+
+def fp8q_gemm_blockscaled_few(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, gb, sB_sn, sB_skb, C, ldc, M, N, K,
+                              stream=None) -> None:
+    _check(lib().fp8q_gemm_blockscaled_few(_ptr(A), fa, lda, _ptr(sA), sA_sm, sA_skb, _ptr(B), fb, ldb, _ptr(sB), gb,
+                                           sB_sn, sB_skb, _ptr(C), _dt(C), ldc, M, N, K, _stream(stream, A)))

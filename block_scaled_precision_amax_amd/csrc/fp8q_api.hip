@@ -7,7 +7,7 @@
 
 #include <atomic>
 
-#include "fp8q_internal.h"
+#include "fp8q_ffn.h"
 
 namespace fp8q {
 
@@ -71,6 +71,78 @@ int check_block_quant(const char* fn, const void* x, int dt, int64_t rows, int64
   if ((ldx * esize(dt)) % 16 != 0 || ldq % 16 != 0)
     return fail(FP8Q_EALIGN, "%s: ldx and ldq must keep rows 16-byte aligned", fn);
   return FP8Q_OK;
+}
+
+// Shared checks of the norm and its gradient.
+int check_norm(const char* fn, int dt, int wdt, int64_t rows, int64_t cols) {
+  if (!valid_dt(dt) || !valid_dt(wdt)) return fail(FP8Q_EINVAL, "%s: bad dtype", fn);
+  if (rows <= 0 || cols <= 0) return fail(FP8Q_EINVAL, "%s: rows and cols must be positive", fn);
+  if (cols % 128 != 0 || cols > kNormMaxCols)
+    return fail(FP8Q_ESHAPE, "%s: cols (%lld) must be a multiple of 128, at most %lld", fn, (long long)cols,
+                (long long)kNormMaxCols);
+  if (rows > 0x7FFFFFFF) return fail(FP8Q_ESHAPE, "%s: more than 2^31-1 rows", fn);
+  return FP8Q_OK;
+}
+struct NormRow {
+  const void* p;
+  int64_t ld;
+};
+int check_norm_rows(const char* fn, const NormRow* r, int n, int dt, int64_t cols) {
+  for (int i = 0; i < n; ++i) {
+    if (!r[i].p) continue;
+    if (r[i].ld < cols) return fail(FP8Q_EINVAL, "%s: leading dimension smaller than the row", fn);
+    if (!aligned(r[i].p, 16) || (r[i].ld * esize(dt)) % 16 != 0)
+      return fail(FP8Q_EALIGN, "%s: tensors and their rows must be 16-byte aligned", fn);
+  }
+  return FP8Q_OK;
+}
+
+// Shared checks of the gated projections and the product of a few rows.
+int check_proj(const char* fn, const uint8_t* A, int fa, int64_t lda, const float* sA, int64_t sA_sm, int64_t sA_skb,
+               const uint8_t* B0, const uint8_t* B1, int fb, int64_t ldb, const float* s0, const float* s1,
+               int64_t sB_sn, int64_t sB_skb, int64_t M, int64_t N, int64_t K) {
+  if (!A || !sA || !B0 || !B1 || !s0 || !s1) return fail(FP8Q_EINVAL, "%s: null pointer", fn);
+  if (!valid_fmt(fa) || !valid_fmt(fb)) return fail(FP8Q_EINVAL, "%s: bad format", fn);
+  if (M <= 0 || N <= 0 || K <= 0) return fail(FP8Q_EINVAL, "%s: the sizes must be positive", fn);
+  if (K % 128 != 0) return fail(FP8Q_ESHAPE, "%s: K (%lld) must be a multiple of 128", fn, (long long)K);
+  if (lda < K || ldb < K) return fail(FP8Q_EINVAL, "%s: leading dimension too small", fn);
+  if (sA_sm < 0 || sA_skb < 0 || sB_sn < 0 || sB_skb < 0) return fail(FP8Q_EINVAL, "%s: negative scale stride", fn);
+  if (!aligned(A, 16) || !aligned(B0, 16) || !aligned(B1, 16) || lda % 16 != 0 || ldb % 16 != 0)
+    return fail(FP8Q_EALIGN, "%s: the operands and their leading dimensions must be 16-byte aligned", fn);
+  if (!aligned(sA, 4) || !aligned(s0, 4) || !aligned(s1, 4)) return fail(FP8Q_EALIGN, "%s: misaligned scales", fn);
+  // per-lane operand offsets are 32-bit
+  if ((M - 1) * lda + K > 0xFFFFFFFFll || (N - 1) * ldb + K > 0xFFFFFFFFll)
+    return fail(FP8Q_ESHAPE, "%s: an operand spans 4 GiB or more", fn);
+  return FP8Q_OK;
+}
+int check_gu(const char* fn, int act, const uint16_t* gu, int64_t ldgu, int64_t F) {
+  if (act != FP8Q_ACT_SILU && act != FP8Q_ACT_GELU) return fail(FP8Q_EINVAL, "%s: bad activation", fn);
+  if (gu && ldgu < 2 * F) return fail(FP8Q_EINVAL, "%s: leading dimension too small", fn);
+  if (!aligned(gu, 2)) return fail(FP8Q_EALIGN, "%s: misaligned gu", fn);
+  return FP8Q_OK;
+}
+Proj make_proj(const uint8_t* A, int fa, int64_t lda, const float* sA, int64_t sA_sm, int64_t sA_skb,
+               const uint8_t* B0, const uint8_t* B1, int fb, int64_t ldb, const float* s0, const float* s1, int gb,
+               int64_t sB_sn, int64_t sB_skb, int64_t M, int64_t N, int64_t K) {
+  Proj p = {};
+  p.A = A, p.fa = fa, p.lda = lda, p.sA = sA, p.sA_sm = sA_sm, p.sA_skb = sA_skb;
+  p.B0 = B0, p.B1 = B1, p.fb = fb, p.ldb = ldb, p.s0 = s0, p.s1 = s1, p.gb = gb, p.sB_sn = sB_sn, p.sB_skb = sB_skb;
+  p.M = M, p.N = N, p.K = K;
+  return p;
+}
+int glu_entry(const char* fn, bool fast, const uint8_t* A, int fa, int64_t lda, const float* sA, int64_t sA_sm,
+              int64_t sA_skb, const uint8_t* Bg, const uint8_t* Bu, int fb, int64_t ldb, const float* sBg,
+              const float* sBu, int64_t sB_sn, int64_t sB_skb, int act, void* H, int out_dt, int64_t ldh,
+              uint16_t* gu, int64_t ldgu, int64_t M, int64_t F, int64_t K, void* stream) {
+  if (!H) return fail(FP8Q_EINVAL, "%s: null pointer", fn);
+  if (!valid_dt(out_dt)) return fail(FP8Q_EINVAL, "%s: bad dtype", fn);
+  if (int rc = check_proj(fn, A, fa, lda, sA, sA_sm, sA_skb, Bg, Bu, fb, ldb, sBg, sBu, sB_sn, sB_skb, M, F, K)) return rc;
+  if (int rc = check_gu(fn, act, gu, ldgu, F)) return rc;
+  if (ldh < F) return fail(FP8Q_EINVAL, "%s: leading dimension too small", fn);
+  if (!aligned(H, out_dt == FP8Q_F32 ? 4 : 2)) return fail(FP8Q_EALIGN, "%s: misaligned H", fn);
+  Proj p = make_proj(A, fa, lda, sA, sA_sm, sA_skb, Bg, Bu, fb, ldb, sBg, sBu, FP8Q_GRAN_128x128, sB_sn, sB_skb, M, F, K);
+  p.out = H, p.ldo = ldh, p.out_dt = out_dt, p.act = act, p.gu = gu, p.ldgu = ldgu;
+  return launch_glu(p, fast, fn, S(stream));
 }
 
 }  // namespace
@@ -356,6 +428,136 @@ int fp8q_gemm_blockscaled_fast(const uint8_t* A, fp8q_format fa, int64_t lda, co
                                int64_t N, int64_t K, void* stream) {
   return gemm_entry("gemm_blockscaled_fast", A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, gb, sB_sn,
                     sB_skb, C, out_dt, ldc, M, N, K, true, stream);
+}
+
+int fp8q_rmsnorm_1x128(const void* x, fp8q_dtype dt, int64_t ldx, const void* res, int64_t ldr, const void* w,
+                       fp8q_dtype wdt, int64_t rows, int64_t cols, float norm_eps, void* z, int64_t ldz, void* y,
+                       int64_t ldy, fp8q_format f, float eps, uint8_t* q, int64_t ldq, float* scales, int64_t ld_s,
+                       float* rstd, void* stream) {
+  const char* fn = "rmsnorm_1x128";
+  if (!x || !w || (!q && !y)) return fail(FP8Q_EINVAL, "%s: null pointer", fn);
+  if ((q == nullptr) != (scales == nullptr)) return fail(FP8Q_EINVAL, "%s: q and scales go together", fn);
+  if (!valid_fmt(f)) return fail(FP8Q_EINVAL, "%s: bad format", fn);
+  if (!(eps > 0.0f) || !isfinite(eps)) return fail(FP8Q_EINVAL, "%s: eps must be finite and > 0", fn);
+  if (!(norm_eps > 0.0f) || !isfinite(norm_eps)) return fail(FP8Q_EINVAL, "%s: norm_eps must be finite and > 0", fn);
+  if (int rc = check_norm(fn, dt, wdt, rows, cols)) return rc;
+  const NormRow r[] = {{x, ldx}, {res, ldr}, {z, ldz}, {y, ldy}};
+  if (int rc = check_norm_rows(fn, r, 4, dt, cols)) return rc;
+  if (q && (ldq < cols || ld_s < cols / 128)) return fail(FP8Q_EINVAL, "%s: leading dimension smaller than the row", fn);
+  if (!aligned(w, 16) || (q && (!aligned(q, 16) || ldq % 16 != 0)))
+    return fail(FP8Q_EALIGN, "%s: w, q and the rows of q must be 16-byte aligned", fn);
+  if (!aligned(scales, 4) || !aligned(rstd, 4)) return fail(FP8Q_EALIGN, "%s: scales and rstd must be 4-byte aligned", fn);
+  NormFwd p;
+  p.x = x, p.res = res, p.w = w, p.z = z, p.y = y, p.q = q, p.scales = scales, p.rstd = rstd;
+  p.ldx = ldx, p.ldr = ldr, p.ldz = ldz, p.ldy = ldy, p.ldq = ldq, p.ld_s = ld_s, p.rows = rows, p.cols = cols;
+  p.neps = norm_eps, p.qeps = eps, p.dt = dt, p.wdt = wdt, p.fmt = f;
+  return launch_rmsnorm_1x128(p, S(stream));
+}
+
+int64_t fp8q_rmsnorm_bwd_workspace(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0 || cols % 128 != 0 || cols > kNormMaxCols) return 0;
+  return 4 * cols * rmsnorm_bwd_parts(rows, cols);
+}
+
+int fp8q_rmsnorm_bwd(const void* dy, fp8q_dtype dt, int64_t lddy, const void* z, int64_t ldz, const void* w,
+                     fp8q_dtype wdt, const float* rstd, const void* dres, int64_t lddr, int64_t rows, int64_t cols,
+                     void* dx, int64_t lddx, float* dw, void* ws, int64_t ws_bytes, void* stream) {
+  const char* fn = "rmsnorm_bwd";
+  if (!dy || !z || !w || !rstd || !dx) return fail(FP8Q_EINVAL, "%s: null pointer", fn);
+  if (int rc = check_norm(fn, dt, wdt, rows, cols)) return rc;
+  const NormRow r[] = {{dy, lddy}, {z, ldz}, {dres, lddr}, {dx, lddx}};
+  if (int rc = check_norm_rows(fn, r, 4, dt, cols)) return rc;
+  if (dw && (!ws || ws_bytes < fp8q_rmsnorm_bwd_workspace(rows, cols)))
+    return fail(FP8Q_EINVAL, "%s: the workspace needs %lld bytes", fn, (long long)fp8q_rmsnorm_bwd_workspace(rows, cols));
+  if (!aligned(w, 16) || (dw && !aligned(ws, 16))) return fail(FP8Q_EALIGN, "%s: w and ws must be 16-byte aligned", fn);
+  if (!aligned(rstd, 4) || !aligned(dw, 4)) return fail(FP8Q_EALIGN, "%s: rstd and dw must be 4-byte aligned", fn);
+  NormBwd p;
+  p.dy = dy, p.z = z, p.w = w, p.dres = dres, p.rstd = rstd, p.dx = dx, p.dw = dw, p.ws = (float*)ws;
+  p.lddy = lddy, p.ldz = ldz, p.lddr = lddr, p.lddx = lddx, p.rows = rows, p.cols = cols, p.dt = dt, p.wdt = wdt;
+  return launch_rmsnorm_bwd(p, S(stream));
+}
+
+int fp8q_glu_blockscaled(const uint8_t* A, fp8q_format fa, int64_t lda, const float* sA, int64_t sA_sm,
+                         int64_t sA_skb, const uint8_t* Bg, const uint8_t* Bu, fp8q_format fb, int64_t ldb,
+                         const float* sBg, const float* sBu, int64_t sB_sn, int64_t sB_skb, fp8q_act act, void* H,
+                         fp8q_dtype out_dt, int64_t ldh, uint16_t* gu, int64_t ldgu, int64_t M, int64_t F, int64_t K,
+                         void* stream) {
+  return glu_entry("glu_blockscaled", false, A, fa, lda, sA, sA_sm, sA_skb, Bg, Bu, fb, ldb, sBg, sBu, sB_sn, sB_skb,
+                   act, H, out_dt, ldh, gu, ldgu, M, F, K, stream);
+}
+
+int fp8q_glu_blockscaled_fast(const uint8_t* A, fp8q_format fa, int64_t lda, const float* sA, int64_t sA_sm,
+                              int64_t sA_skb, const uint8_t* Bg, const uint8_t* Bu, fp8q_format fb, int64_t ldb,
+                              const float* sBg, const float* sBu, int64_t sB_sn, int64_t sB_skb, fp8q_act act,
+                              void* H, fp8q_dtype out_dt, int64_t ldh, uint16_t* gu, int64_t ldgu, int64_t M,
+                              int64_t F, int64_t K, void* stream) {
+  return glu_entry("glu_blockscaled_fast", true, A, fa, lda, sA, sA_sm, sA_skb, Bg, Bu, fb, ldb, sBg, sBu, sB_sn,
+                   sB_skb, act, H, out_dt, ldh, gu, ldgu, M, F, K, stream);
+}
+
+int fp8q_glu_blockscaled_q(const uint8_t* A, fp8q_format fa, int64_t lda, const float* sA, int64_t sA_sm,
+                           int64_t sA_skb, const uint8_t* Bg, const uint8_t* Bu, fp8q_format fb, int64_t ldb,
+                           const float* sBg, const float* sBu, int64_t sB_sn, int64_t sB_skb, fp8q_act act,
+                           fp8q_format fc, float eps, uint8_t* Hq, int64_t ldhq, float* Hs, int64_t ld_hs,
+                           uint16_t* gu, int64_t ldgu, int64_t M, int64_t F, int64_t K, void* stream) {
+  const char* fn = "glu_blockscaled_q";
+  if (!Hq || !Hs) return fail(FP8Q_EINVAL, "%s: null pointer", fn);
+  if (!valid_fmt(fc)) return fail(FP8Q_EINVAL, "%s: bad format", fn);
+  if (!(eps > 0.0f) || !isfinite(eps)) return fail(FP8Q_EINVAL, "%s: eps must be finite and > 0", fn);
+  if (int rc = check_proj(fn, A, fa, lda, sA, sA_sm, sA_skb, Bg, Bu, fb, ldb, sBg, sBu, sB_sn, sB_skb, M, F, K)) return rc;
+  if (int rc = check_gu(fn, act, gu, ldgu, F)) return rc;
+  if (F % 128 != 0) return fail(FP8Q_ESHAPE, "%s: F (%lld) must be a multiple of 128", fn, (long long)F);
+  if (ldhq < F || ld_hs < F / 128) return fail(FP8Q_EINVAL, "%s: leading dimension too small", fn);
+  if (!aligned(Hs, 4)) return fail(FP8Q_EALIGN, "%s: misaligned scales", fn);
+  Proj p = make_proj(A, fa, lda, sA, sA_sm, sA_skb, Bg, Bu, fb, ldb, sBg, sBu, FP8Q_GRAN_128x128, sB_sn, sB_skb, M, F, K);
+  p.out = Hq, p.ldo = ldhq, p.scales = Hs, p.ld_s = ld_hs, p.fc = fc, p.eps = eps, p.act = act, p.gu = gu, p.ldgu = ldgu;
+  return launch_glu(p, false, fn, S(stream));
+}
+
+int fp8q_glu_bwd_q(const void* dH, fp8q_dtype dt, int64_t lddh, const uint16_t* gu, int64_t ldgu, fp8q_act act,
+                   fp8q_format fc, float eps, uint8_t* Dq, int64_t lddq, float* Ds, int64_t ld_ds, uint8_t* Dt,
+                   int64_t lddt, float* Dst, int64_t ld_dst, fp8q_format fh, uint8_t* Ht, int64_t ldht, float* Hst,
+                   int64_t ld_hst, int64_t M, int64_t F, void* stream) {
+  const char* fn = "glu_bwd_q";
+  if (!dH || !gu || !Dq || !Ds) return fail(FP8Q_EINVAL, "%s: null pointer", fn);
+  if ((Dt == nullptr) != (Dst == nullptr) || (Ht == nullptr) != (Hst == nullptr))
+    return fail(FP8Q_EINVAL, "%s: a transposed output needs both its codes and its scales (or neither)", fn);
+  if (!valid_dt(dt) || !valid_fmt(fc) || !valid_fmt(fh)) return fail(FP8Q_EINVAL, "%s: bad dtype or format", fn);
+  if (act != FP8Q_ACT_SILU && act != FP8Q_ACT_GELU) return fail(FP8Q_EINVAL, "%s: bad activation", fn);
+  if (!(eps > 0.0f) || !isfinite(eps)) return fail(FP8Q_EINVAL, "%s: eps must be finite and > 0", fn);
+  if (M <= 0 || F <= 0) return fail(FP8Q_EINVAL, "%s: M and F must be positive", fn);
+  if (F % 128 != 0) return fail(FP8Q_ESHAPE, "%s: F (%lld) must be a multiple of 128", fn, (long long)F);
+  const int64_t Mp = (M + 127) / 128 * 128;
+  if (lddh < F || ldgu < 2 * F || lddq < 2 * F || ld_ds < 2 * F / 128 || (Dt && (lddt < Mp || ld_dst < Mp / 128)) ||
+      (Ht && (ldht < Mp || ld_hst < Mp / 128)))
+    return fail(FP8Q_EINVAL, "%s: leading dimension too small", fn);
+  if (!aligned(dH, 16) || (lddh * esize(dt)) % 16 != 0 || !aligned(gu, 16) || ldgu % 8 != 0 || !aligned(Dq, 16) ||
+      lddq % 16 != 0 || (Dt && (!aligned(Dt, 16) || lddt % 16 != 0)) || (Ht && (!aligned(Ht, 16) || ldht % 16 != 0)))
+    return fail(FP8Q_EALIGN, "%s: dH, gu, Dq, Dt, Ht and their rows must be 16-byte aligned", fn);
+  if (!aligned(Ds, 4) || !aligned(Dst, 4) || !aligned(Hst, 4)) return fail(FP8Q_EALIGN, "%s: misaligned scales", fn);
+  GluBwd p;
+  p.dh = dH, p.gu = gu, p.d = Dq, p.dt_ = Dt, p.ht = Ht, p.ds = Ds, p.dts = Dst, p.hts = Hst;
+  p.lddh = lddh, p.ldgu = ldgu, p.ldd = lddq, p.ld_ds = ld_ds, p.lddt = lddt, p.ld_dts = ld_dst, p.ldht = ldht,
+  p.ld_hts = ld_hst, p.M = M, p.F = F, p.eps = eps, p.dh_dt = dt, p.act = act, p.fc = fc, p.fh = fh;
+  return launch_glu_bwd(p, S(stream));
+}
+
+int fp8q_gemm_blockscaled_few(const uint8_t* A, fp8q_format fa, int64_t lda, const float* sA, int64_t sA_sm,
+                              int64_t sA_skb, const uint8_t* B, fp8q_format fb, int64_t ldb, const float* sB,
+                              fp8q_gran gb, int64_t sB_sn, int64_t sB_skb, void* C, fp8q_dtype out_dt, int64_t ldc,
+                              int64_t M, int64_t N, int64_t K, void* stream) {
+  const char* fn = "gemm_blockscaled_few";
+  if (!C) return fail(FP8Q_EINVAL, "%s: null pointer", fn);
+  if (!valid_dt(out_dt)) return fail(FP8Q_EINVAL, "%s: bad dtype", fn);
+  if (gb != FP8Q_GRAN_128x128 && gb != FP8Q_GRAN_1x128)
+    return fail(FP8Q_EINVAL, "%s: B scales must be 128x128 or 1x128", fn);
+  if (int rc = check_proj(fn, A, fa, lda, sA, sA_sm, sA_skb, B, B, fb, ldb, sB, sB, sB_sn, sB_skb, M, N, K)) return rc;
+  if (M > kFewRows) return fail(FP8Q_ESHAPE, "%s: M (%lld) is more than %lld rows", fn, (long long)M, (long long)kFewRows);
+  if (ldc < N) return fail(FP8Q_EINVAL, "%s: leading dimension too small", fn);
+  if (!aligned(C, out_dt == FP8Q_F32 ? 4 : 2)) return fail(FP8Q_EALIGN, "%s: misaligned C", fn);
+  Proj p = make_proj(A, fa, lda, sA, sA_sm, sA_skb, B, nullptr, fb, ldb, sB, nullptr, gb, sB_sn, sB_skb, M, N, K);
+  p.out = C, p.ldo = ldc, p.out_dt = out_dt;
+  return launch_few(p, fn, S(stream));
 }
 
 }  // extern "C"

@@ -60,6 +60,10 @@ typedef enum { FP8Q_GRAN_TENSOR = 0, FP8Q_GRAN_1x128 = 1, FP8Q_GRAN_128x128 = 2 
  * average smoothing the amax, as Transformer Engine does; [A] 4.3). */
 typedef enum { FP8Q_STAT_MAX = 0, FP8Q_STAT_MEAN = 1, FP8Q_STAT_EMA = 2 } fp8q_window_stat;
 
+/* Activation of the gated projection: SiLU g / (1 + e^-g), or GELU in its
+ * tanh form g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2. */
+typedef enum { FP8Q_ACT_SILU = 0, FP8Q_ACT_GELU = 1 } fp8q_act;
+
 /* Delayed-scaling state ([A] 4.2 DelayedScaler): a window of the last
  * `window` amax values and the scale derived from them.  Device-resident,
  * caller-allocated (8-byte aligned), plain data (copy it to the host to
@@ -345,6 +349,116 @@ int fp8q_gemm_blockscaled_qt(const uint8_t* A, fp8q_format fa, int64_t lda, cons
 int fp8q_gemm_mx(const uint8_t* A, fp8q_format fa, int64_t lda, const uint8_t* sA, int64_t ld_sa,
                  const uint8_t* B, fp8q_format fb, int64_t ldb, const uint8_t* sB, int64_t ld_sb, void* C,
                  fp8q_dtype out_dt, int64_t ldc, int64_t M, int64_t N, int64_t K, void* stream);
+
+/* ---- Feed-forward operators: what stands between two block-scaled products
+ * of a transformer layer, forward and backward, for prompts, training steps
+ * and single tokens. */
+
+/* Root-mean-square norm with the residual's addition and a 1x128 FP8 output,
+ * the input of the next fp8q_gemm_blockscaled / fp8q_glu_blockscaled ([A]
+ * 5.1: casts through a wide type between FP8 operations eat the gain):
+ *   v = x + res (res NULL: v = x);  rstd = 1 / sqrt(mean_c(v^2) + norm_eps);
+ *   y = (v * rstd) * w;  q, scales = fp8q_quantize_1x128(y).
+ * v, the sum of squares and y are fp32; z and y are rounded once, to the
+ * nearest even, when they are stored, and neither the norm nor the codes
+ * read the rounded values.
+ * x, res, z, y: rows x cols of dtype dt (row strides ldx, ldr, ldz, ldy).
+ * res, z, y, rstd nullable; z is v (the residual stream), and may be x or
+ * res itself.  w: cols weights of dtype wdt.  q nullable together with
+ * scales (y is then required): codes of format f at q[r*ldq + c], fp32
+ * scales at scales[r*ld_s + c/128], ld_s >= cols/128; eps is their amax
+ * clamp.  rstd: rows fp32, what fp8q_rmsnorm_bwd takes.
+ * cols % 128 == 0, cols <= 65536 (else FP8Q_ESHAPE); norm_eps > 0; every
+ * pointer and row 16-B aligned (scales, rstd 4-B).  A row that holds a NaN
+ * gives NaN scales and codes 0x7F; the fp32 sum of squares overflows to Inf
+ * where |v| passes about 1e19, and such a row gives zeros (NaN at an Inf). */
+int fp8q_rmsnorm_1x128(const void* x, fp8q_dtype dt, int64_t ldx, const void* res, int64_t ldr, const void* w,
+                       fp8q_dtype wdt, int64_t rows, int64_t cols, float norm_eps, void* z, int64_t ldz, void* y,
+                       int64_t ldy, fp8q_format f, float eps, uint8_t* q, int64_t ldq, float* scales, int64_t ld_s,
+                       float* rstd, void* stream);
+
+/* Bytes of workspace fp8q_rmsnorm_bwd needs for the weight's gradient (at
+ * most 4096 bytes per column; 0 for sizes it refuses). */
+int64_t fp8q_rmsnorm_bwd_workspace(int64_t rows, int64_t cols);
+
+/* Gradients of fp8q_rmsnorm_1x128 (the quantization passed straight through):
+ *   xh = z * rstd, t = dy * w,
+ *   dx = rstd * (t - xh * mean_c(t * xh)) + dres,   dw[c] = sum_r dy * xh.
+ * dx is the gradient of x and of res alike.  dy, z, dres, dx: rows x cols of
+ * dtype dt; z is the forward's z (x itself without a residual), rstd its
+ * rstd.  dres (nullable): the gradient that reaches v past the norm, on the
+ * residual stream; dx may be dy or dres itself.  dw: cols fp32, overwritten; NULL
+ * skips it (ws then unused).  ws: ws_bytes >= fp8q_rmsnorm_bwd_workspace,
+ * 16-B aligned, overwritten; calls in flight must not share it.  Sums are
+ * fp32, in an order fixed by rows and cols alone.  Sizes and alignment as
+ * fp8q_rmsnorm_1x128. */
+int fp8q_rmsnorm_bwd(const void* dy, fp8q_dtype dt, int64_t lddy, const void* z, int64_t ldz, const void* w,
+                     fp8q_dtype wdt, const float* rstd, const void* dres, int64_t lddr, int64_t rows, int64_t cols,
+                     void* dx, int64_t lddx, float* dw, void* ws, int64_t ws_bytes, void* stream);
+
+/* Gated projection: both products, the activation and the product of the
+ * two in one kernel,
+ *   g = A Bg^T,  u = A Bu^T  (each as fp8q_gemm_blockscaled),
+ *   H[m,n] = act(g[m,n]) * u[m,n].
+ * A: M x K codes, 1x128 scales, as fp8q_gemm_blockscaled.  Bg, Bu: F x K
+ * codes of format fb, both with row stride ldb; sBg, sBu: their 128x128
+ * scales at [(n/128)*sB_sn + kb*sB_skb].  One [2F, K] matrix is passed as
+ * its two halves.  H: M x F fp32 or bf16 at H[m*ldh + n].  gu (nullable):
+ * g and u rounded to bf16 for the backward pass, M x 2F at gu[m*ldgu + n]
+ * and gu[m*ldgu + F + n], ldgu >= 2F; H is made from the unrounded ones.
+ * K % 128 == 0 (else FP8Q_ESHAPE); M, F >= 1; alignment as the GEMM. */
+int fp8q_glu_blockscaled(const uint8_t* A, fp8q_format fa, int64_t lda, const float* sA, int64_t sA_sm,
+                         int64_t sA_skb, const uint8_t* Bg, const uint8_t* Bu, fp8q_format fb, int64_t ldb,
+                         const float* sBg, const float* sBu, int64_t sB_sn, int64_t sB_skb, fp8q_act act, void* H,
+                         fp8q_dtype out_dt, int64_t ldh, uint16_t* gu, int64_t ldgu, int64_t M, int64_t F, int64_t K,
+                         void* stream);
+
+/* The same on the FP8 matrix cores (twice the rate), g and u within the
+ * bound of fp8q_gemm_blockscaled_fast; a few rows, which the weight's bytes
+ * bound, are computed exactly here too. */
+int fp8q_glu_blockscaled_fast(const uint8_t* A, fp8q_format fa, int64_t lda, const float* sA, int64_t sA_sm,
+                              int64_t sA_skb, const uint8_t* Bg, const uint8_t* Bu, fp8q_format fb, int64_t ldb,
+                              const float* sBg, const float* sBu, int64_t sB_sn, int64_t sB_skb, fp8q_act act,
+                              void* H, fp8q_dtype out_dt, int64_t ldh, uint16_t* gu, int64_t ldgu, int64_t M,
+                              int64_t F, int64_t K, void* stream);
+
+/* fp8q_glu_blockscaled with H as 1x128 codes of format fc, the input of the
+ * down projection: bit for bit what fp8q_quantize_1x128 makes of its fp32 H.
+ * Hq: M x F codes (ldhq >= F), Hs: [M, F/128] fp32 (ld_hs >= F/128); eps the
+ * amax clamp.  F % 128 == 0 as well (else FP8Q_ESHAPE). */
+int fp8q_glu_blockscaled_q(const uint8_t* A, fp8q_format fa, int64_t lda, const float* sA, int64_t sA_sm,
+                           int64_t sA_skb, const uint8_t* Bg, const uint8_t* Bu, fp8q_format fb, int64_t ldb,
+                           const float* sBg, const float* sBu, int64_t sB_sn, int64_t sB_skb, fp8q_act act,
+                           fp8q_format fc, float eps, uint8_t* Hq, int64_t ldhq, float* Hs, int64_t ld_hs,
+                           uint16_t* gu, int64_t ldgu, int64_t M, int64_t F, int64_t K, void* stream);
+
+/* Gradient of the gated projection at its pre-activations, quantized for the
+ * products that follow, with H recomputed:
+ *   dg = dH * u * act'(g),  du = dH * act(g),  H = act(g) * u   (fp32),
+ * D = [dg | du] (M x 2F).  From dH (M x F of dtype dt) and the forward's gu:
+ *   Dq, Ds: D as 1x128 codes along features, codes at Dq[m*lddq + n], scales
+ *     [M, 2F/128] (ld_ds): dX = D [Wg; Wu] is fp8q_gemm_blockscaled of Dq and
+ *     the weight stored [K, 2F];
+ *   Dt, Dst (nullable together): D^T as 1x128 codes along tokens, 2F x Mp at
+ *     Dt[n*lddt + m], scales [2F, Mp/128] (ld_dst): d[Wg; Wu] = D^T X;
+ *   Ht, Hst (nullable together): H^T likewise, F x Mp, of format fh, for the
+ *     down projection's weight gradient.
+ * Mp is M rounded up to a multiple of 128: the padding is written as zero
+ * codes, so any M can be reduced over.  fc: format of D (E4M3FN or E5M2);
+ * eps the amax clamp.  F % 128 == 0 (else FP8Q_ESHAPE); lddt, ldht >= Mp;
+ * dH, gu, Dq, Dt, Ht and their rows 16-B aligned. */
+int fp8q_glu_bwd_q(const void* dH, fp8q_dtype dt, int64_t lddh, const uint16_t* gu, int64_t ldgu, fp8q_act act,
+                   fp8q_format fc, float eps, uint8_t* Dq, int64_t lddq, float* Ds, int64_t ld_ds, uint8_t* Dt,
+                   int64_t lddt, float* Dst, int64_t ld_dst, fp8q_format fh, uint8_t* Ht, int64_t ldht, float* Hst,
+                   int64_t ld_hst, int64_t M, int64_t F, void* stream);
+
+/* fp8q_gemm_blockscaled for a few rows (1 <= M <= 64: single tokens, decoding
+ * batches), where the bytes of B are the work.  Arguments, layout and error
+ * bound as fp8q_gemm_blockscaled; more rows are FP8Q_ESHAPE. */
+int fp8q_gemm_blockscaled_few(const uint8_t* A, fp8q_format fa, int64_t lda, const float* sA, int64_t sA_sm,
+                              int64_t sA_skb, const uint8_t* B, fp8q_format fb, int64_t ldb, const float* sB,
+                              fp8q_gran gb, int64_t sB_sn, int64_t sB_skb, void* C, fp8q_dtype out_dt, int64_t ldc,
+                              int64_t M, int64_t N, int64_t K, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,132 @@
+"""Refusals of the feed-forward entry points, without a GPU: every bad
+argument is answered with its status before anything would be enqueued, and
+the binding's dtype checks raise."""
+import pytest
+import torch
+
+FAKE = 0x10000  # a 16-byte aligned address that is never dereferenced
+
+
+def _call(fq, name, ok, kw):
+    assert not set(kw) - set(ok), kw
+    rc = getattr(fq.lib(), name)(*{**ok, **kw}.values())
+    return rc, fq.lib().fp8q_last_error().decode()
+
+
+NORM = dict(x=FAKE, dt=1, ldx=256, res=FAKE, ldr=256, w=FAKE, wdt=0, rows=4, cols=256, neps=1e-6, z=FAKE, ldz=256, y=FAKE,
+            ldy=256, f=0, eps=1e-12, q=FAKE, ldq=256, s=FAKE, ld_s=2, rstd=FAKE, stream=None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(x=None), "EINVAL"), (dict(w=None), "EINVAL"), (dict(q=None), "EINVAL"), (dict(s=None), "EINVAL"),
+    (dict(q=None, s=None, y=None), "EINVAL"), (dict(dt=2), "EINVAL"), (dict(wdt=3), "EINVAL"), (dict(f=2), "EINVAL"),
+    (dict(rows=0), "EINVAL"), (dict(rows=-1), "EINVAL"), (dict(cols=0), "EINVAL"), (dict(neps=0.0), "EINVAL"),
+    (dict(neps=float("nan")), "EINVAL"), (dict(eps=0.0), "EINVAL"), (dict(eps=float("inf")), "EINVAL"),
+    (dict(cols=200), "ESHAPE"), (dict(cols=65536 + 128), "ESHAPE"), (dict(rows=1 << 31), "ESHAPE"),
+    (dict(ldx=128), "EINVAL"), (dict(ldr=128), "EINVAL"), (dict(ldz=128), "EINVAL"), (dict(ldy=128), "EINVAL"),
+    (dict(ldq=128), "EINVAL"), (dict(ld_s=1), "EINVAL"), (dict(x=FAKE + 8), "EALIGN"), (dict(w=FAKE + 4), "EALIGN"),
+    (dict(ldx=260), "EALIGN"), (dict(ldq=264), "EALIGN"), (dict(s=FAKE + 2), "EALIGN"), (dict(rstd=FAKE + 1), "EALIGN"),
+])
+def test_rmsnorm_refusals(fq, kw, status):
+    rc, msg = _call(fq, "fp8q_rmsnorm_1x128", NORM, kw)
+    assert rc == getattr(fq, status) and msg.startswith("rmsnorm_1x128"), (rc, msg)
+
+
+NORM_BWD = dict(dy=FAKE, dt=1, lddy=256, z=FAKE, ldz=256, w=FAKE, wdt=0, rstd=FAKE, dres=FAKE, lddr=256, rows=4, cols=256,
+                dx=FAKE, lddx=256, dw=FAKE, ws=FAKE, ws_bytes=1 << 20, stream=None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dy=None), "EINVAL"), (dict(z=None), "EINVAL"), (dict(rstd=None), "EINVAL"), (dict(dx=None), "EINVAL"),
+    (dict(ws=None), "EINVAL"), (dict(ws_bytes=64), "EINVAL"), (dict(dt=5), "EINVAL"), (dict(rows=0), "EINVAL"),
+    (dict(cols=130), "ESHAPE"), (dict(lddx=128), "EINVAL"), (dict(lddy=260), "EALIGN"), (dict(ws=FAKE + 4), "EALIGN"),
+    (dict(dw=FAKE + 2), "EALIGN"), (dict(dres=FAKE + 8), "EALIGN"),
+])
+def test_rmsnorm_bwd_refusals(fq, kw, status):
+    rc, msg = _call(fq, "fp8q_rmsnorm_bwd", NORM_BWD, kw)
+    assert rc == getattr(fq, status) and msg.startswith("rmsnorm_bwd"), (rc, msg)
+
+
+def test_rmsnorm_bwd_workspace(fq):
+    for rows in (1, 3, 100, 5000, 1 << 20):
+        for cols in (128, 2048, 4096, 16384, 65536):
+            b = fq.fp8q_rmsnorm_bwd_workspace(rows, cols)
+            assert 4 * cols <= b <= 4096 * cols and b % (4 * cols) == 0
+    for bad in ((0, 128), (1, 0), (1, 130), (1, 65664), (-1, 128)):
+        assert fq.fp8q_rmsnorm_bwd_workspace(*bad) == 0
+
+
+GLU = dict(A=FAKE, fa=0, lda=256, sA=FAKE, sm=2, skb=1, Bg=FAKE, Bu=FAKE, fb=0, ldb=256, sBg=FAKE, sBu=FAKE, sn=2, sk=1,
+           act=0, H=FAKE, odt=1, ldh=128, gu=FAKE, ldgu=256, M=40, F=128, K=256, stream=None)
+PROJ_BAD = [
+    (dict(A=None), "EINVAL"), (dict(sA=None), "EINVAL"), (dict(fa=2), "EINVAL"), (dict(fb=-1), "EINVAL"),
+    (dict(M=0), "EINVAL"), (dict(K=0), "EINVAL"), (dict(K=192), "ESHAPE"), (dict(lda=128), "EINVAL"),
+    (dict(ldb=128), "EINVAL"), (dict(sm=-1), "EINVAL"), (dict(sk=-1), "EINVAL"), (dict(A=FAKE + 8), "EALIGN"),
+    (dict(ldb=264), "EALIGN"), (dict(sA=FAKE + 2), "EALIGN"), (dict(ldb=1 << 32), "ESHAPE"),
+]
+GLU_BAD = PROJ_BAD + [(dict(Bg=None), "EINVAL"), (dict(Bu=None), "EINVAL"), (dict(sBu=None), "EINVAL"), (dict(F=0), "EINVAL"),
+                      (dict(act=2), "EINVAL"), (dict(act=-1), "EINVAL"), (dict(ldgu=255), "EINVAL"),
+                      (dict(gu=FAKE + 1), "EALIGN"), (dict(Bu=FAKE + 4), "EALIGN")]
+
+
+@pytest.mark.parametrize("name", ["fp8q_glu_blockscaled", "fp8q_glu_blockscaled_fast"])
+@pytest.mark.parametrize("kw,status", GLU_BAD + [(dict(H=None), "EINVAL"), (dict(odt=2), "EINVAL"), (dict(ldh=127), "EINVAL"),
+                                                 (dict(H=FAKE + 1), "EALIGN")])
+def test_glu_refusals(fq, name, kw, status):
+    rc, msg = _call(fq, name, GLU, kw)
+    assert rc == getattr(fq, status) and msg.startswith(name[5:]), (rc, msg)
+
+
+GLU_Q = dict(A=FAKE, fa=0, lda=256, sA=FAKE, sm=2, skb=1, Bg=FAKE, Bu=FAKE, fb=0, ldb=256, sBg=FAKE, sBu=FAKE, sn=2, sk=1,
+             act=1, fc=0, eps=1e-12, Hq=FAKE, ldhq=128, Hs=FAKE, ld_hs=1, gu=None, ldgu=0, M=40, F=128, K=256, stream=None)
+
+
+@pytest.mark.parametrize("kw,status", [(k if "ldgu" not in k else dict(gu=FAKE, **k), s) for k, s in GLU_BAD] + [
+    (dict(Hq=None), "EINVAL"), (dict(Hs=None), "EINVAL"), (dict(fc=2), "EINVAL"), (dict(eps=-1.0), "EINVAL"),
+    (dict(F=100), "ESHAPE"), (dict(ldhq=100), "EINVAL"), (dict(ld_hs=0), "EINVAL"), (dict(Hs=FAKE + 2), "EALIGN")])
+def test_glu_q_refusals(fq, kw, status):
+    rc, msg = _call(fq, "fp8q_glu_blockscaled_q", GLU_Q, {**dict(gu=None), **kw} if "gu" not in kw else {"ldgu": 256, **kw})
+    assert rc == getattr(fq, status) and msg.startswith("glu_blockscaled_q"), (rc, msg)
+
+
+GLU_BWD = dict(dH=FAKE, dt=1, lddh=128, gu=FAKE, ldgu=256, act=0, fc=1, eps=1e-12, Dq=FAKE, lddq=256, Ds=FAKE, ld_ds=2,
+               Dt=FAKE, lddt=256, Dst=FAKE, ld_dst=2, fh=0, Ht=FAKE, ldht=256, Hst=FAKE, ld_hst=2, M=200, F=128, stream=None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dH=None), "EINVAL"), (dict(gu=None), "EINVAL"), (dict(Dq=None), "EINVAL"), (dict(Ds=None), "EINVAL"),
+    (dict(Dst=None), "EINVAL"), (dict(Dt=None), "EINVAL"), (dict(Hst=None), "EINVAL"), (dict(dt=2), "EINVAL"),
+    (dict(fc=2), "EINVAL"), (dict(fh=2), "EINVAL"), (dict(act=7), "EINVAL"), (dict(eps=0.0), "EINVAL"),
+    (dict(M=0), "EINVAL"), (dict(F=0), "EINVAL"), (dict(F=96), "ESHAPE"), (dict(lddh=64), "EINVAL"),
+    (dict(ldgu=248), "EINVAL"), (dict(lddq=128), "EINVAL"), (dict(ld_ds=1), "EINVAL"), (dict(lddt=208), "EINVAL"),
+    (dict(ld_dst=1), "EINVAL"), (dict(ldht=208), "EINVAL"), (dict(ld_hst=1), "EINVAL"), (dict(dH=FAKE + 8), "EALIGN"),
+    (dict(lddh=132), "EALIGN"), (dict(ldgu=260), "EALIGN"), (dict(lddt=264), "EALIGN"), (dict(Ht=FAKE + 4), "EALIGN"),
+    (dict(Dst=FAKE + 2), "EALIGN"),
+])
+def test_glu_bwd_refusals(fq, kw, status):
+    rc, msg = _call(fq, "fp8q_glu_bwd_q", GLU_BWD, kw)
+    assert rc == getattr(fq, status) and msg.startswith("glu_bwd_q"), (rc, msg)
+
+
+FEW = dict(A=FAKE, fa=0, lda=256, sA=FAKE, sm=2, skb=1, B=FAKE, fb=0, ldb=256, sB=FAKE, gb=2, sn=2, sk=1, C=FAKE, odt=0,
+           ldc=128, M=4, N=128, K=256, stream=None)
+
+
+@pytest.mark.parametrize("kw,status", PROJ_BAD + [
+    (dict(B=None), "EINVAL"), (dict(C=None), "EINVAL"), (dict(gb=0), "EINVAL"), (dict(odt=2), "EINVAL"),
+    (dict(N=0), "EINVAL"), (dict(M=65), "ESHAPE"), (dict(ldc=127), "EINVAL"), (dict(C=FAKE + 2), "EALIGN")])
+def test_few_refusals(fq, kw, status):
+    rc, msg = _call(fq, "fp8q_gemm_blockscaled_few", FEW, kw)
+    assert rc == getattr(fq, status) and msg.startswith("gemm_blockscaled_few"), (rc, msg)
+
+
+def test_mixed_dtypes_are_refused_by_the_binding(fq):
+    x, r = torch.zeros(2, 128, dtype=torch.bfloat16), torch.zeros(2, 128)
+    w = torch.ones(128)
+    with pytest.raises(TypeError):
+        fq.fp8q_rmsnorm_1x128(x, 128, r, 128, w, 2, 128, 1e-6, None, 0, None, 0, 0, 1e-12, 1, 128, 1, 1, None, stream=0)
+    with pytest.raises(TypeError):
+        fq.fp8q_rmsnorm_bwd(x, 128, r, 128, w, w, None, 0, 2, 128, x, 128, stream=0)
+    with pytest.raises(TypeError):
+        fq.fp8q_glu_bwd_q(x.half(), 128, 1, 256, 0, 0, 1e-12, 1, 256, 1, 2, None, 0, None, 0, 0, None, 0, None, 0, 2, 128,
+                          stream=0)

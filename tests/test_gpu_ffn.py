@@ -1,0 +1,560 @@
+"""GPU checks of the feed-forward operators against plain implementations in
+64 bits: the norm with residual and 1x128 output and its gradients, the gated
+projection (exact, FP8-MFMA, quantized; single tokens to many tiles), its
+gradient, and the product of a few rows.
+
+Tolerances, with u = 2^-24 (half an fp32 step): a chain of n fp32 additions is
+off by at most n*u of the sum of magnitudes, a rounding to bf16 by 2^-8 of the
+value, to E4M3 by 2^-4 and to E5M2 by 2^-3 (or half the format's smallest
+step times the scale).
+"""
+import numpy as np
+import pytest
+import torch
+
+from block_scaled_precision_amax_amd import workloads as W
+
+pytestmark = pytest.mark.gpu
+
+E4, E5 = 0, 1
+MAXF = {E4: 448.0, E5: 57344.0}
+HALF = {E4: 2.0 ** -4, E5: 2.0 ** -3}        # half a step, relative
+TINY = {E4: 2.0 ** -10, E5: 2.0 ** -17}      # half the smallest step
+EPS, NEPS = 1e-12, 1e-6
+U = 2.0 ** -24
+BF = 2.0 ** -8
+F8 = {E4: torch.float8_e4m3fn, E5: torch.float8_e5m2}
+
+
+def dec(q, s, fmt, by_row=True):
+    """Codes [r, c] and 1x128 scales [r, c/128] as float64."""
+    v = q.cpu().view(F8[fmt]).double()
+    return v * s.cpu().double().repeat_interleave(128, dim=1)
+
+
+def dec_w(q, s, fmt=E4):
+    """Codes [n, k] and 128x128 scales as float64."""
+    v = q.cpu().view(F8[fmt]).double()
+    return v * s.cpu().double().repeat_interleave(128, 0)[:q.shape[0]].repeat_interleave(128, 1)
+
+
+def strided(t, extra, fill=None):
+    """The same values in rows `extra` elements further apart, and the whole buffer."""
+    b = torch.full((t.shape[0], t.shape[1] + extra), -3.0 if fill is None else fill, dtype=t.dtype, device=t.device)
+    b[:, :t.shape[1]] = t
+    return b
+
+
+# ------------------------------------------------------------------ norm
+def norm_ref(x, r, w):
+    v = x.double().cpu() + (r.double().cpu() if r is not None else 0)
+    rstd = 1 / torch.sqrt((v * v).mean(1) + NEPS)
+    return v, rstd, v * rstd[:, None] * w.double().cpu()
+
+
+def run_norm(fq, x, r, w, fmt, pad=0, want_y=True, want_z=True, stream=None):
+    rows, cols = x.shape
+    ld = cols + pad
+    dev = x.device
+    xb = strided(x, pad) if pad else x
+    rb = strided(r, pad) if pad and r is not None else r
+    z = torch.full((rows, ld), 7.0, dtype=x.dtype, device=dev) if want_z else None
+    y = torch.full((rows, ld), 7.0, dtype=x.dtype, device=dev) if want_y else None
+    q = torch.full((rows, ld), 0xAA, dtype=torch.uint8, device=dev)
+    s = torch.full((rows, cols // 128 + pad), -7.0, device=dev)
+    rstd = torch.empty(rows, device=dev)
+    fq.fp8q_rmsnorm_1x128(xb, ld, rb, ld, w, rows, cols, NEPS, z, ld, y, ld, fmt, EPS, q, ld, s, s.shape[1], rstd,
+                          stream=stream)
+    torch.cuda.synchronize()
+    if pad:
+        assert (q[:, cols:] == 0xAA).all() and (s[:, cols // 128:] == -7).all()
+        assert all((t[:, cols:] == 7).all() for t in (z, y) if t is not None)
+    cut = lambda t: None if t is None else t[:, :cols]  # noqa: E731
+    return cut(z), cut(y), cut(q), s[:, :cols // 128], rstd
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 128), (1, 7168), (5, 256), (3, 640), (7, 1152), (33, 2048), (2, 2176), (6, 4096),
+                                       (9, 7168), (3, 10368), (2, 16384), (2, 18432), (1, 65536)])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_norm(fq, orc, gpu, rows, cols, dt):
+    fmt = E4 if rows % 2 else E5
+    x = W.activation(rows, cols, seed=rows + cols, factor=30.0, device=gpu, dtype=dt)
+    r = W.normal((rows, cols), seed=5, device=gpu, std=2.0, dtype=dt) if cols != 640 else None
+    w = 1 + W.normal((cols,), seed=6, device=gpu, std=0.1, dtype=torch.float32)
+    if cols == 1152:
+        w = w.bfloat16()
+    z, y, q, s, rstd = run_norm(fq, x, r, w, fmt, pad=64 if rows in (3, 33) else 0)
+    v, rs, yr = norm_ref(x, r, w)
+    # the sum of squares: at most 64 fused additions a lane, 6 across lanes and 16 across wavefronts, halved by the root;
+    # then the root, the quotient and two products
+    n = 0.5 * 86 + 6
+    assert ((rstd.cpu().double() - rs).abs() <= n * U * rs).all()
+    tol = (n + 4) * U * yr.abs() + (BF * yr.abs() if dt == torch.bfloat16 else 0)
+    assert ((y.cpu().double() - yr).abs() <= tol).all()
+    # the stored sum is the sum rounded once
+    zf = x.float() + (r.float() if r is not None else 0)
+    assert torch.equal(z, zf.to(dt))
+    # the codes are those the quantizer makes of the fp32 norm
+    y32 = y if dt == torch.float32 else run_norm(fq, x.float(), None if r is None else r.float(), w, fmt)[1]
+    wq, ws = orc.quantize_blocks(np.ascontiguousarray(y32.cpu().numpy()), 1, 128, fmt)
+    assert np.array_equal(q.cpu().numpy(), wq) and np.array_equal(s.cpu().numpy(), ws)
+
+
+def test_norm_optional_outputs_and_in_place(fq, gpu):
+    rows, cols = 10, 1024
+    x = W.activation(rows, cols, seed=1, factor=5.0, device=gpu, dtype=torch.bfloat16)
+    r = W.normal((rows, cols), seed=2, device=gpu, dtype=torch.bfloat16)
+    w = torch.ones(cols, device=gpu)
+    z, y, q, s, rstd = run_norm(fq, x, r, w, E4)
+    _, y2, q2, s2, _ = run_norm(fq, x, r, w, E4, want_y=False, want_z=False)
+    assert torch.equal(q, q2) and torch.equal(s, s2) and y2 is None
+    # no codes: y alone
+    y3 = torch.empty_like(x)
+    fq.fp8q_rmsnorm_1x128(x, cols, r, cols, w, rows, cols, NEPS, None, 0, y3, cols, E4, EPS, None, 0, None, 0)
+    assert torch.equal(y, y3)
+    # z over the residual, and over x
+    for which in (0, 1):
+        a, b = x.clone(), r.clone()
+        q4, s4 = torch.empty_like(q), torch.empty_like(s)
+        fq.fp8q_rmsnorm_1x128(a, cols, b, cols, w, rows, cols, NEPS, (a, b)[which], cols, None, 0, E4, EPS, q4, cols, s4,
+                              cols // 128)
+        assert torch.equal((a, b)[which], z) and torch.equal(q4, q) and torch.equal(s4, s)
+        assert torch.equal((b, a)[which], (r, x)[which])
+
+
+def test_norm_special_rows(fq, gpu):
+    cols = 512
+    x = torch.randn(5, cols, device=gpu)
+    x[0] = 0.0
+    x[1, 3] = float("nan")
+    x[2, 7] = float("inf")
+    x[3] = -0.0
+    w = torch.ones(cols, device=gpu)
+    z, y, q, s, rstd = run_norm(fq, x, None, w, E4)
+    assert (y[0] == 0).all() and (q[0] == 0).all() and (q[3] == 0x80).all()
+    assert torch.allclose(rstd[0], torch.tensor(NEPS, device=gpu).rsqrt())
+    assert torch.equal(s[0], torch.full((4,), float(np.float32(EPS) / np.float32(448)), device=gpu))
+    assert y[1].isnan().all() and (q[1] == 0x7F).all() and s[1].isnan().all()
+    assert rstd[2] == 0 and y[2, 7].isnan() and (y[2, :7] == 0).all() and (q[2, :128] == 0x7F).all()
+    assert (q[2, 128:] & 0x7F == 0).all()
+    yr = norm_ref(x[4:], None, w)[2]
+    assert ((y[4:].cpu().double() - yr).abs() <= 60 * U * yr.abs()).all()
+
+
+def bwd_ref(dy, z, w, rstd, dres):
+    dy, z, w, rs = dy.double().cpu(), z.double().cpu(), w.double().cpu(), rstd.double().cpu()[:, None]
+    xh, t = z * rs, dy * w
+    dot = (t * xh).mean(1, keepdim=True)
+    dx = rs * (t - xh * dot)
+    mag = rs * (t.abs() + xh.abs() * (t * xh).abs().mean(1, keepdim=True))
+    if dres is not None:
+        dx = dx + dres.double().cpu()
+    return dx, (dy * xh).sum(0), mag, (dy * xh).abs().sum(0)
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 128), (3, 384), (2500, 128), (41, 1024), (2300, 1920), (700, 2304), (9, 7168),
+                                       (1300, 4096), (5, 16384), (3, 18432), (1, 65536)])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_norm_bwd(fq, gpu, rows, cols, dt):
+    pad = 64 if rows % 2 else 0
+    z = W.activation(rows, cols, seed=rows, factor=20.0, device=gpu, dtype=dt)
+    dy = W.gradient(rows, cols, seed=3, device=gpu, dtype=dt)
+    dres = W.normal((rows, cols), seed=4, device=gpu, std=1e-3, dtype=dt) if cols != 1024 else None
+    w = 1 + W.normal((cols,), seed=6, device=gpu, std=0.1, dtype=torch.float32)
+    if cols == 2304:
+        w = w.bfloat16()
+    rstd = (z.double().square().mean(1) + NEPS).rsqrt().float()
+    ws_bytes = fq.fp8q_rmsnorm_bwd_workspace(rows, cols)
+    guard = torch.full((ws_bytes // 4 + 64,), 5.0, device=gpu)
+    dx = torch.full((rows, cols + pad), 7.0, dtype=dt, device=gpu)
+    dw = torch.empty(cols, device=gpu)
+    sp = lambda t: None if t is None else strided(t, pad) if pad else t  # noqa: E731
+    ld = cols + pad
+    zb, dyb, drb = sp(z), sp(dy), sp(dres)
+
+    def call(dw):
+        fq.fp8q_rmsnorm_bwd(dyb, ld, zb, ld, w, rstd, drb, ld, rows, cols, dx, ld, dw, guard, ws_bytes)
+        torch.cuda.synchronize()
+        return dx.clone()
+
+    first = call(dw)
+    assert (guard[ws_bytes // 4:] == 5).all(), "wrote past the workspace"
+    if pad:
+        assert (first[:, cols:] == 7).all()
+    want, want_w, mag, mag_w = bwd_ref(dy, z, w, rstd, dres)
+    # 64 fused additions a lane, 22 across lanes and wavefronts, then a handful of products
+    tol = 96 * U * mag + 4 * U * want.abs() + (BF * want.abs() if dt == torch.bfloat16 else 0)
+    assert ((first[:, :cols].cpu().double() - want).abs() <= tol).all()
+    # rows of one workgroup, its four row groups, the partial rows an eighth at a time
+    parts = ws_bytes // (4 * cols)
+    n = -(-rows // parts) + 4 + -(-parts // 8) + 8 + 4
+    assert ((dw.cpu().double() - want_w).abs() <= n * U * mag_w).all()
+    # the same bits again, and without the weight's gradient
+    dw2 = torch.empty_like(dw)
+    assert torch.equal(call(dw2), first) and torch.equal(dw, dw2)
+    assert torch.equal(call(None), first)
+
+
+def test_norm_bwd_in_place_and_differences(fq, gpu):
+    rows, cols = 3, 256
+    x = torch.randn(rows, cols, dtype=torch.float64)
+    w = 1 + 0.1 * torch.randn(cols, dtype=torch.float64)
+    dy = torch.randn(rows, cols, dtype=torch.float64)
+    x, w, dy = x.float().double(), w.float().double(), dy.float().double()
+
+    def loss(x, w):
+        return (x * (1 / torch.sqrt(x.square().mean(1, keepdim=True) + NEPS)) * w * dy).sum(1)
+
+    h = 1e-5
+    num = torch.empty_like(x)
+    for c in range(cols):
+        e = torch.zeros(cols, dtype=torch.float64)
+        e[c] = h
+        num[:, c] = (loss(x + e, w) - loss(x - e, w)) / (2 * h)
+    numw = torch.stack([(loss(x, w + h * torch.eye(cols, dtype=torch.float64)[c]).sum()
+                         - loss(x, w - h * torch.eye(cols, dtype=torch.float64)[c]).sum()) / (2 * h) for c in range(cols)])
+    z, g, wd = x.float().to(gpu), dy.float().to(gpu), w.float().to(gpu)
+    rstd = (x.square().mean(1) + NEPS).rsqrt().float().to(gpu)
+    ws = torch.empty(fq.fp8q_rmsnorm_bwd_workspace(rows, cols) // 4, device=gpu)
+    dw = torch.empty(cols, device=gpu)
+    dx = torch.empty_like(z)
+    fq.fp8q_rmsnorm_bwd(g, cols, z, cols, wd, rstd, None, 0, rows, cols, dx, cols, dw, ws, ws.numel() * 4)
+    want, want_w, mag, mag_w = bwd_ref(g, z, wd, rstd, None)
+    # central differences in 64 bits: h^2 times a third derivative of order 1, and cancellation of 1e-16 * 300 / h
+    assert ((dx.cpu().double() - num).abs() <= 96 * U * mag + 1e-8).all()
+    assert ((dw.cpu().double() - numw).abs() <= 96 * U * mag_w + 1e-8).all()
+    # dx over dy, and over the residual's gradient
+    for over in (0, 1):
+        a, b = g.clone(), torch.zeros_like(g)
+        out = (a, b)[over]
+        fq.fp8q_rmsnorm_bwd(a, cols, z, cols, wd, rstd, b, cols, rows, cols, out, cols)
+        assert torch.equal(out, dx)
+
+
+# ------------------------------------------------------------------ gated projection, few rows
+def operands(gpu, M, F, K, fa=E4, fb=E4, pad=0, seed=0):
+    """Codes over the whole finite code space for A (small exponents), Gaussian weights; strided."""
+    g = W._gen(seed, gpu)
+    Kb = K // 128
+    A = (torch.randn(M, K, generator=g, device=gpu) * 100).clamp(-MAXF[fa], MAXF[fa]).to(F8[fa]).view(torch.uint8)
+    sA = torch.exp(torch.randn(M, Kb, generator=g, device=gpu)) * 0.01
+    B = [(torch.randn(F, K, generator=g, device=gpu) * 60).clamp(-MAXF[fb], MAXF[fb]).to(F8[fb]).view(torch.uint8) for _ in range(2)]
+    sB = [torch.exp(0.5 * torch.randn(-(-F // 128), Kb, generator=g, device=gpu)) * 2e-3 / K ** 0.5 * 8 for _ in range(2)]
+    if pad:
+        A, B = strided(A, pad, 0x7F), [strided(b, pad, 0x7F) for b in B]
+    return A, sA, B, sB
+
+
+def glu_call(fq, fn, A, fa, sA, B, fb, sB, act, out, gu, M, F, K, q=None, stream=None):
+    Kb = K // 128
+    a = (A, fa, A.stride(0), sA, Kb, 1, B[0], B[1], fb, B[0].stride(0), sB[0], sB[1], Kb, 1, act)
+    g = (gu, gu.stride(0) if gu is not None else 0)
+    if q is not None:
+        fc, hs = q
+        fq.fp8q_glu_blockscaled_q(*a, fc, EPS, out, out.stride(0), hs, hs.stride(0), *g, M, F, K, stream=stream)
+    else:
+        getattr(fq, fn)(*a, out, out.stride(0), *g, M, F, K, stream=stream)
+
+
+def act64(act, g):
+    return g * torch.sigmoid(g) if act == 0 else 0.5 * g * (1 + torch.tanh((2 / np.pi) ** 0.5 * (g + 0.044715 * g ** 3)))
+
+
+GLU_SHAPES = [(1, 128, 128), (1, 256, 1024), (2, 7, 256), (15, 130, 384), (16, 384, 640), (17, 1000, 256), (33, 256, 1152),
+              (64, 129, 512), (65, 128, 128), (70, 260, 384), (128, 256, 256), (129, 384, 640), (257, 200, 512),
+              (300, 1152, 1280)]
+
+
+@pytest.mark.parametrize("M,F,K", GLU_SHAPES)
+@pytest.mark.parametrize("fast", [False, True])
+def test_glu(fq, orc, gpu, M, F, K, fast):
+    i = GLU_SHAPES.index((M, F, K))
+    fa, fb, act, pad = (i // 2) % 2, (i // 4) % 2, i % 2, (16 if i % 3 == 0 else 0)
+    A, sA, B, sB = operands(gpu, M, F, K, fa, fb, pad, seed=M + F)
+    fn = "fp8q_glu_blockscaled_fast" if fast else "fp8q_glu_blockscaled"
+    h = torch.full((M, F + 3), 7.0, device=gpu)
+    gu = torch.full((M, 2 * F + 5), 7.0, dtype=torch.bfloat16, device=gpu)
+    glu_call(fq, fn, A, fa, sA, B, fb, sB, act, h, gu, M, F, K)
+    hb = torch.full((M, (F + 7) // 8 * 8), 7.0, dtype=torch.bfloat16, device=gpu)
+    glu_call(fq, fn, A, fa, sA, B, fb, sB, act, hb, None, M, F, K)
+    torch.cuda.synchronize()
+    assert (h[:, F:] == 7).all() and (gu[:, 2 * F:] == 7).all() and (hb[:, F:] == 7).all()
+    assert torch.equal(hb[:, :F], h[:, :F].bfloat16()), "bf16 output is the fp32 one rounded once"
+    An, Bn = A[:, :K].cpu().numpy(), [b[:, :K].cpu().numpy() for b in B]
+    (g, Dg), (u, Du) = [orc.gemm_blockscaled(An, fa, sA.cpu().numpy(), Bn[j], fb, sB[j].cpu().numpy(), orc.GRAN_128x128)
+                        for j in (0, 1)]
+    g, u, Dg, Du = map(torch.from_numpy, (g, u, Dg, Du))
+    rel = 2.0 ** -10 if fast else 1e-5  # the GEMM's own bounds
+    a64 = act64(act, g)
+    # |act'| <= 1.13 for both; the exponential's argument is off by a few u of at most 176
+    tol = 1.13 * rel * Dg * (u.abs() + rel * Du) + a64.abs() * rel * Du + (a64 * u).abs() * 600 * U + 1e-30
+    assert ((h[:, :F].cpu().double() - a64 * u).abs() <= tol).all()
+    for k, (x, D) in enumerate(((g, Dg), (u, Du))):
+        got = gu[:, k * F:(k + 1) * F].cpu().double()
+        assert ((got - x).abs() <= BF * x.abs() + 1.01 * rel * D).all()
+
+
+@pytest.mark.parametrize("M,F,K", [(1, 128, 256), (3, 384, 128), (16, 256, 1024), (40, 128, 640), (64, 256, 256),
+                                   (66, 128, 384), (130, 384, 256), (300, 640, 512)])
+@pytest.mark.parametrize("fc", [E4, E5])
+def test_glu_q_equals_quantized_output(fq, gpu, M, F, K, fc):
+    A, sA, B, sB = operands(gpu, M, F, K, seed=M)
+    act = M % 2
+    h = torch.empty(M, F, device=gpu)
+    gu = torch.empty(M, 2 * F, dtype=torch.bfloat16, device=gpu)
+    glu_call(fq, "fp8q_glu_blockscaled", A, E4, sA, B, E4, sB, act, h, gu, M, F, K)
+    want, ws = torch.empty(M, F, dtype=torch.uint8, device=gpu), torch.empty(M, F // 128, device=gpu)
+    fq.fp8q_quantize_1x128(h, M, F, F, fc, EPS, want, F, ws, F // 128)
+    off = 4 if M % 3 == 0 else 0  # codes need no alignment
+    q = torch.full((M, F + 16 + off), 0xAA, dtype=torch.uint8, device=gpu)
+    s = torch.full((M, F // 128 + 1), -7.0, device=gpu)
+    gu2 = torch.empty_like(gu)
+    glu_call(fq, None, A, E4, sA, B, E4, sB, act, q[:, off:], gu2, M, F, K, q=(fc, s))
+    torch.cuda.synchronize()
+    assert torch.equal(q[:, off:off + F], want) and torch.equal(s[:, :-1], ws) and torch.equal(gu, gu2)
+    assert (q[:, :off] == 0xAA).all() and (q[:, off + F:] == 0xAA).all() and (s[:, -1] == -7).all()
+
+
+def test_glu_halves_of_one_matrix_and_scale_strides(fq, gpu):
+    """One [2F, K] weight passed as its halves; transposed scale layouts."""
+    for M in (5, 200):
+        F, K = 256, 384
+        A, sA, B, sB = operands(gpu, M, F, K, seed=9)
+        want = torch.empty(M, F, device=gpu)
+        glu_call(fq, "fp8q_glu_blockscaled", A, E4, sA, B, E4, sB, 0, want, None, M, F, K)
+        W2, s2 = torch.cat(B).contiguous(), torch.cat(sB).t().contiguous()  # scales [K/128, 2F/128]
+        sAt = sA.t().contiguous()
+        h = torch.empty(M, F, device=gpu)
+        fq.fp8q_glu_blockscaled(A, E4, K, sAt, 1, M, W2, W2[F:], E4, K, s2, s2[:, F // 128:].data_ptr(), 1, 2 * F // 128, 0, h,
+                                F, None, 0, M, F, K)
+        assert torch.equal(h, want)
+
+
+def test_glu_many_tiles(fq, orc, gpu):
+    """More tiles than compute units, a ragged edge both ways, checked on sampled rows."""
+    M, F, K = 2305, 4000, 256
+    A, sA, B, sB = operands(gpu, M, F, K, seed=4)
+    rows = np.array([0, 1, 127, 128, 255, 256, 1000, 2047, 2048, 2303, 2304])
+    for fn, rel in (("fp8q_glu_blockscaled", 1e-5), ("fp8q_glu_blockscaled_fast", 2.0 ** -10)):
+        h = torch.full((M, F), 7.0, device=gpu)
+        glu_call(fq, fn, A, E4, sA, B, E4, sB, 0, h, None, M, F, K)
+        (g, Dg), (u, Du) = [orc.gemm_blockscaled(A.cpu().numpy(), E4, sA.cpu().numpy(), B[j].cpu().numpy(), E4,
+                                                 sB[j].cpu().numpy(), orc.GRAN_128x128, rows=rows) for j in (0, 1)]
+        g, u, Dg, Du = map(torch.from_numpy, (g, u, Dg, Du))
+        tol = 1.13 * rel * Dg * (u.abs() + rel * Du) + act64(0, g).abs() * rel * Du + (act64(0, g) * u).abs() * 600 * U
+        assert ((h[rows].cpu().double() - act64(0, g) * u).abs() <= tol + 1e-30).all()
+        assert h.isfinite().all() and not (h == 7.0).any()
+
+
+def test_glu_rows_do_not_touch_each_other(fq, gpu):
+    """A NaN code spoils its own row alone, in the few-row and in the tiled kernel."""
+    for M in (20, 150):
+        F, K = 256, 256
+        A, sA, B, sB = operands(gpu, M, F, K, seed=1)
+        h0, h1 = torch.empty(M, F, device=gpu), torch.empty(M, F, device=gpu)
+        glu_call(fq, "fp8q_glu_blockscaled", A, E4, sA, B, E4, sB, 0, h0, None, M, F, K)
+        A[3, 200] = 0x7F
+        glu_call(fq, "fp8q_glu_blockscaled", A, E4, sA, B, E4, sB, 0, h1, None, M, F, K)
+        keep = torch.arange(M, device=gpu) != 3
+        assert h1[3].isnan().all() and torch.equal(h0[keep], h1[keep])
+        q, s = torch.empty(M, F, dtype=torch.uint8, device=gpu), torch.empty(M, F // 128, device=gpu)
+        glu_call(fq, None, A, E4, sA, B, E4, sB, 0, q, None, M, F, K, q=(E4, s))
+        assert (q[3] == 0x7F).all() and s[3].isnan().all() and s[keep].isfinite().all()
+
+
+@pytest.mark.parametrize("M", [1, 2, 15, 16, 17, 32, 33, 48, 49, 64])
+@pytest.mark.parametrize("N,K", [(128, 128), (1, 256), (100, 384), (1000, 2176)])
+def test_few(fq, orc, gpu, M, N, K):
+    fa, fb, pad, gb = M % 2, (M // 2) % 2, (32 if M % 3 == 0 else 0), (1 if M % 5 == 0 else 2)
+    A, sA, B, sB = operands(gpu, M, N, K, fa, fb, pad, seed=N)
+    sb = sB[0] if gb == 2 else sB[0].repeat_interleave(128, 0)[:N] * torch.linspace(0.5, 2.0, N, device=gpu)[:, None]
+    sb = sb.contiguous()
+    C = torch.full((M, N + 3), 7.0, device=gpu)
+    args = (A, fa, A.stride(0), sA, K // 128, 1, B[0], fb, B[0].stride(0), sb, gb, K // 128, 1)
+    fq.fp8q_gemm_blockscaled_few(*args, C, N + 3, M, N, K)
+    Cb = torch.full((M, N), 7.0, dtype=torch.bfloat16, device=gpu)
+    fq.fp8q_gemm_blockscaled_few(*args, Cb, N, M, N, K)
+    torch.cuda.synchronize()
+    ref, D = orc.gemm_blockscaled(A[:, :K].cpu().numpy(), fa, sA.cpu().numpy(), B[0][:, :K].cpu().numpy(), fb,
+                                  sb.cpu().numpy(), gb)
+    assert (np.abs(C[:, :N].cpu().numpy().astype(np.float64) - ref) <= 1e-5 * D).all()
+    assert (C[:, N:] == 7).all() and torch.equal(Cb, C[:, :N].bfloat16())
+
+
+# ------------------------------------------------------------------ gradient of the gated projection
+def bwd_call(fq, dh, gu, act, fc, fh, M, F, want_t=True, want_h=True, pad=0, stream=None):
+    dev, Mp = dh.device, -(-M // 128) * 128
+    u8 = lambda r, c: torch.full((r, c + pad), 0xAA, dtype=torch.uint8, device=dev)  # noqa: E731
+    f4 = lambda r, c: torch.full((r, c + (1 if pad else 0)), -7.0, device=dev)  # noqa: E731
+    D, Ds = u8(M, 2 * F), f4(M, 2 * F // 128)
+    Dt, Dts = (u8(2 * F, Mp), f4(2 * F, Mp // 128)) if want_t else (None, None)
+    Ht, Hts = (u8(F, Mp), f4(F, Mp // 128)) if want_h else (None, None)
+    st = lambda t: 0 if t is None else t.stride(0)  # noqa: E731
+    fq.fp8q_glu_bwd_q(dh, dh.stride(0), gu, gu.stride(0), act, fc, EPS, D, st(D), Ds, st(Ds), Dt, st(Dt), Dts, st(Dts), fh, Ht,
+                      st(Ht), Hts, st(Hts), M, F, stream=stream)
+    torch.cuda.synchronize()
+    if pad:
+        for t, n in ((D, 2 * F), (Dt, Mp), (Ht, Mp)):
+            assert t is None or (t[:, n:] == 0xAA).all()
+        for t, n in ((Ds, 2 * F // 128), (Dts, Mp // 128), (Hts, Mp // 128)):
+            assert t is None or (t[:, n:] == -7).all()
+    cut = lambda t, n: None if t is None else t[:, :n].contiguous()  # noqa: E731
+    return (cut(D, 2 * F), cut(Ds, 2 * F // 128), cut(Dt, Mp), cut(Dts, Mp // 128), cut(Ht, Mp), cut(Hts, Mp // 128))
+
+
+BWD_SHAPES = [(1, 128), (5, 256), (127, 128), (128, 384), (129, 256), (300, 640)]
+
+
+@pytest.mark.parametrize("M,F", BWD_SHAPES)
+@pytest.mark.parametrize("fc", [E4, E5])
+def test_glu_bwd_exact_values(fq, orc, gpu, M, F, fc):
+    """g = 40: silu'(g) = 1 and silu(g) = 40 to the last bit, so dg = dh*u, du = 40*dh and h = 40*u are exact in fp32
+    and every code and scale is the quantizer's of those values, in both layouts."""
+    g = torch.Generator().manual_seed(M * F + fc)
+    dh = torch.randn(M, F, generator=g).bfloat16()
+    u = (torch.randn(M, F, generator=g) * 3).bfloat16()
+    u[0, :40] = 0.0
+    gu = torch.cat([torch.full((M, F), 40.0, dtype=torch.bfloat16), u], 1)
+    D, Ds, Dt, Dts, Ht, Hts = bwd_call(fq, dh.to(gpu), gu.to(gpu), 0, fc, 1 - fc, M, F, pad=16)
+    d = torch.cat([dh.float() * u.float(), dh.float() * 40], 1)
+    h = 40 * u.float()
+    Mp = Dt.shape[1]
+    padt = lambda t: np.ascontiguousarray(torch.nn.functional.pad(t.t(), (0, Mp - M)).numpy())  # noqa: E731
+    for q, s, v, fmt in ((D, Ds, d.numpy(), fc), (Dt, Dts, padt(d), fc), (Ht, Hts, padt(h), 1 - fc)):
+        wq, ws = orc.quantize_blocks(v, 1, 128, fmt)
+        assert np.array_equal(q.cpu().numpy(), wq) and np.array_equal(s.cpu().numpy(), ws)
+
+
+@pytest.mark.parametrize("act", [0, 1])
+@pytest.mark.parametrize("M,F,dt", [(3, 128, torch.float32), (200, 256, torch.bfloat16), (130, 384, torch.float32)])
+def test_glu_bwd_against_formula_and_differences(fq, gpu, act, M, F, dt):
+    fc, fh = M % 2, E4
+    g = W.normal((M, F), seed=1, std=2.0, dtype=torch.bfloat16)
+    u = W.normal((M, F), seed=2, std=1.5, dtype=torch.bfloat16)
+    dh = W.gradient(M, F, seed=3, dtype=dt)
+    g[0, :8] = torch.tensor([0.0, -0.0, 30.0, -30.0, 88.0, -88.0, 200.0, -200.0])
+    D, Ds, Dt, Dts, Ht, Hts = bwd_call(fq, dh.to(gpu), torch.cat([g, u], 1).to(gpu), act, fc, fh, M, F)
+    g, u, dh = g.double(), u.double(), dh.double()
+    step = 1e-4
+    num = (act64(act, g + step) - act64(act, g - step)) / (2 * step)  # off by step^2/6 * |act'''| < 1e-8, and 1e-16*200/step
+    if act == 0:
+        p = torch.sigmoid(g)
+        da = p * (1 + g * (1 - p))
+    else:
+        c, a = (2 / np.pi) ** 0.5, 0.044715
+        th = torch.tanh(c * (g + a * g ** 3))
+        da = 0.5 * (1 + th) + 0.5 * g * (1 - th * th) * c * (1 + 3 * a * g * g)
+    assert ((num - da).abs() <= 1e-8 + 1e-9).all()
+    h = act64(act, g) * u
+    for dg in (dh * u * da, dh * u * num):
+        d = torch.cat([dg, dh * act64(act, g)], 1)
+        mag = torch.cat([(dh * u).abs() * 1.13, dh.abs() * act64(act, g).abs()], 1)
+        for q, s, v, m, fmt in ((D, Ds, d, mag, fc), (Dt, Dts, d.t(), mag.t(), fc), (Ht, Hts, h.t(), h.abs().t(), fh)):
+            v, m = (torch.nn.functional.pad(t, (0, q.shape[1] - t.shape[1])) for t in (v, m))
+            err = 700 * U * m + 2e-8 * m  # the exponential's argument, and a few products; the differences' own error
+            am = v.abs().view(v.shape[0], -1, 128).amax(2)
+            em = err.view(v.shape[0], -1, 128).amax(2)
+            assert ((s.cpu().double() - am.clamp(min=EPS) / MAXF[fmt]).abs() <= em / MAXF[fmt] + 4 * U * am / MAXF[fmt]).all()
+            sf = s.cpu().double().repeat_interleave(128, 1)
+            got = dec(q, s, fmt)
+            assert ((got - v).abs() <= (HALF[fmt] + 2 ** -20) * v.abs() + TINY[fmt] * sf + 1.2 * err).all()
+
+
+def test_glu_bwd_optional_outputs_zero_and_special(fq, gpu):
+    M, F = 140, 256
+    dh = torch.randn(M, F, device=gpu, dtype=torch.bfloat16)
+    gu = torch.randn(M, 2 * F, device=gpu, dtype=torch.bfloat16)
+    dh[2] = 0.0
+    full = bwd_call(fq, dh, gu, 0, E5, E4, M, F)
+    for t, h in ((False, False), (True, False), (False, True)):
+        part = bwd_call(fq, dh, gu, 0, E5, E4, M, F, want_t=t, want_h=h)
+        for a, b in zip(full, part):
+            assert b is None or torch.equal(a, b)
+    assert (full[0][2] & 0x7F == 0).all() and (full[2][:, M:] == 0).all() and (full[4][:, M:] == 0).all()
+    # a NaN in dh spoils its row's two blocks and its column's block of D^T, not h
+    dh[5, 130] = float("nan")
+    bad = bwd_call(fq, dh, gu, 0, E5, E4, M, F)
+    assert bad[1][5, 1].isnan() and bad[1][5, 3].isnan() and bad[1].isnan().sum() == 2
+    assert bad[3][130, 0].isnan() and bad[3][F + 130, 0].isnan() and bad[3].isnan().sum() == 2
+    assert torch.equal(bad[4], full[4]) and (bad[0][5, 128:256] == 0x7F).all()
+
+
+def test_gradient_products_of_a_ragged_batch(fq, gpu):
+    """dX and dW through the library's products, from the quantized gradients, against 64 bits from the same codes and
+    against the unquantized gradients within the codes' rounding."""
+    M, F, K = 200, 256, 384
+    Mp = 256
+    g = torch.Generator().manual_seed(5)
+    X = torch.zeros(Mp, K)
+    X[:M] = torch.randn(M, K, generator=g)
+    Wgu = 0.05 * torch.randn(2 * F, K, generator=g)
+    dh = torch.randn(M, F, generator=g).bfloat16().to(gpu)
+    gu = torch.randn(M, 2 * F, generator=g).bfloat16().to(gpu)
+    Wt, sWt = torch.empty(K, 2 * F, dtype=torch.uint8, device=gpu), torch.empty(K // 128, 2 * F // 128, device=gpu)
+    fq.fp8q_quantize_128x128(Wgu.t().contiguous().to(gpu), K, 2 * F, 2 * F, E4, EPS, Wt, 2 * F, sWt, 2 * F // 128)
+    Xt, sXt = torch.empty(K, Mp, dtype=torch.uint8, device=gpu), torch.empty(K, Mp // 128, device=gpu)
+    fq.fp8q_quantize_1x128_t(X.to(gpu), Mp, K, K, E4, EPS, Xt, Mp, sXt, Mp // 128)
+    D, Ds, Dt, Dts, Ht, Hts = bwd_call(fq, dh, gu, 0, E5, E4, M, F)
+    dX, dW = torch.empty(M, K, device=gpu), torch.empty(2 * F, K, device=gpu)
+    fq.fp8q_gemm_blockscaled(D, E5, 2 * F, Ds, 2 * F // 128, 1, Wt, E4, 2 * F, sWt, 2, 2 * F // 128, 1, dX, K, M, K, 2 * F)
+    fq.fp8q_gemm_blockscaled(Dt, E5, Mp, Dts, Mp // 128, 1, Xt, E4, Mp, sXt, 1, Mp // 128, 1, dW, K, 2 * F, K, Mp)
+    d64, dt64, w64, x64 = dec(D, Ds, E5), dec(Dt, Dts, E5), dec_w(Wt, sWt), dec(Xt, sXt, E4)
+    assert ((dX.cpu().double() - d64 @ w64.t()).abs() <= 1e-5 * (d64.abs() @ w64.abs().t())).all()
+    assert ((dW.cpu().double() - dt64 @ x64.t()).abs() <= 1e-5 * (dt64.abs() @ x64.abs().t())).all()
+    gg, u, dh64 = gu[:, :F].cpu().double(), gu[:, F:].cpu().double(), dh.cpu().double()
+    p = torch.sigmoid(gg)
+    d = torch.cat([dh64 * u * p * (1 + gg * (1 - p)), dh64 * gg * p], 1)
+    # E5M2 gradients and E4M3 operands: each term off by at most 2^-3 and 2^-4 of itself (and the formats' smallest steps)
+    lim = (2 ** -3 + 2 ** -4 + 2 ** -7) * 1.01
+    assert ((dX.cpu().double() - d @ Wgu.double()).abs() <= lim * (d.abs() @ Wgu.double().abs()) + 1e-3).all()
+    assert ((dW.cpu().double() - d.t() @ X[:M].double()).abs() <= lim * (d.abs().t() @ X[:M].double().abs()) + 1e-3).all()
+
+
+# ------------------------------------------------------------------ streams, graphs
+def test_other_stream_and_graph_replays(fq, gpu):
+    """A decode step and a backward on a side stream, captured once and replayed with changed inputs, equal the eager
+    calls of the same inputs every time."""
+    K, F, M = 512, 384, 3
+    x = torch.randn(M, K, device=gpu).bfloat16()
+    r = torch.randn(M, K, device=gpu).bfloat16()
+    w = torch.ones(K, device=gpu)
+    dh = torch.randn(M, F, device=gpu).bfloat16()
+    dy = torch.randn(M, K, device=gpu).bfloat16()
+    _, _, B, sB = operands(gpu, 1, F, K, seed=3)
+    Wd, sWd = operands(gpu, 1, K, F, seed=4)[2:]
+
+    def buffers():
+        u8, f4 = dict(dtype=torch.uint8, device=gpu), dict(device=gpu)
+        return dict(z=torch.empty_like(x), q=torch.empty(M, K, **u8), s=torch.empty(M, K // 128, **f4),
+                    rstd=torch.empty(M, **f4), h=torch.empty(M, F, **u8), hs=torch.empty(M, F // 128, **f4),
+                    gu=torch.empty(M, 2 * F, dtype=torch.bfloat16, device=gpu), o=torch.empty(M, K, dtype=torch.bfloat16, device=gpu),
+                    D=torch.empty(M, 2 * F, **u8), Ds=torch.empty(M, 2 * F // 128, **f4), Dt=torch.empty(2 * F, 128, **u8),
+                    Dts=torch.empty(2 * F, 1, **f4), Ht=torch.empty(F, 128, **u8), Hts=torch.empty(F, 1, **f4),
+                    dx=torch.empty_like(x), dw=torch.empty(K, **f4),
+                    ws=torch.empty(fq.fp8q_rmsnorm_bwd_workspace(M, K) // 4, **f4))
+
+    def step(b):
+        fq.fp8q_rmsnorm_1x128(x, K, r, K, w, M, K, NEPS, b["z"], K, None, 0, E4, EPS, b["q"], K, b["s"], K // 128, b["rstd"])
+        glu_call(fq, None, b["q"], E4, b["s"], B, E4, sB, 0, b["h"], b["gu"], M, F, K, q=(E4, b["hs"]))
+        fq.fp8q_gemm_blockscaled_few(b["h"], E4, F, b["hs"], F // 128, 1, Wd[0], E4, F, sWd[0], 2, F // 128, 1, b["o"], K, M, K, F)
+        fq.fp8q_glu_bwd_q(dh, F, b["gu"], 2 * F, 0, E5, EPS, b["D"], 2 * F, b["Ds"], 2 * F // 128, b["Dt"], 128, b["Dts"], 1, E4,
+                          b["Ht"], 128, b["Hts"], 1, M, F)
+        fq.fp8q_rmsnorm_bwd(dy, K, b["z"], K, w, b["rstd"], r, K, M, K, b["dx"], K, b["dw"], b["ws"], b["ws"].numel() * 4)
+
+    bg, be = buffers(), buffers()
+    torch.cuda.synchronize()
+    gr, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(gr, stream=side):
+        step(bg)
+    for rep in range(4):
+        gr.replay()
+        with torch.cuda.stream(side):
+            step(be)
+        torch.cuda.synchronize()
+        for k in bg:
+            if k != "ws":
+                assert torch.equal(bg[k].view(torch.uint8), be[k].view(torch.uint8)), (rep, k)
+        x.normal_()
+        dh.mul_(1.5)
+        dy.normal_()
+        torch.cuda.synchronize()
