@@ -22,7 +22,8 @@ LIB = os.path.join(HERE, "libfp8q.so")
 STREAM_LIB = os.path.join(HERE, "libfp8q_stream.so")
 ARCH = os.environ.get("FP8Q_ARCH", "gfx950")
 
-SOURCES = ["fp8q_api.hip", "fp8q_quant.hip", "fp8q_gemm.hip", "fp8q_norm.hip", "fp8q_glu_bwd.hip", "fp8q_few.hip"]
+SOURCES = ["fp8q_api.hip", "fp8q_quant.hip", "fp8q_gemm.hip", "fp8q_norm.hip", "fp8q_few.hip",
+           "fp8q_glu.hip", "fp8q_glu_bwd.hip"]
 STREAM_SOURCES = ["fp8q_stream.hip"]
 
 COMMON = [

@@ -263,7 +263,4 @@ int launch_few(const Proj& p, const char* what, hipStream_t st) {
   return check_launch(what);
 }
 
-// Simple form: every M by the few-row kernel.
-int launch_glu(const Proj& p, bool, const char* what, hipStream_t st) { return launch_few(p, what, st); }
-
 }  // namespace fp8q

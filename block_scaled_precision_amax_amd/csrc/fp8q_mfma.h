@@ -57,19 +57,26 @@ __device__ __forceinline__ v4f mfma32(typename Op<H16>::v8 a, typename Op<H16>::
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// act(g), and act'(g) where asked for.  SiLU: g * sg, sg = 1/(1 + e^-g); e^-g
-// overflows to Inf below g = -88 and gives -0, the limit.  GELU (tanh form):
-// g * p with p = (1 + tanh(k))/2 = 1/(1 + e^-2k), k = sqrt(2/pi) (g + 0.044715 g^3).
+// 1 / (1 + e^-x) by the hardware's base-2 exponential and reciprocal (each
+// within an fp32 step): off by at most (|x| + 3) 2^-24 of its value, where
+// the rounding of x log2(e) gives the first term.  e^-x passes to Inf below
+// x = -88 and the result to 0, its limit.
+__device__ __forceinline__ float sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.4426950408889634f));
+}
+
+// act(g), and act'(g) where asked for.  SiLU: g * sigmoid(g).  GELU (tanh
+// form): g * p with p = (1 + tanh(k))/2 = sigmoid(2k),
+// k = sqrt(2/pi) (g + 0.044715 g^3).
 template <bool GRAD>
 __device__ __forceinline__ float activation(int act, float g, float& grad) {
   if (act == FP8Q_ACT_SILU) {
-    const float sg = 1.0f / (1.0f + expf(-g));
+    const float sg = sigmoid(g);
     if (GRAD) grad = sg * (1.0f + g * (1.0f - sg));
     return g * sg;
   }
   const float c = 0.7978845608028654f, a = 0.044715f;
-  const float k = c * (g + a * g * g * g);
-  const float p = 1.0f / (1.0f + expf(-2.0f * k));
+  const float p = sigmoid(2.0f * c * (g + a * g * g * g));
   if (GRAD) {
     // p' = 2 p (1 - p) k'; 0 where p is 0 or 1, though g^2 may be Inf there
     const float d = 2.0f * p * (1.0f - p);
@@ -80,6 +87,47 @@ __device__ __forceinline__ float activation(int act, float g, float& grad) {
 __device__ __forceinline__ float activation(int act, float g) {
   float unused;
   return activation<false>(act, g, unused);
+}
+
+// ---- tiles.  The layouts, the copies and the tile order are those of the
+// block-scaled GEMM: a staged row is 128 bytes (one K block), its 16-byte
+// chunk c in slot c ^ swz(row) so that the sixteen rows of a fragment read
+// fall on different banks.
+__device__ __forceinline__ int swz_chunk(int r, int c) { return c ^ ((r & 6) | ((r >> 3) & 1)); }
+
+// Global-to-LDS copies as inline assembly: the compiler would wait for every
+// one of them before the first LDS read.  The kernel orders them with its own
+// vmcnt waits and barriers.  M0 holds the LDS address of lane 0; lane l
+// writes `size` bytes at M0 + l * size.
+__device__ __forceinline__ void lds_dma16(uint32_t lds_addr, const uint8_t* sbase, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(lds_addr), "v"(voff), "s"(sbase)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void lds_dma4(uint32_t lds_addr, const float* gptr) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+               :
+               : "s"(lds_addr), "v"(gptr)
+               : "memory", "m0");
+}
+__device__ __forceinline__ uint32_t lds_addr_of(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+// An empty asm that claims to rewrite v, which keeps the compiler from
+// moving the arithmetic around it.
+__device__ __forceinline__ void pin(v4f& v) { asm volatile("" : "+v"(v)); }
+
+// Tile number -> (tile row, tile column): each XCD gets a contiguous range,
+// walked in groups of eight tile rows.
+__device__ __forceinline__ void tile_of(int64_t bid, int64_t nbid, int64_t ntm, int64_t ntn, int64_t& tm, int64_t& tn) {
+  int64_t t = bid;
+  if ((nbid & 7) == 0) t = (bid & 7) * (nbid >> 3) + (bid >> 3);
+  const int64_t per_group = 8 * ntn, g = t / per_group, first = 8 * g;
+  const int64_t gs = (ntm - first) < 8 ? (ntm - first) : 8, r = t - g * per_group;
+  tm = first + r % gs;
+  tn = r / gs;
 }
 
 // Four consecutive elements of an output row from one lane; `vec`: the row
