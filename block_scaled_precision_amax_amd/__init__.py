@@ -165,6 +165,9 @@ def _stream(stream, t=None) -> int | None:
     import torch
 
     dev = t.device if (t is not None and not isinstance(t, int)) else None
+    if dev is not None and dev.type == "cuda":
+        # the handle alone: building a Stream object takes longer than a small launch
+        return torch._C._cuda_getCurrentRawStream(dev.index)
     return torch.cuda.current_stream(dev).cuda_stream
 
 

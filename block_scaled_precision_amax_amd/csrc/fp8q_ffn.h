@@ -77,10 +77,18 @@ __device__ __forceinline__ void load_w8(const void* w, int wdt, int64_t i, float
 }
 
 // Sum over the 64 lanes, the same bits in every lane (each step adds the
-// same two partial sums in both partners).
+// same two partial sums in both partners): quads, half rows and rows of 16
+// lanes by DPP, then the rows.
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+#define FP8Q_DPP_ADD(CTRL_) \
+  v += __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL_, 0xF, 0xF, false))
+  FP8Q_DPP_ADD(0xB1);   // lane ^ 1
+  FP8Q_DPP_ADD(0x4E);   // lane ^ 2
+  FP8Q_DPP_ADD(0x141);  // the other quad of the half row
+  FP8Q_DPP_ADD(0x140);  // the other half of the row
+#undef FP8Q_DPP_ADD
+  v += __shfl_xor(v, 16);
+  v += __shfl_xor(v, 32);
   return v;
 }
 

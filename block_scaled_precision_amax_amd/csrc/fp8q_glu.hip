@@ -85,7 +85,8 @@ __device__ __forceinline__ void drain_tile(const uint8_t* stg, int tid, T* out, 
 
 // OUT: FP8Q_F32, FP8Q_BF16 or 2 + format (1x128 codes).
 template <int FA, int FB, int OUT, bool FAST>
-__global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, int64_t ntm, int64_t ntn) {
+__global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, const float* __restrict__ s0,
+                                                     const float* __restrict__ s1, int64_t ntm, int64_t ntn) {
   using S = Shape<FAST>;
   constexpr int TI = S::TI, BM = S::BM, NST = S::NST;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
@@ -165,9 +166,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, int64_t ntm, 
     const int a_row0 = (wm * TI * 16 + lr) * BK;
     auto b_row = [&](int j) { return ((j >> 1) * 128 + 32 * wn + 16 * (j & 1) + lr) * BK; };
     const int o0 = 16 * swz_chunk(lr, 2 * lq), o1 = 16 * swz_chunk(lr, 2 * lq + 1);
-    // every column of the tile lies in one 128-column block of scales
-    const float* sg = p.s0 + (n0 >> 7) * p.sB_sn;
-    const float* su = p.s1 + (n0 >> 7) * p.sB_sn;
+    // every column of the tile lies in one 128-column block of scales; they
+    // are read by scalar loads (restrict arguments): a vector load here would
+    // wait for every copy in flight
+    const float* sg = s0 + (n0 >> 7) * p.sB_sn;
+    const float* su = s1 + (n0 >> 7) * p.sB_sn;
 
     constexpr bool H16 = FA == FP8Q_E5M2 || FB == FP8Q_E5M2;
     using V8 = typename Op<H16>::v8;
@@ -424,7 +427,8 @@ static void launch_t(const Proj& p, hipStream_t st) {
   int64_t g = device_cu_count() / 8 * 8;
   if (g < 8) g = 8;
   if (ntm * ntn < g) g = ntm * ntn;
-  hipLaunchKernelGGL((k_glu<FA, FB, OUT, FAST>), dim3((unsigned)g), dim3(kThreads), 0, st, p, ntm, ntn);
+  hipLaunchKernelGGL((k_glu<FA, FB, OUT, FAST>), dim3((unsigned)g), dim3(kThreads), 0, st, p, p.s0, p.s1,
+                     ntm, ntn);
 }
 
 template <int FA, int FB>

@@ -33,10 +33,29 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
   return v;
 }
 
+// Eight elements of a row as loaded, and as fp32.
+template <int DT>
+struct Raw8 {
+  u32x4 v[DT == FP8Q_F32 ? 2 : 1];
+  template <bool STREAM = true>
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    const u32x4* q = (const u32x4*)((const char*)p + i * (DT == FP8Q_F32 ? 4 : 2));
+#pragma unroll
+    for (int k = 0; k < (DT == FP8Q_F32 ? 2 : 1); ++k) v[k] = STREAM ? __builtin_nontemporal_load(q + k) : q[k];
+  }
+  __device__ __forceinline__ float operator[](int e) const {
+    if constexpr (DT == FP8Q_F32) return __uint_as_float(v[e >> 2][e & 3]);
+    else return e & 1 ? bf_hi(v[0][e >> 1]) : bf_lo(v[0][e >> 1]);
+  }
+};
+
 // One row per TPR threads, V groups of eight consecutive elements a thread:
 // group g of thread t is elements 8 * (g * TPR + t), so 16 neighbouring
-// lanes hold one 128-element block.
-template <int DT, int FMT, int TPR, int V>
+// lanes hold one 128-element block.  All of a row's loads, the weight's among
+// them, are issued before its sum and without a branch (a thread past the
+// last column reads the last group again), so the row costs one trip to
+// memory.
+template <int DT, int WDT, int TPR, int V, bool RES>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm_1x128(const NormFwd p) {
   constexpr int TH = TPR < 256 ? 256 : TPR;
   __shared__ float part[TH / 64];
@@ -44,81 +63,95 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm_1x128(const N
   const int64_t row = (int64_t)blockIdx.x * (TH / TPR) + threadIdx.x / TPR;
   if (TPR == 64 && row >= p.rows) return;  // whole wavefronts; no barrier with TPR == 64
   const int nv = (int)(p.cols / 8);
+  Raw8<DT> x[V], r[V];
+  Raw8<WDT> w[V];
+  int cc[V];
+  bool in[V];
+#pragma unroll
+  for (int g = 0; g < V; ++g) {
+    in[g] = g * TPR + t < nv;
+    cc[g] = in[g] ? g * TPR + t : nv - 1;
+    x[g].load(p.x, row * p.ldx + 8 * cc[g]);
+    if constexpr (RES) r[g].load(p.res, row * p.ldr + 8 * cc[g]);
+  }
+#pragma unroll
+  for (int g = 0; g < V; ++g) w[g].template load<false>(p.w, 8 * cc[g]);
   float v[V][8];
   float ss = 0.0f;
 #pragma unroll
   for (int g = 0; g < V; ++g) {
-    const int c = g * TPR + t;
-    if (c < nv) {
-      load8<DT>(p.x, row * p.ldx + 8 * c, v[g]);
-      if (p.res) {
-        float r[8];
-        load8<DT>(p.res, row * p.ldr + 8 * c, r);
+    float s = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[g][e] += r[e];
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[g][e] = 0.0f;
+    for (int e = 0; e < 8; ++e) {
+      v[g][e] = RES ? x[g][e] + r[g][e] : x[g][e];
+      s = __builtin_fmaf(v[g][e], v[g][e], s);
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[g][e], v[g][e], ss);
+    ss += in[g] ? s : 0.0f;
   }
   ss = row_sum<TPR>(ss, part);
   const float rstd = 1.0f / sqrtf(ss / (float)p.cols + p.neps);
   if (t == 0 && p.rstd) p.rstd[row] = rstd;
 #pragma unroll
   for (int g = 0; g < V; ++g) {
-    const int c = g * TPR + t;
-    if (c >= nv) continue;  // whole 16-lane rows: cols is a multiple of 128
+    if (!in[g]) continue;  // whole 16-lane rows: cols is a multiple of 128
+    const int c = cc[g];
     // the sum is stored in x's type; the norm goes on from the unrounded sum
     if (p.z) store8<DT>(p.z, row * p.ldz + 8 * c, v[g]);
-    float w[8], y[8];
-    load_w8(p.w, p.wdt, 8 * c, w);
+    float y[8];
     uint32_t m = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      y[e] = v[g][e] * rstd * w[e];
+      y[e] = v[g][e] * rstd * w[g][e];
       m = max(m, abs_bits(y[e]));
     }
     if (p.y) store8<DT>(p.y, row * p.ldy + 8 * c, y);
     if (p.q) {
-      const float s = block_scale<FMT>(__uint_as_float(canon_abs_bits(row16_max(m))), p.qeps);
+      const float amax = __uint_as_float(canon_abs_bits(row16_max(m)));
+      const bool e4 = p.fmt == FP8Q_E4M3FN;
+      const float s = e4 ? block_scale<FP8Q_E4M3FN>(amax, p.qeps) : block_scale<FP8Q_E5M2>(amax, p.qeps);
       const bool fast = scale_ok(s);
-      const float r = 1.0f / s;
-      const u32x2 q = {encode4<FMT>(y[0], y[1], y[2], y[3], s, r, fast),
-                       encode4<FMT>(y[4], y[5], y[6], y[7], s, r, fast)};
+      const float inv = 1.0f / s;
+      u32x2 q;
+      if (e4)
+        q = u32x2{encode4<FP8Q_E4M3FN>(y[0], y[1], y[2], y[3], s, inv, fast),
+                  encode4<FP8Q_E4M3FN>(y[4], y[5], y[6], y[7], s, inv, fast)};
+      else
+        q = u32x2{encode4<FP8Q_E5M2>(y[0], y[1], y[2], y[3], s, inv, fast),
+                  encode4<FP8Q_E5M2>(y[4], y[5], y[6], y[7], s, inv, fast)};
       __builtin_nontemporal_store(q, (u32x2*)(p.q + row * p.ldq + 8 * c));
       if ((t & 15) == 0) p.scales[row * p.ld_s + (c >> 4)] = s;
     }
   }
 }
 
-template <int DT, int FMT, int TPR, int V>
+template <int DT, int WDT, int TPR, int V>
 static void launch_fwd(const NormFwd& p, hipStream_t st) {
   constexpr int TH = TPR < 256 ? 256 : TPR, R = TH / TPR;
-  hipLaunchKernelGGL((k_rmsnorm_1x128<DT, FMT, TPR, V>), dim3((unsigned)((p.rows + R - 1) / R)), dim3(TH), 0, st, p);
+  const dim3 grid((unsigned)((p.rows + R - 1) / R)), block(TH);
+  if (p.res) hipLaunchKernelGGL((k_rmsnorm_1x128<DT, WDT, TPR, V, true>), grid, block, 0, st, p);
+  else hipLaunchKernelGGL((k_rmsnorm_1x128<DT, WDT, TPR, V, false>), grid, block, 0, st, p);
 }
 
-template <int DT, int FMT>
+template <int DT, int WDT>
 static void dispatch_fwd(const NormFwd& p, hipStream_t st) {
   const int64_t c = p.cols;
-  if (c <= 64 * 8) launch_fwd<DT, FMT, 64, 1>(p, st);
-  else if (c <= 64 * 8 * 2) launch_fwd<DT, FMT, 64, 2>(p, st);
-  else if (c <= 64 * 8 * 4) launch_fwd<DT, FMT, 64, 4>(p, st);
-  else if (c <= 256 * 8 * 2) launch_fwd<DT, FMT, 256, 2>(p, st);
-  else if (c <= 256 * 8 * 4) launch_fwd<DT, FMT, 256, 4>(p, st);
-  else if (c <= 256 * 8 * 8) launch_fwd<DT, FMT, 256, 8>(p, st);
-  else launch_fwd<DT, FMT, 1024, 8>(p, st);
+  if (c <= 64 * 8) launch_fwd<DT, WDT, 64, 1>(p, st);
+  else if (c <= 64 * 8 * 2) launch_fwd<DT, WDT, 64, 2>(p, st);
+  else if (c <= 64 * 8 * 4) launch_fwd<DT, WDT, 64, 4>(p, st);
+  else if (c <= 256 * 8 * 2) launch_fwd<DT, WDT, 256, 2>(p, st);
+  else if (c <= 256 * 8 * 4) launch_fwd<DT, WDT, 256, 4>(p, st);
+  else if (c <= 512 * 8 * 4) launch_fwd<DT, WDT, 512, 4>(p, st);
+  else if (c <= 1024 * 8 * 4) launch_fwd<DT, WDT, 1024, 4>(p, st);
+  else launch_fwd<DT, WDT, 1024, 8>(p, st);
 }
 
 int launch_rmsnorm_1x128(const NormFwd& p, hipStream_t st) {
   if (p.dt == FP8Q_F32) {
-    if (p.fmt == FP8Q_E4M3FN) dispatch_fwd<FP8Q_F32, FP8Q_E4M3FN>(p, st);
-    else dispatch_fwd<FP8Q_F32, FP8Q_E5M2>(p, st);
+    if (p.wdt == FP8Q_F32) dispatch_fwd<FP8Q_F32, FP8Q_F32>(p, st);
+    else dispatch_fwd<FP8Q_F32, FP8Q_BF16>(p, st);
   } else {
-    if (p.fmt == FP8Q_E4M3FN) dispatch_fwd<FP8Q_BF16, FP8Q_E4M3FN>(p, st);
-    else dispatch_fwd<FP8Q_BF16, FP8Q_E5M2>(p, st);
+    if (p.wdt == FP8Q_F32) dispatch_fwd<FP8Q_BF16, FP8Q_F32>(p, st);
+    else dispatch_fwd<FP8Q_BF16, FP8Q_BF16>(p, st);
   }
   return check_launch("rmsnorm_1x128");
 }
@@ -127,23 +160,41 @@ int launch_rmsnorm_1x128(const NormFwd& p, hipStream_t st) {
 // Each TPR threads walk rows part, part + parts, ... and keep the weight's
 // gradient of their columns in registers; at the end every workgroup writes
 // its sums as one row of the workspace, and k_norm_dw adds those rows in a
-// fixed order, so the result does not depend on timing.
+// fixed order, so the result does not depend on timing.  The next row's
+// loads are issued before this row's sum is joined.  Parts: at most two
+// workgroups a compute unit (512; what their registers allow), and no more
+// than one per eight rows above 256, so that the partial rows stay a few
+// percent of the traffic.
 static constexpr int64_t kNormParts = 512;
 
-static int norm_tpr(int64_t cols) { return cols <= 2048 ? 64 : cols <= 16384 ? 256 : 1024; }
-
 int64_t rmsnorm_bwd_parts(int64_t rows, int64_t cols) {
-  const int64_t per = norm_tpr(cols) == 64 ? 4 : 1;  // rows a workgroup holds at once
-  const int64_t g = (rows + per - 1) / per;
-  return g < kNormParts ? g : kNormParts;
+  const int64_t per = cols <= 2048 ? 4 : 1;  // rows a workgroup holds at once
+  const int64_t all = (rows + per - 1) / per;
+  int64_t g = rows / 8 < 256 ? 256 : rows / 8;
+  if (g > kNormParts) g = kNormParts;
+  return all < g ? all : g;
 }
 
-template <int DT, int TPR, int V>
+template <int DT, int TPR, int V, bool RES>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm_bwd(const NormBwd p) {
   constexpr int TH = TPR < 256 ? 256 : TPR, R = TH / TPR;
+  // The weight waits in LDS (two planes of four, free of bank conflicts), as
+  // far as it fits: a global read here would come back behind the next row's
+  // loads.
+  constexpr int NW = V * TPR;  // groups of eight columns
+  constexpr bool WL = NW * 32 <= 128 * 1024;
   __shared__ float part[2][TH / 64];
+  __shared__ float4 w_lds[2][WL ? NW : 1];
   const int t = threadIdx.x % TPR;
   const int nv = (int)(p.cols / 8);
+  auto weights = [&](int c, float(&w)[8]) {
+    if constexpr (WL) {
+      const float4 a = w_lds[0][c], b = w_lds[1][c];
+      w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    } else {
+      load_w8(p.w, p.wdt, 8 * c, w);
+    }
+  };
   float dw[V][8];
 #pragma unroll
   for (int g = 0; g < V; ++g)
@@ -151,44 +202,84 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm_bwd(const Nor
     for (int e = 0; e < 8; ++e) dw[g][e] = 0.0f;
   const float rc = 1.0f / (float)p.cols;
   int flip = 0;
-  for (int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / TPR; row < p.rows; row += (int64_t)gridDim.x * R) {
-    const float rstd = p.rstd[row];
-    float tt[V][8], xh[V][8];
+  const int64_t step = (int64_t)gridDim.x * R;
+  int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / TPR;
+  // The loop has no branch around a load, so that each wait counts exactly
+  // what it needs: a thread past the last column reads the last group again
+  // and its part of the sum is dropped, and the last row is read again for
+  // want of a next one (cache hits).
+  int cc[V];
+  bool in[V];
+#pragma unroll
+  for (int g = 0; g < V; ++g) {
+    in[g] = g * TPR + t < nv;
+    cc[g] = in[g] ? g * TPR + t : nv - 1;
+  }
+  // rows are held as loaded and widened twice: in fp32 their registers would
+  // leave room for fewer workgroups
+  struct Row {
+    Raw8<DT> dy[V], z[V];
+    float rstd;
+  } even, odd;  // taken in turn: copying one to the other would wait for its loads
+  auto load = [&](Row& w, int64_t r) {
+    if (r >= p.rows) r = p.rows - 1;
+    w.rstd = p.rstd[r];
+#pragma unroll
+    for (int g = 0; g < V; ++g) {
+      w.dy[g].load(p.dy, r * p.lddy + 8 * cc[g]);
+      w.z[g].load(p.z, r * p.ldz + 8 * cc[g]);
+    }
+  };
+  load(even, row);
+  if constexpr (WL) {
+    for (int c = threadIdx.x; c < nv; c += TH) {
+      float w[8];
+      load_w8(p.w, p.wdt, 8 * c, w);
+      w_lds[0][c] = make_float4(w[0], w[1], w[2], w[3]);
+      w_lds[1][c] = make_float4(w[4], w[5], w[6], w[7]);
+    }
+    __syncthreads();
+  }
+  auto one = [&](Row& cur, Row& nxt) {
+    const float rs = cur.rstd;
+    Raw8<DT> dr[V];
+    if constexpr (RES) {
+#pragma unroll
+      for (int g = 0; g < V; ++g) dr[g].load(p.dres, row * p.lddr + 8 * cc[g]);
+    }
     float dot = 0.0f;
 #pragma unroll
     for (int g = 0; g < V; ++g) {
-      const int c = g * TPR + t;
-      if (c < nv) {
-        float w[8];
-        load8<DT>(p.dy, row * p.lddy + 8 * c, tt[g]);
-        load8<DT>(p.z, row * p.ldz + 8 * c, xh[g]);
-        load_w8(p.w, p.wdt, 8 * c, w);
+      float w[8], d = 0.0f;
+      weights(cc[g], w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          xh[g][e] *= rstd;
-          dw[g][e] = __builtin_fmaf(tt[g][e], xh[g][e], dw[g][e]);
-          tt[g][e] *= w[e];
-          dot = __builtin_fmaf(tt[g][e], xh[g][e], dot);
-        }
+      for (int e = 0; e < 8; ++e) {
+        const float xh = cur.z[g][e] * rs;
+        dw[g][e] = __builtin_fmaf(cur.dy[g][e], xh, dw[g][e]);
+        d = __builtin_fmaf(cur.dy[g][e] * w[e], xh, d);
       }
+      dot += in[g] ? d : 0.0f;
     }
+    load(nxt, row + step);
     dot = row_sum<TPR>(dot, part[flip]) * rc;
     flip ^= 1;  // the next row's sums go to the other slots: no wave still reads those
 #pragma unroll
     for (int g = 0; g < V; ++g) {
-      const int c = g * TPR + t;
-      if (c >= nv) continue;
-      float d[8];
+      float w[8], d[8];
+      weights(cc[g], w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[e] = rstd * __builtin_fmaf(-xh[g][e], dot, tt[g][e]);
-      if (p.dres) {
-        float r[8];
-        load8<DT>(p.dres, row * p.lddr + 8 * c, r);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] += r[e];
+      for (int e = 0; e < 8; ++e) {
+        d[e] = rs * __builtin_fmaf(-(cur.z[g][e] * rs), dot, cur.dy[g][e] * w[e]);
+        if constexpr (RES) d[e] += dr[g][e];
       }
-      store8<DT>(p.dx, row * p.lddx + 8 * c, d);
+      if (in[g]) store8<DT>(p.dx, row * p.lddx + 8 * cc[g], d);
     }
+  };
+  for (; row < p.rows; row += step) {
+    one(even, odd);
+    row += step;
+    if (row >= p.rows) break;
+    one(odd, even);
   }
   if (!p.dw) return;
   if constexpr (R > 1) {
@@ -217,28 +308,36 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm_bwd(const Nor
   }
 }
 
-// dw[c] = sum of the partial rows: 32 columns per workgroup, eight threads
-// per column each adding every eighth row, joined in a fixed order.
+// dw[c] = sum of the partial rows: 64 columns per workgroup, sixteen groups
+// of threads each adding every sixteenth row, joined in a fixed order.
 __global__ __launch_bounds__(256) void k_norm_dw(const float* __restrict__ ws, int64_t parts, int64_t cols,
                                                  float* __restrict__ dw) {
-  __shared__ float sum[8][32];
-  const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
-  const int64_t col = (int64_t)blockIdx.x * 32 + c;
-  float a = 0.0f;
-  for (int64_t r = k; r < parts; r += 8) a += ws[r * cols + col];
-  sum[k][c] = a;
-  __syncthreads();
-  if (k == 0) {
-    a = 0.0f;
+  __shared__ float sum[16][64];
+  const int c = threadIdx.x & 15, k = threadIdx.x >> 4;
+  const float* p = ws + (int64_t)blockIdx.x * 64 + 4 * c;
+  v4f a = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+  for (int64_t r = k; r < parts; r += 16) {
+    const v4f b = *(const v4f*)(p + r * cols);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a += sum[i][c];
-    dw[col] = a;
+    for (int e = 0; e < 4; ++e) a[e] += b[e];
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sum[k][4 * c + e] = a[e];
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t += sum[i][threadIdx.x];
+    dw[(int64_t)blockIdx.x * 64 + threadIdx.x] = t;
   }
 }
 
 template <int DT, int TPR, int V>
 static void launch_bwd(const NormBwd& p, int64_t parts, hipStream_t st) {
-  hipLaunchKernelGGL((k_rmsnorm_bwd<DT, TPR, V>), dim3((unsigned)parts), dim3(TPR < 256 ? 256 : TPR), 0, st, p);
+  const dim3 grid((unsigned)parts), block(TPR < 256 ? 256 : TPR);
+  if (p.dres) hipLaunchKernelGGL((k_rmsnorm_bwd<DT, TPR, V, true>), grid, block, 0, st, p);
+  else hipLaunchKernelGGL((k_rmsnorm_bwd<DT, TPR, V, false>), grid, block, 0, st, p);
 }
 
 template <int DT>
@@ -249,7 +348,8 @@ static void dispatch_bwd(const NormBwd& p, int64_t parts, hipStream_t st) {
   else if (c <= 64 * 8 * 4) launch_bwd<DT, 64, 4>(p, parts, st);
   else if (c <= 256 * 8 * 2) launch_bwd<DT, 256, 2>(p, parts, st);
   else if (c <= 256 * 8 * 4) launch_bwd<DT, 256, 4>(p, parts, st);
-  else if (c <= 256 * 8 * 8) launch_bwd<DT, 256, 8>(p, parts, st);
+  else if (c <= 512 * 8 * 4) launch_bwd<DT, 512, 4>(p, parts, st);
+  else if (c <= 1024 * 8 * 4) launch_bwd<DT, 1024, 4>(p, parts, st);
   else launch_bwd<DT, 1024, 8>(p, parts, st);
 }
 
@@ -258,7 +358,7 @@ int launch_rmsnorm_bwd(const NormBwd& p, hipStream_t st) {
   if (p.dt == FP8Q_F32) dispatch_bwd<FP8Q_F32>(p, parts, st);
   else dispatch_bwd<FP8Q_BF16>(p, parts, st);
   if (p.dw)
-    hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)(p.cols / 32)), dim3(256), 0, st, p.ws, parts, p.cols, p.dw);
+    hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)(p.cols / 64)), dim3(256), 0, st, p.ws, parts, p.cols, p.dw);
   return check_launch("rmsnorm_bwd");
 }
 
