@@ -53,6 +53,7 @@ SYMBOLS = (
     "fp8q_glu_blockscaled",
     "fp8q_glu_blockscaled_fast",
     "fp8q_glu_blockscaled_q",
+    "fp8q_glu_blockscaled_q_workspace",
     "fp8q_glu_bwd_q",
     "fp8q_gemm_blockscaled_few",
 )
@@ -126,7 +127,8 @@ def lib() -> ctypes.CDLL:
             "fp8q_glu_blockscaled_fast": (i32, [vp, i32, i64, vp, i64, i64, vp, vp, i32, i64, vp, vp, i64, i64, i32, vp,
                                                 i32, i64, vp, i64, i64, i64, i64, vp]),
             "fp8q_glu_blockscaled_q": (i32, [vp, i32, i64, vp, i64, i64, vp, vp, i32, i64, vp, vp, i64, i64, i32, i32,
-                                             f32, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp]),
+                                             f32, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp, i64, vp]),
+            "fp8q_glu_blockscaled_q_workspace": (i64, [i64, i64]),
             "fp8q_glu_bwd_q": (i32, [vp, i32, i64, vp, i64, i32, i32, f32, vp, i64, vp, i64, vp, i64, vp, i64, i32, vp,
                                      i64, vp, i64, i64, i64, vp]),
             "fp8q_gemm_blockscaled_few": (i32, [vp, i32, i64, vp, i64, i64, vp, i32, i64, vp, i32, i64, i64, vp, i32,
@@ -315,11 +317,25 @@ def fp8q_glu_blockscaled_fast(A, fa, lda, sA, sA_sm, sA_skb, Bg, Bu, fb, ldb, sB
                                            ldgu, M, F, K, _stream(stream, A)))
 
 
+def fp8q_glu_blockscaled_q_workspace(M, F) -> int:
+    return lib().fp8q_glu_blockscaled_q_workspace(M, F)
+
+
 def fp8q_glu_blockscaled_q(A, fa, lda, sA, sA_sm, sA_skb, Bg, Bu, fb, ldb, sBg, sBu, sB_sn, sB_skb, act, fc, eps, Hq,
-                           ldhq, Hs, ld_hs, gu, ldgu, M, F, K, stream=None) -> None:
+                           ldhq, Hs, ld_hs, gu, ldgu, M, F, K, ws=None, ws_bytes=0, stream=None) -> None:
+    """Without `ws`, the few bytes a call of few rows needs come from torch's allocator."""
+    handle = _stream(stream, A)
+    if ws is None:
+        ws_bytes = lib().fp8q_glu_blockscaled_q_workspace(M, F)
+        if ws_bytes:
+            import torch
+
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=Hq.device)
+            if stream is not None:  # the allocator may hand it out again only behind that stream's work
+                ws.record_stream(torch.cuda.ExternalStream(handle, device=Hq.device))
     _check(lib().fp8q_glu_blockscaled_q(_ptr(A), fa, lda, _ptr(sA), sA_sm, sA_skb, _ptr(Bg), _ptr(Bu), fb, ldb,
                                         _ptr(sBg), _ptr(sBu), sB_sn, sB_skb, act, fc, eps, _ptr(Hq), ldhq, _ptr(Hs),
-                                        ld_hs, _ptr(gu), ldgu, M, F, K, _stream(stream, A)))
+                                        ld_hs, _ptr(gu), ldgu, M, F, K, _ptr(ws), ws_bytes, handle))
 
 
 def fp8q_glu_bwd_q(dH, lddh, gu, ldgu, act, fc, eps, Dq, lddq, Ds, ld_ds, Dt, lddt, Dst, ld_dst, fh, Ht, ldht, Hst,

@@ -499,7 +499,8 @@ int fp8q_glu_blockscaled_q(const uint8_t* A, fp8q_format fa, int64_t lda, const 
                            int64_t sA_skb, const uint8_t* Bg, const uint8_t* Bu, fp8q_format fb, int64_t ldb,
                            const float* sBg, const float* sBu, int64_t sB_sn, int64_t sB_skb, fp8q_act act,
                            fp8q_format fc, float eps, uint8_t* Hq, int64_t ldhq, float* Hs, int64_t ld_hs,
-                           uint16_t* gu, int64_t ldgu, int64_t M, int64_t F, int64_t K, void* stream) {
+                           uint16_t* gu, int64_t ldgu, int64_t M, int64_t F, int64_t K, void* ws, int64_t ws_bytes,
+                           void* stream) {
   const char* fn = "glu_blockscaled_q";
   if (!Hq || !Hs) return fail(FP8Q_EINVAL, "%s: null pointer", fn);
   if (!valid_fmt(fc)) return fail(FP8Q_EINVAL, "%s: bad format", fn);
@@ -508,11 +509,18 @@ int fp8q_glu_blockscaled_q(const uint8_t* A, fp8q_format fa, int64_t lda, const 
   if (int rc = check_gu(fn, act, gu, ldgu, F)) return rc;
   if (F % 128 != 0) return fail(FP8Q_ESHAPE, "%s: F (%lld) must be a multiple of 128", fn, (long long)F);
   if (ldhq < F || ld_hs < F / 128) return fail(FP8Q_EINVAL, "%s: leading dimension too small", fn);
-  if (!aligned(Hs, 4)) return fail(FP8Q_EALIGN, "%s: misaligned scales", fn);
+  if (!aligned(Hs, 4) || !aligned(Hq, 4) || ldhq % 4 != 0)
+    return fail(FP8Q_EALIGN, "%s: Hq, its rows and Hs must be 4-byte aligned", fn);
+  const int64_t need = glu_q_workspace(M, F);
+  if (need && (!ws || ws_bytes < need)) return fail(FP8Q_EINVAL, "%s: the workspace needs %lld bytes", fn, (long long)need);
+  if (need && !aligned(ws, 16)) return fail(FP8Q_EALIGN, "%s: ws must be 16-byte aligned", fn);
   Proj p = make_proj(A, fa, lda, sA, sA_sm, sA_skb, Bg, Bu, fb, ldb, sBg, sBu, FP8Q_GRAN_128x128, sB_sn, sB_skb, M, F, K);
   p.out = Hq, p.ldo = ldhq, p.scales = Hs, p.ld_s = ld_hs, p.fc = fc, p.eps = eps, p.act = act, p.gu = gu, p.ldgu = ldgu;
+  p.ws = (float*)ws;
   return launch_glu(p, false, fn, S(stream));
 }
+
+int64_t fp8q_glu_blockscaled_q_workspace(int64_t M, int64_t F) { return M <= 0 || F <= 0 || F % 128 != 0 ? 0 : glu_q_workspace(M, F); }
 
 int fp8q_glu_bwd_q(const void* dH, fp8q_dtype dt, int64_t lddh, const uint16_t* gu, int64_t ldgu, fp8q_act act,
                    fp8q_format fc, float eps, uint8_t* Dq, int64_t lddq, float* Ds, int64_t ld_ds, uint8_t* Dt,

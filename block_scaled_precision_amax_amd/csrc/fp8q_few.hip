@@ -13,17 +13,19 @@
 // (24 GB/s a compute unit measured, against 41 with whole lines), so a load
 // takes eight rows, eight lanes a line; the rows then change lanes through a
 // 2 KB tile of LDS that is the wavefront's own (no barrier), are decoded
-// without loss and multiplied against the same block of A.  Loads run PD
-// blocks ahead of the arithmetic: a wavefront's own stream has to cover the
-// memory's latency.  Everything after the decode is fp32: products of two
+// without loss and multiplied against the same block of A.  The next
+// block's loads are issued as soon as this one's rows are in LDS; a deeper
+// pipeline cost registers and was slower (21.5 against 23.7 us for 7168 x
+// 18432, one row).  Everything after the decode is fp32: products of two
 // codes are exact, each block sum is folded into an fp32 accumulator with its
 // scales.
 //
-// The sum over K blocks is the same for every split: block kb belongs to
-// class kb % 8, the blocks of a class are added in order, and the classes are
-// joined as (((0+1)+2)+3) + (((4+5)+6)+7).  KS wavefronts share the classes
-// and join their own in registers, the rest in LDS, so the quantized output
-// holds the codes of exactly the fp32 values that the unquantized one stores.
+// Wavefront w of a workgroup adds blocks w, w + 8, ... in order and the eight
+// sums are joined in LDS in a fixed order.  The quantized output of the gated
+// projection is the same kernel's fp32 output in a workspace and the 1x128
+// quantizer: a workgroup that held the 128 columns of a block would leave
+// most compute units without work (2048 columns: 16 workgroups, 42 us against
+// 12).
 #include "fp8q_mfma.h"
 
 #include <type_traits>
@@ -32,35 +34,30 @@ namespace fp8q {
 
 using namespace ffn;
 
-static constexpr int kClasses = 8;
+static constexpr int kWaves = 8;
 // K blocks whose A scales a workgroup keeps in LDS.  Read where they are
 // used, they cost a request per lane and block (sixteen rows, a line each),
 // more than A itself; K beyond this (20480) reads them so.
 static constexpr int kScaleBlocks = 160;
 
-__device__ __forceinline__ v4f add4(v4f a, v4f b) {
-  return v4f{a[0] + b[0], a[1] + b[1], a[2] + b[2], a[3] + b[3]};
-}
-
-// KS wavefronts share the K blocks of a group of 16 NJ columns (GLU: 16 of g
-// and of u, NJ = 2); NCG such groups a workgroup; RT tiles of 16 rows.  OUT:
-// FP8Q_F32, FP8Q_BF16, or 2 + format for 1x128 codes (NCG = 8: a workgroup
-// then holds the 128 columns of a block).
-template <int FA, int FB, int GB, bool GLU, int OUT, int NJ, int NCG, int KS, int RT, int PD>
-__global__ __launch_bounds__(64 * NCG * KS) void k_few(const Proj p) {
+// Eight wavefronts share the K blocks of a group of columns: 16 of g and the
+// same 16 of u (GLU, NJ = 2), or 16 NJ columns.  RT tiles of 16 rows.  OUT:
+// FP8Q_F32 or FP8Q_BF16.
+template <int FA, int FB, int GB, bool GLU, int OUT, int NJ, int RT>
+__global__ __launch_bounds__(64 * kWaves) void k_few(const Proj p) {
   constexpr bool H16 = FA == FP8Q_E5M2 || FB == FP8Q_E5M2;
-  constexpr int GC = GLU ? 16 : 16 * NJ;  // columns of a group
+  constexpr int NS = GB == FP8Q_GRAN_1x128 ? 4 : 1;  // B scales of a lane's four columns
   using V8 = typename Op<H16>::v8;
   // the wavefronts' exchange tiles (NJ of B, RT of A), then their partial sums
-  constexpr int XCH = NCG * KS * (NJ + RT) * 2048, RED = KS * NCG * RT * NJ * 1024;
+  constexpr int XCH = kWaves * (NJ + RT) * 2048, RED = kWaves * RT * NJ * 1024;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[XCH > RED ? XCH : RED];
-  __shared__ uint32_t rmax[OUT >= 2 ? NCG : 1][RT * 16];
   constexpr int SP = RT * 16 + 1;  // [block][row], padded for the writes
   __shared__ float sa_lds[kScaleBlocks * SP];
   const int lane = threadIdx.x & 63, lr = lane & 15, lq = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int cg = wave / KS, ks = wave % KS;
-  const int64_t n0 = ((int64_t)blockIdx.x * NCG + cg) * GC;
+  const int64_t n0 = (int64_t)blockIdx.x * (GLU ? 16 : 16 * NJ);
+  const int64_t m0 = (int64_t)blockIdx.y * (16 * RT);
+  const int rows = (int)(p.M - m0 < 16 * RT ? p.M - m0 : 16 * RT);
   const int nkb = (int)(p.K / 128);
 
   // the lane's rows of B and of A, l / 8 and 8 + l / 8 of a tile, and its
@@ -68,87 +65,45 @@ __global__ __launch_bounds__(64 * NCG * KS) void k_few(const Proj p) {
   // results are never stored)
   const int xr = lane >> 3, xc = lane & 7;
   auto clampn = [&](int64_t n) { return n < p.N ? n : p.N - 1; };
-  const uint8_t* b[NJ][2];
-  const float* sb[NJ];
+  auto clampm = [&](int m) { return m < rows ? m : rows - 1; };
+  const uint8_t *b[NJ][2], *a[RT][2];
+  const float *sb[NJ], *sa[RT];
+  int srow[RT];
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     const int64_t c0 = GLU ? n0 : n0 + 16 * j;
 #pragma unroll
     for (int v = 0; v < 2; ++v) b[j][v] = (GLU && j ? p.B1 : p.B0) + clampn(c0 + 8 * v + xr) * p.ldb + 16 * xc;
-    // 1x128 scales: the lane's four columns start at sb[j]
-    sb[j] = (GLU && j ? p.s1 : p.s0) + (GB == FP8Q_GRAN_1x128 ? 0 : (clampn(c0) >> 7) * p.sB_sn);
+    sb[j] = (GLU && j ? p.s1 : p.s0) + (NS == 4 ? 0 : (clampn(c0) >> 7) * p.sB_sn);
   }
-  const uint8_t* a[RT][2];
-  const float* sa[RT];
-  int srow[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
-    auto clampm = [&](int64_t m) { return m < p.M ? m : p.M - 1; };
 #pragma unroll
-    for (int v = 0; v < 2; ++v) a[i][v] = p.A + clampm(16 * i + 8 * v + xr) * p.lda + 16 * xc;
-    srow[i] = (int)clampm(16 * i + lr);
-    sa[i] = p.sA + srow[i] * p.sA_sm;
+    for (int v = 0; v < 2; ++v) a[i][v] = p.A + (m0 + clampm(16 * i + 8 * v + xr)) * p.lda + 16 * xc;
+    srow[i] = clampm(16 * i + lr);
+    sa[i] = p.sA + (m0 + srow[i]) * p.sA_sm;
   }
   // exchange: chunk c of row r in slot swz_chunk(r, c) of the row
   uint8_t* const xch = lds + wave * (NJ + RT) * 2048;
   const int w0 = xr * 128 + 16 * swz_chunk(xr, xc), w1 = (8 + xr) * 128 + 16 * swz_chunk(8 + xr, xc);
   const int r0 = lr * 128 + 16 * swz_chunk(lr, 2 * lq), r1 = lr * 128 + 16 * swz_chunk(lr, 2 * lq + 1);
 
-  struct Stage {
-    u32x4 rb[NJ][2], ra[RT][2];
-    float sb[NJ][GB == FP8Q_GRAN_1x128 ? 4 : 1];
-  };
-  Stage ring[PD];
-  auto load_b = [&](Stage& g, int kb) {
+  u32x4 rb[NJ][2], ra[RT][2];
+  float sbv[NJ][NS];
+  auto load = [&](int kb) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
 #pragma unroll
-      for (int v = 0; v < 2; ++v) g.rb[j][v] = __builtin_nontemporal_load((const u32x4*)(b[j][v] + (int64_t)kb * 128));
-      if constexpr (GB == FP8Q_GRAN_1x128) {
+      for (int v = 0; v < 2; ++v) rb[j][v] = __builtin_nontemporal_load((const u32x4*)(b[j][v] + (int64_t)kb * 128));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) g.sb[j][e] = sb[j][clampn(n0 + 16 * j + 4 * lq + e) * p.sB_sn + kb * p.sB_skb];
-      } else {
-        g.sb[j][0] = sb[j][kb * p.sB_skb];
-      }
+      for (int e = 0; e < NS; ++e)
+        sbv[j][e] = sb[j][(NS == 4 ? clampn(n0 + 16 * j + 4 * lq + e) * p.sB_sn : 0) + kb * p.sB_skb];
     }
-  };
-  auto load_a = [&](Stage& g, int kb) {
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-#pragma unroll
-      for (int v = 0; v < 2; ++v) g.ra[i][v] = *(const u32x4*)(a[i][v] + (int64_t)kb * 128);
-    }
-  };
-  auto load = [&](Stage& g, int kb) {
-    load_b(g, kb);
-    load_a(g, kb);
-  };
-
-  constexpr int CL = kClasses / KS;  // classes CL * ks .. of this wavefront
-  static_assert(CL == 1 || CL == 4 || CL == 8, "the joins below");
-  // the next block of the wavefront: its class's next, or the first of its
-  // next class (nkb: none is left)
-  auto next = [&](int kb) {
-    if (kb + kClasses < nkb) return kb + kClasses;
-    const int c = (kb & (kClasses - 1)) + 1;
-    return c < CL * (ks + 1) && c < nkb ? c : nkb;
-  };
-  v4f acc[RT][NJ], sum[CL == 8 ? 2 : 1][RT][NJ];
-  auto each = [&](auto f) {
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) f(i, j);
+      for (int v = 0; v < 2; ++v) ra[i][v] = *(const u32x4*)(a[i][v] + (int64_t)kb * 128);
   };
-  const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  each([&](int i, int j) {
-    acc[i][j] = zero;
-    sum[0][i][j] = zero;
-    if (CL == 8) sum[CL == 8][i][j] = zero;
-  });
-
-  // One block: its rows go to the exchange tiles, which frees the registers
-  // for the block PD ahead (`ahead` loads it), then the products.
   auto put = [&](const u32x4* raw, int slot) {
     *(u32x4*)(xch + slot * 2048 + w0) = raw[0];
     *(u32x4*)(xch + slot * 2048 + w1) = raw[1];
@@ -162,23 +117,40 @@ __global__ __launch_bounds__(64 * NCG * KS) void k_few(const Proj p) {
     f[2] = dec8<FM, H16>(x1.x, x1.y);
     f[3] = dec8<FM, H16>(x1.z, x1.w);
   };
-  const bool sa_in_lds = nkb <= kScaleBlocks;
-  auto consume = [&](Stage& g, int kb, auto ahead) {
-    float s[RT][NJ][GB == FP8Q_GRAN_1x128 ? 4 : 1];
+
+  const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  v4f acc[RT][NJ];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) put(g.rb[j], j);
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = zero;
+
+  if (wave < nkb) load(wave);
+  const bool sa_in_lds = nkb <= kScaleBlocks;
+  if (sa_in_lds) {
+#pragma unroll 4
+    for (int t = threadIdx.x; t < rows * nkb; t += 64 * kWaves) {
+      const int r = t / nkb, kb = t - r * nkb;
+      sa_lds[kb * SP + r] = p.sA[(m0 + r) * p.sA_sm + kb * p.sA_skb];
+    }
+  }
+  __syncthreads();
+  for (int kb = wave; kb < nkb; kb += kWaves) {
+    float s[RT][NJ][NS];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) put(rb[j], j);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-      put(g.ra[i], NJ + i);
+      put(ra[i], NJ + i);
       const float sai = sa_in_lds ? sa_lds[kb * SP + srow[i]] : sa[i][kb * p.sA_skb];
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
-        for (int e = 0; e < (GB == FP8Q_GRAN_1x128 ? 4 : 1); ++e) s[i][j][e] = sai * g.sb[j][e];
+        for (int e = 0; e < NS; ++e) s[i][j][e] = sai * sbv[j][e];
     }
     // the lanes read each other's rows; the wavefront's LDS accesses run in order
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
-    ahead();
+    if (kb + kWaves < nkb) load(kb + kWaves);
     V8 fb[NJ][4];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) get(j, std::integral_constant<int, FB>{}, fb[j]);
@@ -193,185 +165,83 @@ __global__ __launch_bounds__(64 * NCG * KS) void k_few(const Proj p) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) t = mfma32<H16>(fb[j][k], fa[k], t);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          acc[i][j][e] = __builtin_fmaf(t[e], s[i][j][GB == FP8Q_GRAN_1x128 ? e : 0], acc[i][j][e]);
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(t[e], s[i][j][NS == 4 ? e : 0], acc[i][j][e]);
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");  // read before the next block's rows
-  };
+  }
 
-  int kp = CL * ks;  // the next block to load
-  if (kp > nkb) kp = nkb;
-#pragma unroll
-  for (int u = 0; u < PD; ++u) {
-    if (kp < nkb) {
-      load(ring[u], kp);
-      kp = next(kp);
-    }
-  }
-  if (sa_in_lds) {
-#pragma unroll 4
-    for (int t = threadIdx.x; t < (int)p.M * nkb; t += 64 * NCG * KS) {
-      const int r = t / nkb, kb = t - r * nkb;
-      sa_lds[kb * SP + r] = p.sA[r * p.sA_sm + kb * p.sA_skb];
-    }
-  }
-  __syncthreads();
-  for (int kb = CL * ks; kb < nkb;) {
-#pragma unroll
-    for (int u = 0; u < PD; ++u) {
-      if (kb >= nkb) break;
-      consume(ring[u], kb, [&] {
-        if (kp < nkb) {
-          load(ring[u], kp);
-          kp = next(kp);
-        }
-      });
-      const int nx = next(kb);
-      if constexpr (CL > 1) {
-        if (kb + kClasses >= nkb) {  // the class ends
-          const bool second = CL == 8 && (kb & 4);
-          each([&](int i, int j) {
-            if (second) sum[CL == 8][i][j] = add4(sum[CL == 8][i][j], acc[i][j]);
-            else sum[0][i][j] = add4(sum[0][i][j], acc[i][j]);
-            acc[i][j] = zero;
-          });
-        }
-      }
-      kb = nx;
-    }
-  }
   __syncthreads();  // the exchange tiles become the partial sums
-  v4f(*red)[NCG][RT][NJ][64] = (v4f(*)[NCG][RT][NJ][64])lds;
-  each([&](int i, int j) {
-    red[ks][cg][i][j][lane] = CL == 1 ? acc[i][j] : CL == 4 ? sum[0][i][j] : add4(sum[0][i][j], sum[CL == 8][i][j]);
-  });
+  v4f(*red)[RT][NJ][64] = (v4f(*)[RT][NJ][64])lds;
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) red[wave][i][j][lane] = acc[i][j];
   __syncthreads();
 
-  // wavefront ks of a column group finishes row tiles ks, ks + KS, ...
-  constexpr int IT = (RT + KS - 1) / KS;
-  constexpr int NH = GLU ? 1 : NJ;  // column tiles of the output
-  v4f h[IT][NH];
+  // wavefront i finishes row tile i
+  const int i = wave;
+  const int64_t row = m0 + 16 * i + lr, col = n0 + 4 * lq;
+  if (i >= RT || row >= p.M) return;
+  v4f o[NJ];
 #pragma unroll
-  for (int u = 0; u < IT; ++u) {
-    const int i = u * KS + ks;
-    h[u][0] = zero;
-    if (i >= RT) continue;
-    v4f s[NJ];
+  for (int j = 0; j < NJ; ++j) {
+    o[j] = red[0][i][j][lane];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      v4f o[KS];
+    for (int k = 1; k < kWaves; ++k) {
+      const v4f v = red[k][i][j][lane];
 #pragma unroll
-      for (int k = 0; k < KS; ++k) o[k] = red[k][cg][i][j][lane];
-      if constexpr (KS == 8) {
-#pragma unroll
-        for (int k = 1; k < 4; ++k) o[0] = add4(o[0], o[k]), o[4] = add4(o[4], o[4 + k]);
-        o[0] = add4(o[0], o[4]);
-      } else if constexpr (KS == 2) {
-        o[0] = add4(o[0], o[1]);
-      }
-      s[j] = o[0];
-    }
-    const int64_t row = 16 * i + lr, col = n0 + 4 * lq;
-    const bool in = row < p.M && col < p.N;
-    if constexpr (GLU) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) h[u][0][e] = activation(p.act, s[0][e]) * s[1][e];
-      if (p.gu && in) {
-        uint16_t* g = p.gu + row * p.ldgu + col;
-        const bool vec = ((((uintptr_t)p.gu) | (uintptr_t)(2 * p.ldgu) | (uintptr_t)(2 * p.N)) & 7) == 0;
-        store_row4(g, s[0], p.N - col, vec);
-        store_row4(g + p.N, s[1], p.N - col, vec);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) h[u][j] = s[j];
-    }
-    if constexpr (OUT < 2) {
-      using T = std::conditional_t<OUT == FP8Q_F32, float, uint16_t>;
-      const bool vec = ((((uintptr_t)p.out) | (uintptr_t)(sizeof(T) * p.ldo)) & (4 * sizeof(T) - 1)) == 0;
-      if (row < p.M) {
-#pragma unroll
-        for (int j = 0; j < NH; ++j)
-          if (col + 16 * j < p.N) store_row4((T*)p.out + row * p.ldo + col + 16 * j, h[u][j], p.N - col - 16 * j, vec);
-      }
-    } else {
-      uint32_t m = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) m = max(m, abs_bits(h[u][0][e]));
-      m = max(m, (uint32_t)__shfl_xor((int)m, 16));
-      m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-      if (lq == 0) rmax[cg][16 * i + lr] = m;
+      for (int e = 0; e < 4; ++e) o[j][e] += v[e];
     }
   }
-  if constexpr (OUT >= 2) {
-    static_assert(GLU && NCG == 8, "a workgroup holds the 128 columns of a block");
-    constexpr int QF = OUT - 2;
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < IT; ++u) {
-      const int i = u * KS + ks;
-      if (i >= RT) continue;
-      uint32_t m = 0;
-#pragma unroll
-      for (int c = 0; c < NCG; ++c) m = max(m, rmax[c][16 * i + lr]);
-      const float s = block_scale<QF>(__uint_as_float(canon_abs_bits(m)), p.eps);
-      const float r = 1.0f / s;
-      const int64_t row = 16 * i + lr;
-      if (row >= p.M) continue;
-      const uint32_t w = encode4<QF>(h[u][0][0], h[u][0][1], h[u][0][2], h[u][0][3], s, r, scale_ok(s));
-      uint8_t* dst = (uint8_t*)p.out + row * p.ldo + n0 + 4 * lq;
-      if ((((uintptr_t)p.out | (uintptr_t)p.ldo) & 3) == 0) {
-        *(uint32_t*)dst = w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dst[e] = (uint8_t)(w >> (8 * e));
-      }
-      if (cg == 0 && lq == 0) p.scales[row * p.ld_s + (n0 >> 7)] = s;
+  if constexpr (GLU) {
+    if (p.gu && col < p.N) {
+      uint16_t* g = p.gu + row * p.ldgu + col;
+      const bool vec = ((((uintptr_t)p.gu) | (uintptr_t)(2 * p.ldgu) | (uintptr_t)(2 * p.N)) & 7) == 0;
+      store_row4(g, o[0], p.N - col, vec);
+      store_row4(g + p.N, o[1], p.N - col, vec);
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[0][e] = activation(p.act, o[0][e]) * o[1][e];
   }
+  using T = std::conditional_t<OUT == FP8Q_F32, float, uint16_t>;
+  const bool vec = ((((uintptr_t)p.out) | (uintptr_t)(sizeof(T) * p.ldo)) & (4 * sizeof(T) - 1)) == 0;
+#pragma unroll
+  for (int j = 0; j < (GLU ? 1 : NJ); ++j)
+    if (col + 16 * j < p.N) store_row4((T*)p.out + row * p.ldo + col + 16 * j, o[j], p.N - col - 16 * j, vec);
 }
 
 template <int FA, int FB, int GB, bool GLU, int OUT, int NJ, int RT>
 static void launch_rt(const Proj& p, hipStream_t st) {
-  // codes: 16 wavefronts where their registers suffice
-  #ifndef V_KSQ
-#define V_KSQ 2
-#define V_PDQ 1
-#define V_PD1 1
-#define V_PDN 1
-#endif
-  #ifndef V_NJ
-#define V_NJ 2
-#endif
-  constexpr int NCG = OUT >= 2 ? 8 : 1, KS = OUT < 2 ? 8 : RT == 1 ? V_KSQ : 1, PD = RT == 1 ? (OUT >= 2 ? V_PDQ : V_PD1) : V_PDN;
-  constexpr int COLS = NCG * (GLU ? 16 : 16 * NJ);
-  hipLaunchKernelGGL((k_few<FA, FB, GB, GLU, OUT, NJ, NCG, KS, RT, PD>), dim3((unsigned)((p.N + COLS - 1) / COLS)),
-                     dim3(64 * NCG * KS), 0, st, p);
+  constexpr int COLS = GLU ? 16 : 16 * NJ, ROWS = 16 * RT;
+  hipLaunchKernelGGL((k_few<FA, FB, GB, GLU, OUT, NJ, RT>),
+                     dim3((unsigned)((p.N + COLS - 1) / COLS), (unsigned)((p.M + ROWS - 1) / ROWS)), dim3(64 * kWaves), 0,
+                     st, p);
 }
 
 template <int FA, int FB, int GB, bool GLU, int OUT>
 static void launch_m(const Proj& p, hipStream_t st) {
-  // a plain product of more rows shares each tile of A among 32 columns
+  // a plain product of more than 16 rows shares each tile of A among 32
+  // columns; beyond 64 rows, equal groups of up to 64 each read the weight
+  const int64_t groups = (p.M + 63) / 64, rows = (p.M + groups - 1) / groups;
   if (p.M <= 16) launch_rt<FA, FB, GB, GLU, OUT, GLU ? 2 : 1, 1>(p, st);
-  else if (p.M <= 32) launch_rt<FA, FB, GB, GLU, OUT, 2, 2>(p, st);
-  else if (p.M <= 48) launch_rt<FA, FB, GB, GLU, OUT, 2, 3>(p, st);
+  else if (rows <= 32) launch_rt<FA, FB, GB, GLU, OUT, 2, 2>(p, st);
+  else if (rows <= 48) launch_rt<FA, FB, GB, GLU, OUT, 2, 3>(p, st);
   else launch_rt<FA, FB, GB, GLU, OUT, 2, 4>(p, st);
 }
 
 template <int FA, int FB>
 static void launch_f(const Proj& p, hipStream_t st) {
   constexpr int BLK = FP8Q_GRAN_128x128;
+  const bool f32 = p.out_dt == FP8Q_F32;
   if (p.B1) {
-    if (p.scales && p.fc == FP8Q_E4M3FN) launch_m<FA, FB, BLK, true, 2 + FP8Q_E4M3FN>(p, st);
-    else if (p.scales) launch_m<FA, FB, BLK, true, 2 + FP8Q_E5M2>(p, st);
-    else if (p.out_dt == FP8Q_F32) launch_m<FA, FB, BLK, true, FP8Q_F32>(p, st);
+    if (f32) launch_m<FA, FB, BLK, true, FP8Q_F32>(p, st);
     else launch_m<FA, FB, BLK, true, FP8Q_BF16>(p, st);
   } else if (p.gb == FP8Q_GRAN_1x128) {
-    if (p.out_dt == FP8Q_F32) launch_m<FA, FB, FP8Q_GRAN_1x128, false, FP8Q_F32>(p, st);
+    if (f32) launch_m<FA, FB, FP8Q_GRAN_1x128, false, FP8Q_F32>(p, st);
     else launch_m<FA, FB, FP8Q_GRAN_1x128, false, FP8Q_BF16>(p, st);
   } else {
-    if (p.out_dt == FP8Q_F32) launch_m<FA, FB, BLK, false, FP8Q_F32>(p, st);
+    if (f32) launch_m<FA, FB, BLK, false, FP8Q_F32>(p, st);
     else launch_m<FA, FB, BLK, false, FP8Q_BF16>(p, st);
   }
 }

@@ -118,22 +118,25 @@ int64_t rmsnorm_bwd_parts(int64_t rows, int64_t cols);
 
 // A gated projection (B1 the second matrix, act) or, with B1 null, a plain
 // product; N output columns.  The output is out_dt elements, or codes of
-// format fc with scales when `scales` is given; gu (nullable) gets the
-// pre-activations, [M, 2N] bf16.
+// format fc with scales when `scales` is given (ws: see glu_q_workspace); gu
+// (nullable) gets the pre-activations, [M, 2N] bf16.
 struct Proj {
   const uint8_t *A, *B0, *B1;
   const float *sA, *s0, *s1;
   void* out;
-  float* scales;
+  float *scales, *ws;
   uint16_t* gu;
   int64_t lda, sA_sm, sA_skb, ldb, sB_sn, sB_skb, ldo, ld_s, ldgu, M, N, K;
   float eps;
   int fa, fb, gb, act, out_dt, fc;
 };
-// Rows the few-row kernel takes at most.
+// Rows the product of a few rows takes at most.
 static constexpr int64_t kFewRows = 64;
 int launch_few(const Proj& p, const char* what, hipStream_t st);
 int launch_glu(const Proj& p, bool fast, const char* what, hipStream_t st);
+// Bytes of fp32 workspace the quantized gated projection takes: its output
+// where the few-row kernel makes it, none otherwise.
+int64_t glu_q_workspace(int64_t M, int64_t F);
 
 struct GluBwd {
   const void* dh;

@@ -28,9 +28,9 @@ static constexpr int BK = 128;
 static constexpr int kThreads = 512;
 static constexpr int TJ = 4;
 
-template <bool FAST>
+template <bool FAST, int TI_>
 struct Shape {
-  static constexpr int TI = FAST ? 8 : 4, BM = 32 * TI, NST = FAST ? 2 : 3;
+  static constexpr int TI = TI_, BM = 32 * TI, NST = TI == 8 ? 2 : 3;
   static constexpr int A_STAGE = BM * BK, B_STAGE = 256 * BK;
   static constexpr int LDS = NST * (A_STAGE + B_STAGE);
 };
@@ -84,10 +84,10 @@ __device__ __forceinline__ void drain_tile(const uint8_t* stg, int tid, T* out, 
 }
 
 // OUT: FP8Q_F32, FP8Q_BF16 or 2 + format (1x128 codes).
-template <int FA, int FB, int OUT, bool FAST>
+template <int FA, int FB, int OUT, bool FAST, int TI_>
 __global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, const float* __restrict__ s0,
                                                      const float* __restrict__ s1, int64_t ntm, int64_t ntn) {
-  using S = Shape<FAST>;
+  using S = Shape<FAST, TI_>;
   constexpr int TI = S::TI, BM = S::BM, NST = S::NST;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
   __shared__ __attribute__((aligned(16))) float lds_sa[NST][BM];
@@ -188,10 +188,11 @@ __global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, const float* 
       const uint8_t* la = lds + s * S::A_STAGE + a_row0;
       const uint8_t* lb = lds + B0 + s * S::B_STAGE;
       float cf[TI];
+      const float* lc = lds_sa[s] + wm * TI * 16 + lr * TI;
 #pragma unroll
-      for (int q = 0; q < TI / 4; ++q) {
-        const float4 c4 = *(const float4*)(lds_sa[s] + wm * TI * 16 + lr * TI + 4 * q);
-        cf[4 * q] = c4.x, cf[4 * q + 1] = c4.y, cf[4 * q + 2] = c4.z, cf[4 * q + 3] = c4.w;
+      for (int q = 0; q < TI / 2; ++q) {
+        const float2 c2 = *(const float2*)(lc + 2 * q);
+        cf[2 * q] = c2.x, cf[2 * q + 1] = c2.y;
       }
       float cg[TI], cu[TI];
 #pragma unroll
@@ -309,13 +310,31 @@ __global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, const float* 
     __syncthreads();
     int st = 0;
     int64_t kb = 0;
-    if constexpr (FAST) {
+    if constexpr (FAST && NST == 2) {
       for (; kb + 1 < nkb; ++kb) {
         stage_block(kb + 1, next_stage(st));
         compute(kb, st, PF0{}, 0, true);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
         st = next_stage(st);
+      }
+    } else if constexpr (FAST) {
+      // two blocks in flight: block kb + 2 goes into the stage that block
+      // kb - 1 left at the last barrier
+      for (; kb + 2 < nkb; ++kb) {
+        const int s1 = next_stage(st);
+        stage_block(kb + 2, next_stage(s1));
+        compute(kb, st, PF0{}, 0, true);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NW) : "memory");
+        __syncthreads();
+        st = s1;
+      }
+      if (kb + 1 < nkb) {
+        compute(kb, st, PF0{}, 0, true);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+        st = next_stage(st);
+        ++kb;
       }
     } else {
       auto dec32 = [&](const uint8_t* base, auto fmt, V8* out) {
@@ -419,38 +438,77 @@ __global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, const float* 
   }
 }
 
-template <int FA, int FB, int OUT, bool FAST>
+template <int FA, int FB, int OUT, bool FAST, int TI>
 static void launch_t(const Proj& p, hipStream_t st) {
-  const int64_t ntm = (p.M + Shape<FAST>::BM - 1) / Shape<FAST>::BM, ntn = (p.N + 127) / 128;
+  const int64_t ntm = (p.M + 32 * TI - 1) / (32 * TI), ntn = (p.N + 127) / 128;
   // one workgroup per compute unit, a multiple of eight so that a
   // workgroup's tiles stay on its XCD
   int64_t g = device_cu_count() / 8 * 8;
   if (g < 8) g = 8;
   if (ntm * ntn < g) g = ntm * ntn;
-  hipLaunchKernelGGL((k_glu<FA, FB, OUT, FAST>), dim3((unsigned)g), dim3(kThreads), 0, st, p, p.s0, p.s1,
-                     ntm, ntn);
+  hipLaunchKernelGGL((k_glu<FA, FB, OUT, FAST, TI>), dim3((unsigned)g), dim3(kThreads), 0, st, p, p.s0, p.s1, ntm, ntn);
+}
+
+template <int FA, int FB, int OUT, bool FAST>
+static void launch_h(const Proj& p, bool tall, hipStream_t st) {
+  if (tall) launch_t<FA, FB, OUT, FAST, FAST ? 8 : 4>(p, st);
+  else launch_t<FA, FB, OUT, FAST, FAST ? 4 : 2>(p, st);
 }
 
 template <int FA, int FB>
-static void launch_f(const Proj& p, bool fast, hipStream_t st) {
+static void launch_f(const Proj& p, bool fast, bool tall, hipStream_t st) {
   if (p.scales) {
-    if (p.fc == FP8Q_E4M3FN) launch_t<FA, FB, 2 + FP8Q_E4M3FN, false>(p, st);
-    else launch_t<FA, FB, 2 + FP8Q_E5M2, false>(p, st);
+    if (p.fc == FP8Q_E4M3FN) launch_h<FA, FB, 2 + FP8Q_E4M3FN, false>(p, tall, st);
+    else launch_h<FA, FB, 2 + FP8Q_E5M2, false>(p, tall, st);
   } else if (fast) {
-    if (p.out_dt == FP8Q_F32) launch_t<FA, FB, FP8Q_F32, true>(p, st);
-    else launch_t<FA, FB, FP8Q_BF16, true>(p, st);
+    if (p.out_dt == FP8Q_F32) launch_h<FA, FB, FP8Q_F32, true>(p, tall, st);
+    else launch_h<FA, FB, FP8Q_BF16, true>(p, tall, st);
   } else {
-    if (p.out_dt == FP8Q_F32) launch_t<FA, FB, FP8Q_F32, false>(p, st);
-    else launch_t<FA, FB, FP8Q_BF16, false>(p, st);
+    if (p.out_dt == FP8Q_F32) launch_h<FA, FB, FP8Q_F32, false>(p, tall, st);
+    else launch_h<FA, FB, FP8Q_BF16, false>(p, tall, st);
   }
 }
 
+// Which kernel a call takes, in units of a thousandth of a microsecond per K
+// block (the fixed few microseconds are alike), from the sizes alone:
+//   * tiles: one round of up to a tile per compute unit takes 1.4 us (256 rows
+//     FP8-MFMA, 128 exact) or 0.85 us (half the rows) a block while few units
+//     work and 1.7 and 1.05 when all do; rounds x that, the lower of the two.
+//     M = 512, F = 18432, K = 7168 fast: 195 (2 rounds) against 185 us (3);
+//     M = 1023: 285 (3) against 304 us (5).
+//   * few rows: a workgroup of 16 columns and up to 64 rows takes
+//     0.12 + 0.058 per 16 rows; workgroups per compute unit (at least one) x
+//     that.  F = 4096, K = 4096: 10 us at 16 rows and 25 us at 128 against 30
+//     on tiles, 48 against 31 us at 256; F = 18432, K = 7168: 45 us at 16 rows
+//     and 65 us at 32 against 60 and 62 us.
+struct Plan {
+  bool few, tall;
+};
+static Plan plan(int64_t M, int64_t F, bool fast) {
+  const int64_t cu = device_cu_count(), bm = fast ? 256 : 128, ntn = (F + 127) / 128;
+  auto rounds = [&](int64_t rows) { return ((M + rows - 1) / rows * ntn + cu - 1) / cu; };
+  const int64_t tall = 1360 * rounds(bm), low = 850 * rounds(bm / 2);
+  const int64_t groups = (M + 63) / 64, tiles = ((M + groups - 1) / groups + 15) / 16;
+  int64_t wgs = groups * ((F + 15) / 16);
+  if (wgs < cu) wgs = cu;
+  return {wgs * (120 + 58 * tiles) < (tall < low ? tall : low) * cu, tall <= low};
+}
+
+int64_t glu_q_workspace(int64_t M, int64_t F) { return plan(M, F, false).few ? 4 * M * F : 0; }
+
 int launch_glu(const Proj& p, bool fast, const char* what, hipStream_t st) {
-  if (p.M <= kFewRows) return launch_few(p, what, st);
-  if (p.fa == FP8Q_E4M3FN && p.fb == FP8Q_E4M3FN) launch_f<0, 0>(p, fast, st);
-  else if (p.fa == FP8Q_E5M2 && p.fb == FP8Q_E4M3FN) launch_f<1, 0>(p, fast, st);
-  else if (p.fa == FP8Q_E4M3FN) launch_f<0, 1>(p, fast, st);
-  else launch_f<1, 1>(p, fast, st);
+  const Plan pl = plan(p.M, p.N, fast);
+  if (pl.few && p.scales) {
+    Proj h = p;
+    h.out = p.ws, h.ldo = p.N, h.out_dt = FP8Q_F32, h.scales = nullptr;
+    if (int rc = launch_few(h, what, st)) return rc;
+    return launch_quantize_1x128(p.ws, FP8Q_F32, p.M, p.N, p.N, p.fc, p.eps, (uint8_t*)p.out, p.ldo, p.scales, p.ld_s, st);
+  }
+  if (pl.few) return launch_few(p, what, st);
+  if (p.fa == FP8Q_E4M3FN && p.fb == FP8Q_E4M3FN) launch_f<0, 0>(p, fast, pl.tall, st);
+  else if (p.fa == FP8Q_E5M2 && p.fb == FP8Q_E4M3FN) launch_f<1, 0>(p, fast, pl.tall, st);
+  else if (p.fa == FP8Q_E4M3FN) launch_f<0, 1>(p, fast, pl.tall, st);
+  else launch_f<1, 1>(p, fast, pl.tall, st);
   return check_launch(what);
 }
 

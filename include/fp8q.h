@@ -425,12 +425,20 @@ int fp8q_glu_blockscaled_fast(const uint8_t* A, fp8q_format fa, int64_t lda, con
 /* fp8q_glu_blockscaled with H as 1x128 codes of format fc, the input of the
  * down projection: bit for bit what fp8q_quantize_1x128 makes of its fp32 H.
  * Hq: M x F codes (ldhq >= F), Hs: [M, F/128] fp32 (ld_hs >= F/128); eps the
- * amax clamp.  F % 128 == 0 as well (else FP8Q_ESHAPE). */
+ * amax clamp.  F % 128 == 0 as well (else FP8Q_ESHAPE); Hq and its rows 4-B
+ * aligned.  ws: ws_bytes >= fp8q_glu_blockscaled_q_workspace, 16-B aligned,
+ * overwritten; NULL where that is 0.  Calls in flight must not share it. */
 int fp8q_glu_blockscaled_q(const uint8_t* A, fp8q_format fa, int64_t lda, const float* sA, int64_t sA_sm,
                            int64_t sA_skb, const uint8_t* Bg, const uint8_t* Bu, fp8q_format fb, int64_t ldb,
                            const float* sBg, const float* sBu, int64_t sB_sn, int64_t sB_skb, fp8q_act act,
                            fp8q_format fc, float eps, uint8_t* Hq, int64_t ldhq, float* Hs, int64_t ld_hs,
-                           uint16_t* gu, int64_t ldgu, int64_t M, int64_t F, int64_t K, void* stream);
+                           uint16_t* gu, int64_t ldgu, int64_t M, int64_t F, int64_t K, void* ws, int64_t ws_bytes,
+                           void* stream);
+
+/* Bytes of workspace fp8q_glu_blockscaled_q needs: 4*M*F for a few rows, whose
+ * output is quantized by a second launch, 0 for more (and for sizes it
+ * refuses). */
+int64_t fp8q_glu_blockscaled_q_workspace(int64_t M, int64_t F);
 
 /* Gradient of the gated projection at its pre-activations, quantized for the
  * products that follow, with H recomputed:

@@ -78,15 +78,25 @@ def test_glu_refusals(fq, name, kw, status):
 
 
 GLU_Q = dict(A=FAKE, fa=0, lda=256, sA=FAKE, sm=2, skb=1, Bg=FAKE, Bu=FAKE, fb=0, ldb=256, sBg=FAKE, sBu=FAKE, sn=2, sk=1,
-             act=1, fc=0, eps=1e-12, Hq=FAKE, ldhq=128, Hs=FAKE, ld_hs=1, gu=None, ldgu=0, M=40, F=128, K=256, stream=None)
+             act=1, fc=0, eps=1e-12, Hq=FAKE, ldhq=128, Hs=FAKE, ld_hs=1, gu=None, ldgu=0, M=40, F=128, K=256, ws=FAKE,
+             ws_bytes=4 * 40 * 128, stream=None)
 
 
 @pytest.mark.parametrize("kw,status", [(k if "ldgu" not in k else dict(gu=FAKE, **k), s) for k, s in GLU_BAD] + [
     (dict(Hq=None), "EINVAL"), (dict(Hs=None), "EINVAL"), (dict(fc=2), "EINVAL"), (dict(eps=-1.0), "EINVAL"),
-    (dict(F=100), "ESHAPE"), (dict(ldhq=100), "EINVAL"), (dict(ld_hs=0), "EINVAL"), (dict(Hs=FAKE + 2), "EALIGN")])
+    (dict(F=100), "ESHAPE"), (dict(ldhq=100), "EINVAL"), (dict(ld_hs=0), "EINVAL"), (dict(Hs=FAKE + 2), "EALIGN"),
+    (dict(ws=None), "EINVAL"), (dict(ws_bytes=4 * 40 * 128 - 1), "EINVAL"), (dict(ws=FAKE + 8), "EALIGN"),
+    (dict(Hq=FAKE + 2), "EALIGN"), (dict(ldhq=130), "EALIGN")])
 def test_glu_q_refusals(fq, kw, status):
     rc, msg = _call(fq, "fp8q_glu_blockscaled_q", GLU_Q, {**dict(gu=None), **kw} if "gu" not in kw else {"ldgu": 256, **kw})
     assert rc == getattr(fq, status) and msg.startswith("glu_blockscaled_q"), (rc, msg)
+
+
+def test_glu_q_workspace(fq):
+    assert fq.fp8q_glu_blockscaled_q_workspace(1, 18432) == 4 * 18432
+    assert fq.fp8q_glu_blockscaled_q_workspace(16384, 18432) == 0
+    for bad in ((0, 128), (1, 0), (1, 130)):
+        assert fq.fp8q_glu_blockscaled_q_workspace(*bad) == 0
 
 
 GLU_BWD = dict(dH=FAKE, dt=1, lddh=128, gu=FAKE, ldgu=256, act=0, fc=1, eps=1e-12, Dq=FAKE, lddq=256, Ds=FAKE, ld_ds=2,

@@ -330,11 +330,11 @@ def test_glu_halves_of_one_matrix_and_scale_strides(fq, gpu):
         assert torch.equal(h, want)
 
 
-def test_glu_many_tiles(fq, orc, gpu):
-    """More tiles than compute units, a ragged edge both ways, checked on sampled rows."""
-    M, F, K = 2305, 4000, 256
+@pytest.mark.parametrize("M,F,K", [(2305, 4000, 256), (1025, 6100, 384), (1281, 18400, 128)])
+def test_glu_many_tiles(fq, orc, gpu, M, F, K):
+    """Up to several tiles per compute unit, of either height, a ragged edge both ways, checked on sampled rows."""
     A, sA, B, sB = operands(gpu, M, F, K, seed=4)
-    rows = np.array([0, 1, 127, 128, 255, 256, 1000, 2047, 2048, 2303, 2304])
+    rows = np.array([r for r in (0, 1, 127, 128, 255, 256, 1000, 1024, 1279, 1280, 2047, 2048, 2303, 2304) if r < M])
     for fn, rel in (("fp8q_glu_blockscaled", 1e-5), ("fp8q_glu_blockscaled_fast", 2.0 ** -10)):
         h = torch.full((M, F), 7.0, device=gpu)
         glu_call(fq, fn, A, E4, sA, B, E4, sB, 0, h, None, M, F, K)
