@@ -151,25 +151,38 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
-def _dt(t) -> int:
-    import torch
+_DTYPES: dict = {}  # torch's dtypes, filled by the first call (torch is imported only then)
 
-    if t.dtype == torch.float32:
-        return F32
-    if t.dtype == torch.bfloat16:
-        return BF16
-    raise TypeError(f"fp8q inputs are float32 or bfloat16, got {t.dtype}")
+
+def _dt(t) -> int:
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        import torch
+
+        _DTYPES.update({torch.float32: F32, torch.bfloat16: BF16})
+        d = _DTYPES.get(t.dtype)
+        if d is None:
+            raise TypeError(f"fp8q inputs are float32 or bfloat16, got {t.dtype}")
+    return d
+
+
+_raw_stream = None
 
 
 def _stream(stream, t=None) -> int | None:
+    global _raw_stream
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
+    if t is not None and not isinstance(t, int) and t.is_cuda:
+        # the handle alone: building a Stream object takes longer than a small launch
+        if _raw_stream is None:
+            import torch
+
+            _raw_stream = torch._C._cuda_getCurrentRawStream
+        return _raw_stream(t.get_device())
     import torch
 
     dev = t.device if (t is not None and not isinstance(t, int)) else None
-    if dev is not None and dev.type == "cuda":
-        # the handle alone: building a Stream object takes longer than a small launch
-        return torch._C._cuda_getCurrentRawStream(dev.index)
     return torch.cuda.current_stream(dev).cuda_stream
 
 

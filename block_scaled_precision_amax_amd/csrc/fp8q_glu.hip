@@ -83,8 +83,10 @@ __device__ __forceinline__ void drain_tile(const uint8_t* stg, int tid, T* out, 
   }
 }
 
-// OUT: FP8Q_F32, FP8Q_BF16 or 2 + format (1x128 codes).
-template <int FA, int FB, int OUT, bool FAST, int TI_>
+// OUT: FP8Q_F32, FP8Q_BF16 or 2 + format (1x128 codes).  GLU false: a plain
+// product, whose tiles are 256 columns of one matrix (B1 and its scales are
+// B0's, 128 columns on).
+template <int FA, int FB, int OUT, bool FAST, int TI_, bool GLU>
 __global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, const float* __restrict__ s0,
                                                      const float* __restrict__ s1, int64_t ntm, int64_t ntn) {
   using S = Shape<FAST, TI_>;
@@ -105,7 +107,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, const float* 
     const int wm = wave >> 2, wn = wave & 3;
     int64_t tm, tn;
     tile_of(tile, ntiles, ntm, ntn, tm, tn);
-    const int64_t m0 = tm * BM, n0 = tn * 128;
+    const int64_t m0 = tm * BM, n0 = tn * (GLU ? 128 : 256);
 
     // Copies: a copy stalls the wavefront that issues it, so wavefronts 0-3
     // issue all of them and 4-7, on the same SIMDs, go on with MFMAs.
@@ -114,7 +116,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, const float* 
     // eight-row piece fills slot l % 8 of row l / 8.  Rows past an edge read
     // the last row (their results are never stored).
     constexpr int NA = BM / 64, SAL = BM / 8;
-    uint32_t a_off[2][NA], b_off[4];
+    uint32_t a_off[2][NA], b_off[4], b_off1[4];
     auto off = [&](int64_t r0, int r, int64_t rows, int64_t ld) {
       const int64_t g = r0 + r < rows ? r0 + r : rows - 1;
       return (uint32_t)(g * ld + 16 * swz_chunk(r, lane & 7));
@@ -125,7 +127,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, const float* 
       for (int q = 0; q < NA; ++q)
         a_off[h][q] = off(m0, (((wave & 3) + 4 * h) * NA + q) * 8 + (lane >> 3), M, p.lda);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) b_off[q] = off(n0, ((wave & 3) * 4 + q) * 8 + (lane >> 3), N, p.ldb);
+    for (int q = 0; q < 4; ++q) {
+      b_off[q] = off(n0, ((wave & 3) * 4 + q) * 8 + (lane >> 3), N, p.ldb);
+      b_off1[q] = GLU ? b_off[q] : off(n0 + 128, ((wave & 3) * 4 + q) * 8 + (lane >> 3), N, p.ldb);
+    }
     // A scales in the order the lanes read them: slot h*16TI + lr*TI + i
     // holds row h*16TI + 16i + lr
     const float* sa_row[2];
@@ -148,7 +153,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, const float* 
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         lds_dma16(__builtin_amdgcn_readfirstlane(lb + (wave * 4 + q) * 1024), g, b_off[q]);
-        lds_dma16(__builtin_amdgcn_readfirstlane(lb + (16 + wave * 4 + q) * 1024), u, b_off[q]);
+        lds_dma16(__builtin_amdgcn_readfirstlane(lb + (16 + wave * 4 + q) * 1024), u, b_off1[q]);
       }
       if (lane < SAL) {
 #pragma unroll
@@ -170,7 +175,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, const float* 
     // are read by scalar loads (restrict arguments): a vector load here would
     // wait for every copy in flight
     const float* sg = s0 + (n0 >> 7) * p.sB_sn;
-    const float* su = s1 + (n0 >> 7) * p.sB_sn;
+    const int64_t nu = GLU ? n0 : n0 + 128 < N ? n0 + 128 : N - 1;
+    const float* su = s1 + (nu >> 7) * p.sB_sn;
 
     constexpr bool H16 = FA == FP8Q_E5M2 || FB == FP8Q_E5M2;
     using V8 = typename Op<H16>::v8;
@@ -367,7 +373,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, const float* 
     __syncthreads();
     auto gate = [&](int i, int j) { return acc[i][j]; };
     auto up = [&](int i, int j) { return acc[i][j + 2]; };
-    if (p.gu) {
+    if (GLU && p.gu) {
       stage_tile<uint16_t, TI>(lds, wm, wn, lr, lq, gate);
       stage_tile<uint16_t, TI>(lds + BM * 256, wm, wn, lr, lq, up);
       __syncthreads();
@@ -375,20 +381,25 @@ __global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, const float* 
       drain_tile<uint16_t, BM>(lds + BM * 256, tid, p.gu + N, p.ldgu, m0, n0, M, N);
       __syncthreads();
     }
+    if constexpr (GLU) {
 #pragma unroll
-    for (int i = 0; i < TI; ++i)
+      for (int i = 0; i < TI; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = activation(p.act, acc[i][j][e]) * acc[i][j + 2][e];
-    if constexpr (OUT == FP8Q_F32) {
-      stage_tile<float, TI>(lds, wm, wn, lr, lq, gate);
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = activation(p.act, acc[i][j][e]) * acc[i][j + 2][e];
+    }
+    if constexpr (OUT < 2) {
+      using T = std::conditional_t<OUT == FP8Q_F32, float, uint16_t>;
+      stage_tile<T, TI>(lds, wm, wn, lr, lq, gate);
       __syncthreads();
-      drain_tile<float, BM>(lds, tid, (float*)p.out, p.ldo, m0, n0, M, N);
-    } else if constexpr (OUT == FP8Q_BF16) {
-      stage_tile<uint16_t, TI>(lds, wm, wn, lr, lq, gate);
-      __syncthreads();
-      drain_tile<uint16_t, BM>(lds, tid, (uint16_t*)p.out, p.ldo, m0, n0, M, N);
+      drain_tile<T, BM>(lds, tid, (T*)p.out, p.ldo, m0, n0, M, N);
+      if constexpr (!GLU) {
+        __syncthreads();
+        stage_tile<T, TI>(lds, wm, wn, lr, lq, up);
+        __syncthreads();
+        drain_tile<T, BM>(lds, tid, (T*)p.out, p.ldo, m0, n0 + 128, M, N);
+      }
     } else {
       // a row's 128 columns lie in four wavefronts: their maxima meet in LDS
       constexpr int QF = OUT - 2;
@@ -438,15 +449,16 @@ __global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, const float* 
   }
 }
 
-template <int FA, int FB, int OUT, bool FAST, int TI>
+template <int FA, int FB, int OUT, bool FAST, int TI, bool GLU = true>
 static void launch_t(const Proj& p, hipStream_t st) {
-  const int64_t ntm = (p.M + 32 * TI - 1) / (32 * TI), ntn = (p.N + 127) / 128;
+  const int64_t ntm = (p.M + 32 * TI - 1) / (32 * TI), ntn = GLU ? (p.N + 127) / 128 : (p.N + 255) / 256;
   // one workgroup per compute unit, a multiple of eight so that a
   // workgroup's tiles stay on its XCD
   int64_t g = device_cu_count() / 8 * 8;
   if (g < 8) g = 8;
   if (ntm * ntn < g) g = ntm * ntn;
-  hipLaunchKernelGGL((k_glu<FA, FB, OUT, FAST, TI>), dim3((unsigned)g), dim3(kThreads), 0, st, p, p.s0, p.s1, ntm, ntn);
+  hipLaunchKernelGGL((k_glu<FA, FB, OUT, FAST, TI, GLU>), dim3((unsigned)g), dim3(kThreads), 0, st, p, p.s0, p.s1, ntm,
+                     ntn);
 }
 
 template <int FA, int FB, int OUT, bool FAST>
@@ -484,10 +496,13 @@ static void launch_f(const Proj& p, bool fast, bool tall, hipStream_t st) {
 struct Plan {
   bool few, tall;
 };
+static int64_t tile_rounds(int64_t M, int64_t rows, int64_t ntn) {
+  const int64_t cu = device_cu_count();
+  return ((M + rows - 1) / rows * ntn + cu - 1) / cu;
+}
 static Plan plan(int64_t M, int64_t F, bool fast) {
   const int64_t cu = device_cu_count(), bm = fast ? 256 : 128, ntn = (F + 127) / 128;
-  auto rounds = [&](int64_t rows) { return ((M + rows - 1) / rows * ntn + cu - 1) / cu; };
-  const int64_t tall = 1360 * rounds(bm), low = 850 * rounds(bm / 2);
+  const int64_t tall = 1360 * tile_rounds(M, bm, ntn), low = 850 * tile_rounds(M, bm / 2, ntn);
   const int64_t groups = (M + 63) / 64, tiles = ((M + groups - 1) / groups + 15) / 16;
   int64_t wgs = groups * ((F + 15) / 16);
   if (wgs < cu) wgs = cu;
@@ -509,6 +524,30 @@ int launch_glu(const Proj& p, bool fast, const char* what, hipStream_t st) {
   else if (p.fa == FP8Q_E5M2 && p.fb == FP8Q_E4M3FN) launch_f<1, 0>(p, fast, pl.tall, st);
   else if (p.fa == FP8Q_E4M3FN) launch_f<0, 1>(p, fast, pl.tall, st);
   else launch_f<1, 1>(p, fast, pl.tall, st);
+  return check_launch(what);
+}
+
+// The block-scaled FP8-MFMA product on 128-row tiles, for sizes that leave
+// 256-row tiles few or uneven rounds (the gradients' products of a
+// micro-batch: 1000 x 4096 x 8192 has 64 of those).  The same instructions in
+// the same order per element, so the same bits.
+bool gemm_fast_low(int64_t M, int64_t N) {
+  const int64_t ntn = (N + 255) / 256;
+  return 850 * tile_rounds(M, 128, ntn) < 1360 * tile_rounds(M, 256, ntn);
+}
+
+template <int FA, int FB>
+static void launch_low(const Proj& p, hipStream_t st) {
+  if (p.out_dt == FP8Q_F32) launch_t<FA, FB, FP8Q_F32, true, 4, false>(p, st);
+  else launch_t<FA, FB, FP8Q_BF16, true, 4, false>(p, st);
+}
+
+int launch_gemm_fast_low(Proj p, const char* what, hipStream_t st) {
+  p.B1 = p.B0, p.s1 = p.s0;
+  if (p.fa == FP8Q_E4M3FN && p.fb == FP8Q_E4M3FN) launch_low<0, 0>(p, st);
+  else if (p.fa == FP8Q_E5M2 && p.fb == FP8Q_E4M3FN) launch_low<1, 0>(p, st);
+  else if (p.fa == FP8Q_E4M3FN) launch_low<0, 1>(p, st);
+  else launch_low<1, 1>(p, st);
   return check_launch(what);
 }
 

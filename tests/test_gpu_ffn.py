@@ -381,6 +381,20 @@ def test_few(fq, orc, gpu, M, N, K):
     assert (C[:, N:] == 7).all() and torch.equal(Cb, C[:, :N].bfloat16())
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 1, 128), (100, 300, 256), (129, 4096, 384), (1000, 2200, 640)])
+@pytest.mark.parametrize("fa", [E4, E5])
+def test_fast_product_is_the_same_on_either_tile(fq, gpu, M, N, K, fa):
+    """The FP8-MFMA product of few tiles runs on 128-row tiles; its rows are, bit for bit, those of a product with so many
+    rows that it runs on 256-row tiles."""
+    big = 256 * (256 // -(-N // 256))  # rows that make one round of 256-row tiles, two of 128-row ones
+    A, sA, B, sB = operands(gpu, max(M, big - 99), N, K, fa, seed=N)
+    for dt in (torch.float32, torch.bfloat16):
+        C, D = torch.full((M, N + 5), 7.0, dtype=dt, device=gpu), torch.empty(A.shape[0], N, dtype=dt, device=gpu)
+        for out, rows, ld in ((C, M, N + 5), (D, A.shape[0], N)):
+            fq.fp8q_gemm_blockscaled_fast(A, fa, K, sA, K // 128, 1, B[0], E4, K, sB[0], 2, K // 128, 1, out, ld, rows, N, K)
+        assert torch.equal(C[:, :N], D[:M]) and (C[:, N:] == 7).all()
+
+
 # ------------------------------------------------------------------ gradient of the gated projection
 def bwd_call(fq, dh, gu, act, fc, fh, M, F, want_t=True, want_h=True, pad=0, stream=None):
     dev, Mp = dh.device, -(-M // 128) * 128
