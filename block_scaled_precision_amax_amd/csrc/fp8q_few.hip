@@ -28,8 +28,6 @@
 // 12).
 #include "fp8q_mfma.h"
 
-#include <type_traits>
-
 namespace fp8q {
 
 using namespace ffn;
@@ -201,8 +199,10 @@ __global__ __launch_bounds__(64 * kWaves) void k_few(const Proj p) {
       store_row4(g, o[0], p.N - col, vec);
       store_row4(g + p.N, o[1], p.N - col, vec);
     }
+    with_activation(p.act, [&](auto act) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[0][e] = activation(p.act, o[0][e]) * o[1][e];
+      for (int e = 0; e < 4; ++e) o[0][e] = activation<decltype(act)::value>(o[0][e]) * o[1][e];
+    });
   }
   using T = std::conditional_t<OUT == FP8Q_F32, float, uint16_t>;
   const bool vec = ((((uintptr_t)p.out) | (uintptr_t)(sizeof(T) * p.ldo)) & (4 * sizeof(T) - 1)) == 0;

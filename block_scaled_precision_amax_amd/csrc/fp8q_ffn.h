@@ -18,35 +18,49 @@ __device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v2f{a, b}, v2bf));
 }
 
-// Four values -> four codes of a 1x128 block with scale s, the arithmetic of
-// fp8q_quantize_1x128 on fp32 input: the correctly rounded quotient from
-// r = 1/s while s lies in [2^-80, 2^80] (`fast`), IEEE division otherwise.
-// A block that holds a NaN has a NaN scale and takes the second form (0x7F);
-// one that holds an Inf has an Inf scale, and its finite values become 0.
+// Four values -> four codes of a 1x128 block with the block's own scale s,
+// the arithmetic of fp8q_quantize_1x128 on fp32 input: the correctly rounded
+// quotient from r = 1/s while s lies in [2^-80, 2^80] (`fast`), IEEE division
+// otherwise.  The first needs no saturation: no value passes the block's
+// maximum, whose quotient is at most MAX and one fp32 rounding.  A block that
+// holds a NaN has a NaN scale and takes the second form (0x7F); one that
+// holds an Inf has an Inf scale, and its finite values become 0.
 template <int FMT>
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float s, float r, bool fast) {
-  if (fast)
-    return pack4<FMT>(sat<FMT>(div_rn(a, s, r)), sat<FMT>(div_rn(b, s, r)), sat<FMT>(div_rn(c, s, r)),
-                      sat<FMT>(div_rn(d, s, r)));
+  if (fast) return pack4<FMT>(div_rn(a, s, r), div_rn(b, s, r), div_rn(c, s, r), div_rn(d, s, r));
   return enc1<FMT>(a / s) | (enc1<FMT>(b / s) << 8) | (enc1<FMT>(c / s) << 16) | (enc1<FMT>(d / s) << 24);
+}
+
+// block_scale without the division's long form: MAX is 7 * 2^6 or 7 * 2^13,
+// so fl32(m / MAX) is the quotient by 7, corrected as in div_rn, times a power
+// of two, wherever neither leaves the normal range; NaN, Inf and extreme
+// maxima take the division.
+template <int FMT>
+__device__ __forceinline__ float block_scale7(float amax, float eps) {
+  const float m = (amax < eps) ? eps : amax;
+  if (m >= 0x1p-80f && m <= 0x1p100f) return div_rn(m, 7.0f, 1.0f / 7.0f) * (7.0f / max_finite(FMT));
+  return m / max_finite(FMT);
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
-// Eight consecutive elements of a row as fp32.
+// Eight elements of a row as loaded, and as fp32.
 template <int DT>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
-  if constexpr (DT == FP8Q_F32) {
-    const u32x4* q = (const u32x4*)((const float*)p + i);
-    const u32x4 a = __builtin_nontemporal_load(q), b = __builtin_nontemporal_load(q + 1);
+struct Raw8 {
+  u32x4 v[DT == FP8Q_F32 ? 2 : 1];
+  template <bool STREAM = true>
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    const u32x4* q = (const u32x4*)((const char*)p + i * (DT == FP8Q_F32 ? 4 : 2));
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(a[e]), v[4 + e] = __uint_as_float(b[e]);
-  } else {
-    const u32x4 a = __builtin_nontemporal_load((const u32x4*)((const uint16_t*)p + i));
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[2 * e] = bf_lo(a[e]), v[2 * e + 1] = bf_hi(a[e]);
+    for (int k = 0; k < (DT == FP8Q_F32 ? 2 : 1); ++k) v[k] = STREAM ? __builtin_nontemporal_load(q + k) : q[k];
   }
-}
+  __device__ __forceinline__ float operator[](int e) const {
+    if constexpr (DT == FP8Q_F32) return __uint_as_float(v[e >> 2][e & 3]);
+    else return e & 1 ? bf_hi(v[0][e >> 1]) : bf_lo(v[0][e >> 1]);
+  }
+};
+
+// Eight fp32 values into a row, rounded to its type.
 template <int DT>
 __device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) {
   if constexpr (DT == FP8Q_F32) {

@@ -18,8 +18,6 @@
 // folded into fp32 accumulators with one FMA per element.
 #include "fp8q_mfma.h"
 
-#include <type_traits>
-
 namespace fp8q {
 
 using namespace ffn;
@@ -382,12 +380,15 @@ __global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, const float* 
       __syncthreads();
     }
     if constexpr (GLU) {
+      with_activation(p.act, [&](auto act) {
 #pragma unroll
-      for (int i = 0; i < TI; ++i)
+        for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = activation(p.act, acc[i][j][e]) * acc[i][j + 2][e];
+            for (int e = 0; e < 4; ++e)
+              acc[i][j][e] = activation<decltype(act)::value>(acc[i][j][e]) * acc[i][j + 2][e];
+      });
     }
     if constexpr (OUT < 2) {
       using T = std::conditional_t<OUT == FP8Q_F32, float, uint16_t>;
@@ -419,7 +420,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, const float* 
       for (int i = 0; i < TI; ++i) {
         const int r = (wm * TI + i) * 16 + lr;
         const uint32_t m = max(max(lds_rmax[0][r], lds_rmax[1][r]), max(lds_rmax[2][r], lds_rmax[3][r]));
-        const float s = block_scale<QF>(__uint_as_float(canon_abs_bits(m)), p.eps);
+        const float s = block_scale7<QF>(__uint_as_float(canon_abs_bits(m)), p.eps);
         const float inv = 1.0f / s;
         if (wn == 0 && lq == 0 && m0 + r < M) p.scales[(m0 + r) * p.ld_s + (n0 >> 7)] = s;
 #pragma unroll

@@ -33,7 +33,7 @@ template <int DH, int FC, int FH>
 __global__ __launch_bounds__(512, 4) void k_glu_bwd(const GluBwd p) {
   __shared__ __attribute__((aligned(16))) uint32_t tile[3][128 * 32];
   __shared__ uint32_t cmax[3][8][128];
-  __shared__ __attribute__((aligned(16))) float cs[3][128];
+  __shared__ float2 cs[3][128];  // a column's scale and its reciprocal
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int cl = tid & 15, rg = tid >> 4;
@@ -42,27 +42,27 @@ __global__ __launch_bounds__(512, 4) void k_glu_bwd(const GluBwd p) {
   const int64_t col = f0 + 8 * cl;
 
   float v[3][4][8];  // dg, du, h
+  with_activation(p.act, [&](auto act) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int64_t row = m0 + 4 * rg + q;
-    if (row < p.M) {
-      float dh[8], g[8], u[8];
-      load8<DH>(p.dh, row * p.lddh + col, dh);
-      load8<FP8Q_BF16>(p.gu, row * p.ldgu + col, g);
-      load8<FP8Q_BF16>(p.gu, row * p.ldgu + p.F + col, u);
+    for (int q = 0; q < 4; ++q) {
+      // rows past M read the last one, and their values count as zero
+      const bool in = m0 + 4 * rg + q < p.M;
+      const int64_t row = in ? m0 + 4 * rg + q : p.M - 1;
+      Raw8<DH> dh;
+      Raw8<FP8Q_BF16> g, u;
+      dh.load(p.dh, row * p.lddh + col);
+      g.load(p.gu, row * p.ldgu + col);
+      u.load(p.gu, row * p.ldgu + p.F + col);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         float da;
-        const float a = activation<true>(p.act, g[e], da);
-        v[0][q][e] = dh[e] * u[e] * da;
-        v[1][q][e] = dh[e] * a;
-        v[2][q][e] = a * u[e];
+        const float a = activation<decltype(act)::value, true>(g[e], da);
+        v[0][q][e] = in ? dh[e] * u[e] * da : 0.0f;
+        v[1][q][e] = in ? dh[e] * a : 0.0f;
+        v[2][q][e] = in ? a * u[e] : 0.0f;
       }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[0][q][e] = v[1][q][e] = v[2][q][e] = 0.0f;
     }
-  }
+  });
 
   // along features
 #pragma unroll
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(512, 4) void k_glu_bwd(const GluBwd p) {
       uint32_t m = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) m = max(m, abs_bits(x[e]));
-      const float s = block_scale<FC>(__uint_as_float(canon_abs_bits(row16_max(m))), p.eps);
+      const float s = block_scale7<FC>(__uint_as_float(canon_abs_bits(row16_max(m))), p.eps);
       const float r = 1.0f / s;
       const bool fast = scale_ok(s);
       const u32x2 w = {encode4<FC>(x[0], x[1], x[2], x[3], s, r, fast), encode4<FC>(x[4], x[5], x[6], x[7], s, r, fast)};
@@ -102,8 +102,8 @@ __global__ __launch_bounds__(512, 4) void k_glu_bwd(const GluBwd p) {
 #pragma unroll
     for (int w = 0; w < 8; ++w) m = max(m, cmax[k][w][c]);
     const float amax = __uint_as_float(canon_abs_bits(m));
-    const float s = k < 2 ? block_scale<FC>(amax, p.eps) : block_scale<FH>(amax, p.eps);
-    cs[k][c] = s;
+    const float s = k < 2 ? block_scale7<FC>(amax, p.eps) : block_scale7<FH>(amax, p.eps);
+    cs[k][c] = make_float2(s, 1.0f / s);
     if (k < 2) {
       if (p.dt_) p.dts[(k * p.F + f0 + c) * p.ld_dts + mb] = s;
     } else if (p.ht) {
@@ -115,7 +115,7 @@ __global__ __launch_bounds__(512, 4) void k_glu_bwd(const GluBwd p) {
   for (int k = 0; k < 3; ++k)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float s = cs[k][8 * cl + e], r = 1.0f / s;
+      const float s = cs[k][8 * cl + e].x, r = cs[k][8 * cl + e].y;
       const bool fast = scale_ok(s);
       tile[k][tr_slot(8 * cl + e, rg)] =
           k < 2 ? encode4<FC>(v[k][0][e], v[k][1][e], v[k][2][e], v[k][3][e], s, r, fast)

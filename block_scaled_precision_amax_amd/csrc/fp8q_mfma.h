@@ -4,6 +4,8 @@
 
 #include "fp8q_ffn.h"
 
+#include <type_traits>
+
 namespace fp8q {
 namespace ffn {
 
@@ -68,9 +70,9 @@ __device__ __forceinline__ float sigmoid(float x) {
 // act(g), and act'(g) where asked for.  SiLU: g * sigmoid(g).  GELU (tanh
 // form): g * p with p = (1 + tanh(k))/2 = sigmoid(2k),
 // k = sqrt(2/pi) (g + 0.044715 g^3).
-template <bool GRAD>
-__device__ __forceinline__ float activation(int act, float g, float& grad) {
-  if (act == FP8Q_ACT_SILU) {
+template <int ACT, bool GRAD>
+__device__ __forceinline__ float activation(float g, float& grad) {
+  if constexpr (ACT == FP8Q_ACT_SILU) {
     const float sg = sigmoid(g);
     if (GRAD) grad = sg * (1.0f + g * (1.0f - sg));
     return g * sg;
@@ -84,9 +86,17 @@ __device__ __forceinline__ float activation(int act, float g, float& grad) {
   }
   return g * p;
 }
-__device__ __forceinline__ float activation(int act, float g) {
+template <int ACT>
+__device__ __forceinline__ float activation(float g) {
   float unused;
-  return activation<false>(act, g, unused);
+  return activation<ACT, false>(g, unused);
+}
+// f with the activation as a constant: the choice is made once around a
+// loop, so that the exponentials of its elements overlap.
+template <typename F>
+__device__ __forceinline__ void with_activation(int act, F f) {
+  if (act == FP8Q_ACT_SILU) f(std::integral_constant<int, FP8Q_ACT_SILU>{});
+  else f(std::integral_constant<int, FP8Q_ACT_GELU>{});
 }
 
 // ---- tiles.  The layouts, the copies and the tile order are those of the

@@ -33,22 +33,6 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
   return v;
 }
 
-// Eight elements of a row as loaded, and as fp32.
-template <int DT>
-struct Raw8 {
-  u32x4 v[DT == FP8Q_F32 ? 2 : 1];
-  template <bool STREAM = true>
-  __device__ __forceinline__ void load(const void* p, int64_t i) {
-    const u32x4* q = (const u32x4*)((const char*)p + i * (DT == FP8Q_F32 ? 4 : 2));
-#pragma unroll
-    for (int k = 0; k < (DT == FP8Q_F32 ? 2 : 1); ++k) v[k] = STREAM ? __builtin_nontemporal_load(q + k) : q[k];
-  }
-  __device__ __forceinline__ float operator[](int e) const {
-    if constexpr (DT == FP8Q_F32) return __uint_as_float(v[e >> 2][e & 3]);
-    else return e & 1 ? bf_hi(v[0][e >> 1]) : bf_lo(v[0][e >> 1]);
-  }
-};
-
 // One row per TPR threads, V groups of eight consecutive elements a thread:
 // group g of thread t is elements 8 * (g * TPR + t), so 16 neighbouring
 // lanes hold one 128-element block.  A row's loads are issued together,
@@ -110,7 +94,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm_1x128(const N
     if (p.q) {
       const float amax = __uint_as_float(canon_abs_bits(row16_max(m)));
       const bool e4 = p.fmt == FP8Q_E4M3FN;
-      const float s = e4 ? block_scale<FP8Q_E4M3FN>(amax, p.qeps) : block_scale<FP8Q_E5M2>(amax, p.qeps);
+      const float s = e4 ? block_scale7<FP8Q_E4M3FN>(amax, p.qeps) : block_scale7<FP8Q_E5M2>(amax, p.qeps);
       const bool fast = scale_ok(s);
       const float inv = 1.0f / s;
       u32x2 q;
