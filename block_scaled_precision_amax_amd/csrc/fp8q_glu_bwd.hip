@@ -33,12 +33,19 @@ template <int DH, int FC, int FH>
 __global__ __launch_bounds__(512, 4) void k_glu_bwd(const GluBwd p) {
   __shared__ __attribute__((aligned(16))) uint32_t tile[3][128 * 32];
   __shared__ uint32_t cmax[3][8][128];
-  __shared__ float2 cs[3][128];  // a column's scale and its reciprocal
+  __shared__ float2 cs[3][128];  // a column's scale and its reciprocal, column 8 cl + e at 16 e + cl
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int cl = tid & 15, rg = tid >> 4;
-  const int64_t nf = p.F / 128, mb = blockIdx.x / nf;
-  const int64_t f0 = (blockIdx.x - mb * nf) * 128, m0 = mb * 128;
+  const int64_t nf = p.F / 128, nm = (p.M + 127) / 128;
+  // Order of tiles: each XCD a contiguous part (ids go to the eight in turn),
+  // and in it sixteen token blocks of a feature block after one another, whose
+  // transposed pieces adjoin (8192 x 18432: 385 us against 404 along features).
+  int64_t id = blockIdx.x;
+  if (nf * nm % 8 == 0) id = (id & 7) * (nf * nm / 8) + (id >> 3);
+  const int64_t grp = id / (16 * nf), r16 = id - grp * 16 * nf, gs = nm - grp * 16 < 16 ? nm - grp * 16 : 16;
+  const int64_t fb = r16 / gs, mb = grp * 16 + r16 % gs;
+  const int64_t f0 = fb * 128, m0 = mb * 128;
   const int64_t col = f0 + 8 * cl;
 
   float v[3][4][8];  // dg, du, h
@@ -93,17 +100,17 @@ __global__ __launch_bounds__(512, 4) void k_glu_bwd(const GluBwd p) {
       uint32_t m = max(max(abs_bits(v[k][0][e]), abs_bits(v[k][1][e])), max(abs_bits(v[k][2][e]), abs_bits(v[k][3][e])));
       m = max(m, (uint32_t)__shfl_xor((int)m, 16));
       m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-      if (lane < 16) cmax[k][wave][8 * cl + e] = m;
+      if (lane < 16) cmax[k][wave][16 * e + cl] = m;
     }
   __syncthreads();
   if (tid < 384) {
     const int k = tid >> 7, c = tid & 127;
     uint32_t m = 0;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) m = max(m, cmax[k][w][c]);
+    for (int w = 0; w < 8; ++w) m = max(m, cmax[k][w][(c & 7) * 16 + (c >> 3)]);
     const float amax = __uint_as_float(canon_abs_bits(m));
     const float s = k < 2 ? block_scale7<FC>(amax, p.eps) : block_scale7<FH>(amax, p.eps);
-    cs[k][c] = make_float2(s, 1.0f / s);
+    cs[k][(c & 7) * 16 + (c >> 3)] = make_float2(s, 1.0f / s);
     if (k < 2) {
       if (p.dt_) p.dts[(k * p.F + f0 + c) * p.ld_dts + mb] = s;
     } else if (p.ht) {
@@ -115,7 +122,7 @@ __global__ __launch_bounds__(512, 4) void k_glu_bwd(const GluBwd p) {
   for (int k = 0; k < 3; ++k)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float s = cs[k][8 * cl + e].x, r = cs[k][8 * cl + e].y;
+      const float s = cs[k][16 * e + cl].x, r = cs[k][16 * e + cl].y;
       const bool fast = scale_ok(s);
       tile[k][tr_slot(8 * cl + e, rg)] =
           k < 2 ? encode4<FC>(v[k][0][e], v[k][1][e], v[k][2][e], v[k][3][e], s, r, fast)
