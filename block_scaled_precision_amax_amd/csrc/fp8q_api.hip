@@ -339,12 +339,12 @@ static int gemm_entry(const char* fn, const uint8_t* A, int fa, int64_t lda, con
   if (!aligned(sA, 4) || !aligned(sB, 4) || !aligned(C, out_dt == FP8Q_F32 ? 4 : 2))
     return fail(FP8Q_EALIGN, "%s: misaligned scales or C", fn);
   // both kernels compute every element by the same instructions in the same
-  // order; the tile's height alone differs
-  if (fast && gb == FP8Q_GRAN_128x128 && gemm_fast_low(M, N) && (M - 1) * lda + K <= 0xFFFFFFFFll &&
+  // order; the tiles' heights alone differ
+  if (fast && gb == FP8Q_GRAN_128x128 && gemm_fast_cut(M, N, K) && (M - 1) * lda + K <= 0xFFFFFFFFll &&
       (N - 1) * ldb + K <= 0xFFFFFFFFll) {
     Proj p = make_proj(A, fa, lda, sA, sA_sm, sA_skb, B, nullptr, fb, ldb, sB, nullptr, gb, sB_sn, sB_skb, M, N, K);
     p.out = C, p.ldo = ldc, p.out_dt = out_dt;
-    return launch_gemm_fast_low(p, fn, S(stream));
+    return launch_gemm_fast_cut(p, fn, S(stream));
   }
   return launch_gemm(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, gb, sB_sn, sB_skb, C, out_dt, ldc, M,
                      N, K, fast, S(stream));

@@ -152,10 +152,10 @@ int launch_glu(const Proj& p, bool fast, const char* what, hipStream_t st);
 // where the few-row kernel makes it, none otherwise.
 int64_t glu_q_workspace(int64_t M, int64_t F);
 
-// The block-scaled FP8-MFMA product with 128x128 B scales on tiles of half the
-// height, and whether a product is better off on them.
-bool gemm_fast_low(int64_t M, int64_t N);
-int launch_gemm_fast_low(Proj p, const char* what, hipStream_t st);
+// The block-scaled FP8-MFMA product with 128x128 B scales on tiles of two
+// heights, and whether a product is better off so.
+bool gemm_fast_cut(int64_t M, int64_t N, int64_t K);
+int launch_gemm_fast_cut(Proj p, const char* what, hipStream_t st);
 
 struct GluBwd {
   const void* dh;

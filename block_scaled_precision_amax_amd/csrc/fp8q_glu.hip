@@ -26,6 +26,13 @@ static constexpr int BK = 128;
 static constexpr int kThreads = 512;
 static constexpr int TJ = 4;
 
+// The tiles of one launch: `count` from number `first` of the ntm x ntn tile
+// grid, or (halves) both halves of count / 2 tiles of twice this height.
+struct Part {
+  int64_t ntm, ntn, first, count;
+  bool halves;
+};
+
 template <bool FAST, int TI_>
 struct Shape {
   static constexpr int TI = TI_, BM = 32 * TI, NST = TI == 8 ? 2 : 3;
@@ -86,7 +93,7 @@ __device__ __forceinline__ void drain_tile(const uint8_t* stg, int tid, T* out, 
 // B0's, 128 columns on).
 template <int FA, int FB, int OUT, bool FAST, int TI_, bool GLU>
 __global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, const float* __restrict__ s0,
-                                                     const float* __restrict__ s1, int64_t ntm, int64_t ntn) {
+                                                     const float* __restrict__ s1, const Part t) {
   using S = Shape<FAST, TI_>;
   constexpr int TI = S::TI, BM = S::BM, NST = S::NST;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
@@ -94,9 +101,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, const float* 
   __shared__ uint32_t lds_rmax[OUT >= 2 ? 4 : 1][OUT >= 2 ? BM : 1];
   constexpr int B0 = NST * S::A_STAGE;  // the B stages follow the A stages
   const uint32_t lds_at = lds_addr_of(lds), sa_at = lds_addr_of(lds_sa);
-  const int64_t M = p.M, N = p.N, nkb = p.K / BK, ntiles = ntm * ntn;
+  const int64_t M = p.M, N = p.N, nkb = p.K / BK;
 
-  for (int64_t tile = blockIdx.x; tile < ntiles; tile += gridDim.x) {
+  for (int64_t tile = blockIdx.x; tile < t.count; tile += gridDim.x) {
     // derived again for every tile: hoisted, it all stays live and spills
     int tid = threadIdx.x;
     asm volatile("" : "+v"(tid));
@@ -104,8 +111,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, const float* 
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
     int64_t tm, tn;
-    tile_of(tile, ntiles, ntm, ntn, tm, tn);
-    const int64_t m0 = tm * BM, n0 = tn * (GLU ? 128 : 256);
+    tile_of(t.first + (t.halves ? tile >> 1 : tile), t.ntm * t.ntn, t.ntm, t.ntn, tm, tn);
+    const int64_t m0 = t.halves ? (2 * tm + (tile & 1)) * BM : tm * BM, n0 = tn * (GLU ? 128 : 256);
+    if (m0 >= M) continue;  // the lower half of a ragged tile
 
     // Copies: a copy stalls the wavefront that issues it, so wavefronts 0-3
     // issue all of them and 4-7, on the same SIMDs, go on with MFMAs.
@@ -450,105 +458,128 @@ __global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, const float* 
   }
 }
 
-template <int FA, int FB, int OUT, bool FAST, int TI, bool GLU = true>
-static void launch_t(const Proj& p, hipStream_t st) {
-  const int64_t ntm = (p.M + 32 * TI - 1) / (32 * TI), ntn = GLU ? (p.N + 127) / 128 : (p.N + 255) / 256;
-  // one workgroup per compute unit, a multiple of eight so that a
-  // workgroup's tiles stay on its XCD
-  int64_t g = device_cu_count() / 8 * 8;
-  if (g < 8) g = 8;
-  if (ntm * ntn < g) g = ntm * ntn;
-  hipLaunchKernelGGL((k_glu<FA, FB, OUT, FAST, TI, GLU>), dim3((unsigned)g), dim3(kThreads), 0, st, p, p.s0, p.s1, ntm,
-                     ntn);
+// Workgroups of a launch: one per compute unit, a multiple of eight so that a
+// workgroup's tiles stay on its XCD.
+static int64_t grid_size() {
+  const int64_t g = device_cu_count() / 8 * 8;
+  return g < 8 ? 8 : g;
 }
 
-template <int FA, int FB, int OUT, bool FAST>
-static void launch_h(const Proj& p, bool tall, hipStream_t st) {
-  if (tall) launch_t<FA, FB, OUT, FAST, FAST ? 8 : 4>(p, st);
-  else launch_t<FA, FB, OUT, FAST, FAST ? 4 : 2>(p, st);
+// How a product of ntn tile columns is cut, and what it costs in thousandths
+// of a microsecond per K block.  A round of up to a tile per compute unit takes
+// 1.4 us a block with tall tiles (256 rows FP8-MFMA, 128 exact) and 0.85 with
+// low ones (half the rows) while few units work, 1.7 and 1.05 when all do.
+// So: whole rounds of tall tiles, and the rest, if it is at most half a
+// round, as a second launch of its halves; or low tiles throughout.
+//   exact 1023 x 9000 x 4096 (568 tall tiles): 163 us in three rounds, 146 in
+//   two and a round of halves; fast 128 x 18432 x 7168: 94 us tall, 75 low.
+struct Cut {
+  bool low;       // low tiles throughout
+  int64_t tall;   // tall tiles, then
+  int64_t split;  // tall tiles taken as halves
+  int64_t cost;
+};
+static Cut cut_tiles(int64_t M, int64_t rows, int64_t ntn, int64_t launch_cost) {
+  const int64_t cu = grid_size(), tiles = (M + rows - 1) / rows * ntn;
+  const int64_t low = 850 * ((((M + rows / 2 - 1) / (rows / 2)) * ntn + cu - 1) / cu);
+  const int64_t full = tiles / cu, rest = tiles - full * cu;
+  const bool split = full > 0 && rest > 0 && 2 * rest <= cu && 850 + launch_cost < 1360;
+  const int64_t tall = 1360 * full + (rest == 0 ? 0 : split ? 850 + launch_cost : 1360);
+  if (low < tall) return {true, 0, 0, low};
+  return {false, split ? full * cu : tiles, split ? rest : 0, tall};
+}
+// A second launch costs about 3 us.
+static int64_t second_launch(int64_t K) { return 3000 * 128 / K; }
+
+template <int FA, int FB, int OUT, bool FAST, int TI, bool GLU>
+static void launch_part(const Proj& p, const Part& t, hipStream_t st) {
+  const int64_t g = grid_size();
+  hipLaunchKernelGGL((k_glu<FA, FB, OUT, FAST, TI, GLU>), dim3((unsigned)(t.count < g ? t.count : g)), dim3(kThreads), 0, st,
+                     p, p.s0, p.s1, t);
+}
+
+template <int FA, int FB, int OUT, bool FAST, bool GLU>
+static void launch_cut(const Proj& p, const Cut& c, hipStream_t st) {
+  constexpr int TALL = FAST ? 8 : 4, LOW = TALL / 2;
+  const int64_t ntn = GLU ? (p.N + 127) / 128 : (p.N + 255) / 256;
+  const int64_t ntm = (p.M + 32 * TALL - 1) / (32 * TALL), ltm = (p.M + 32 * LOW - 1) / (32 * LOW);
+  if (c.low) {
+    launch_part<FA, FB, OUT, FAST, LOW, GLU>(p, {ltm, ntn, 0, ltm * ntn, false}, st);
+    return;
+  }
+  launch_part<FA, FB, OUT, FAST, TALL, GLU>(p, {ntm, ntn, 0, c.tall, false}, st);
+  if (c.split) launch_part<FA, FB, OUT, FAST, LOW, GLU>(p, {ntm, ntn, c.tall, 2 * c.split, true}, st);
 }
 
 template <int FA, int FB>
-static void launch_f(const Proj& p, bool fast, bool tall, hipStream_t st) {
+static void launch_f(const Proj& p, bool fast, const Cut& c, hipStream_t st) {
   if (p.scales) {
-    if (p.fc == FP8Q_E4M3FN) launch_h<FA, FB, 2 + FP8Q_E4M3FN, false>(p, tall, st);
-    else launch_h<FA, FB, 2 + FP8Q_E5M2, false>(p, tall, st);
+    if (p.fc == FP8Q_E4M3FN) launch_cut<FA, FB, 2 + FP8Q_E4M3FN, false, true>(p, c, st);
+    else launch_cut<FA, FB, 2 + FP8Q_E5M2, false, true>(p, c, st);
   } else if (fast) {
-    if (p.out_dt == FP8Q_F32) launch_h<FA, FB, FP8Q_F32, true>(p, tall, st);
-    else launch_h<FA, FB, FP8Q_BF16, true>(p, tall, st);
+    if (p.out_dt == FP8Q_F32) launch_cut<FA, FB, FP8Q_F32, true, true>(p, c, st);
+    else launch_cut<FA, FB, FP8Q_BF16, true, true>(p, c, st);
   } else {
-    if (p.out_dt == FP8Q_F32) launch_h<FA, FB, FP8Q_F32, false>(p, tall, st);
-    else launch_h<FA, FB, FP8Q_BF16, false>(p, tall, st);
+    if (p.out_dt == FP8Q_F32) launch_cut<FA, FB, FP8Q_F32, false, true>(p, c, st);
+    else launch_cut<FA, FB, FP8Q_BF16, false, true>(p, c, st);
   }
 }
 
-// Which kernel a call takes, in units of a thousandth of a microsecond per K
-// block (the fixed few microseconds are alike), from the sizes alone:
-//   * tiles: one round of up to a tile per compute unit takes 1.4 us (256 rows
-//     FP8-MFMA, 128 exact) or 0.85 us (half the rows) a block while few units
-//     work and 1.7 and 1.05 when all do; rounds x that, the lower of the two.
-//     M = 512, F = 18432, K = 7168 fast: 195 (2 rounds) against 185 us (3);
-//     M = 1023: 285 (3) against 304 us (5).
-//   * few rows: a workgroup of 16 columns and up to 64 rows takes
-//     0.12 + 0.058 per 16 rows; workgroups per compute unit (at least one) x
-//     that.  F = 4096, K = 4096: 10 us at 16 rows and 25 us at 128 against 30
-//     on tiles, 48 against 31 us at 256; F = 18432, K = 7168: 45 us at 16 rows
-//     and 65 us at 32 against 60 and 62 us.
-struct Plan {
-  bool few, tall;
-};
-static int64_t tile_rounds(int64_t M, int64_t rows, int64_t ntn) {
-  const int64_t cu = device_cu_count();
-  return ((M + rows - 1) / rows * ntn + cu - 1) / cu;
-}
-static Plan plan(int64_t M, int64_t F, bool fast) {
-  const int64_t cu = device_cu_count(), bm = fast ? 256 : 128, ntn = (F + 127) / 128;
-  const int64_t tall = 1360 * tile_rounds(M, bm, ntn), low = 850 * tile_rounds(M, bm / 2, ntn);
+// Whether a call takes the few-row kernel, where a workgroup of 16 columns and
+// up to 64 rows takes 0.12 us and 0.058 per 16 rows a K block; workgroups per
+// compute unit (at least one) x that, against the tiles' cost.  The choice
+// goes by M and F alone, so that the workspace does.
+//   F = 4096, K = 4096: 10 us at 16 rows and 25 us at 128 against 30 on tiles,
+//   48 against 31 us at 256; F = 18432, K = 7168: 45 us at 16 rows and 65 at 32
+//   against 60 and 62.
+static bool few_rows(int64_t M, int64_t F, bool fast) {
+  const int64_t cu = grid_size();
   const int64_t groups = (M + 63) / 64, tiles = ((M + groups - 1) / groups + 15) / 16;
   int64_t wgs = groups * ((F + 15) / 16);
   if (wgs < cu) wgs = cu;
-  return {wgs * (120 + 58 * tiles) < (tall < low ? tall : low) * cu, tall <= low};
+  return wgs * (120 + 58 * tiles) < cut_tiles(M, fast ? 256 : 128, (F + 127) / 128, 0).cost * cu;
 }
 
-int64_t glu_q_workspace(int64_t M, int64_t F) { return plan(M, F, false).few ? 4 * M * F : 0; }
+int64_t glu_q_workspace(int64_t M, int64_t F) { return few_rows(M, F, false) ? 4 * M * F : 0; }
 
 int launch_glu(const Proj& p, bool fast, const char* what, hipStream_t st) {
-  const Plan pl = plan(p.M, p.N, fast);
-  if (pl.few && p.scales) {
+  if (few_rows(p.M, p.N, fast)) {
+    if (!p.scales) return launch_few(p, what, st);
     Proj h = p;
     h.out = p.ws, h.ldo = p.N, h.out_dt = FP8Q_F32, h.scales = nullptr;
     if (int rc = launch_few(h, what, st)) return rc;
     return launch_quantize_1x128(p.ws, FP8Q_F32, p.M, p.N, p.N, p.fc, p.eps, (uint8_t*)p.out, p.ldo, p.scales, p.ld_s, st);
   }
-  if (pl.few) return launch_few(p, what, st);
-  if (p.fa == FP8Q_E4M3FN && p.fb == FP8Q_E4M3FN) launch_f<0, 0>(p, fast, pl.tall, st);
-  else if (p.fa == FP8Q_E5M2 && p.fb == FP8Q_E4M3FN) launch_f<1, 0>(p, fast, pl.tall, st);
-  else if (p.fa == FP8Q_E4M3FN) launch_f<0, 1>(p, fast, pl.tall, st);
-  else launch_f<1, 1>(p, fast, pl.tall, st);
+  const Cut c = cut_tiles(p.M, fast ? 256 : 128, (p.N + 127) / 128, second_launch(p.K));
+  if (p.fa == FP8Q_E4M3FN && p.fb == FP8Q_E4M3FN) launch_f<0, 0>(p, fast, c, st);
+  else if (p.fa == FP8Q_E5M2 && p.fb == FP8Q_E4M3FN) launch_f<1, 0>(p, fast, c, st);
+  else if (p.fa == FP8Q_E4M3FN) launch_f<0, 1>(p, fast, c, st);
+  else launch_f<1, 1>(p, fast, c, st);
   return check_launch(what);
 }
 
-// The block-scaled FP8-MFMA product on 128-row tiles, for sizes that leave
-// 256-row tiles few or uneven rounds (the gradients' products of a
-// micro-batch: 1000 x 4096 x 8192 has 64 of those).  The same instructions in
-// the same order per element, so the same bits.
-bool gemm_fast_low(int64_t M, int64_t N) {
-  const int64_t ntn = (N + 255) / 256;
-  return 850 * tile_rounds(M, 128, ntn) < 1360 * tile_rounds(M, 256, ntn);
+// The block-scaled FP8-MFMA product where whole rounds of 256-row tiles do
+// not fit it (the gradients' products: 1000 x 4096 x 8192 has 64 of them).  The
+// same instructions in the same order per element as its own kernel, so the
+// same bits.
+bool gemm_fast_cut(int64_t M, int64_t N, int64_t K) {
+  const Cut c = cut_tiles(M, 256, (N + 255) / 256, second_launch(K));
+  return c.low || c.split;
 }
 
 template <int FA, int FB>
-static void launch_low(const Proj& p, hipStream_t st) {
-  if (p.out_dt == FP8Q_F32) launch_t<FA, FB, FP8Q_F32, true, 4, false>(p, st);
-  else launch_t<FA, FB, FP8Q_BF16, true, 4, false>(p, st);
+static void launch_product(const Proj& p, const Cut& c, hipStream_t st) {
+  if (p.out_dt == FP8Q_F32) launch_cut<FA, FB, FP8Q_F32, true, false>(p, c, st);
+  else launch_cut<FA, FB, FP8Q_BF16, true, false>(p, c, st);
 }
 
-int launch_gemm_fast_low(Proj p, const char* what, hipStream_t st) {
+int launch_gemm_fast_cut(Proj p, const char* what, hipStream_t st) {
   p.B1 = p.B0, p.s1 = p.s0;
-  if (p.fa == FP8Q_E4M3FN && p.fb == FP8Q_E4M3FN) launch_low<0, 0>(p, st);
-  else if (p.fa == FP8Q_E5M2 && p.fb == FP8Q_E4M3FN) launch_low<1, 0>(p, st);
-  else if (p.fa == FP8Q_E4M3FN) launch_low<0, 1>(p, st);
-  else launch_low<1, 1>(p, st);
+  const Cut c = cut_tiles(p.M, 256, (p.N + 255) / 256, second_launch(p.K));
+  if (p.fa == FP8Q_E4M3FN && p.fb == FP8Q_E4M3FN) launch_product<0, 0>(p, c, st);
+  else if (p.fa == FP8Q_E5M2 && p.fb == FP8Q_E4M3FN) launch_product<1, 0>(p, c, st);
+  else if (p.fa == FP8Q_E4M3FN) launch_product<0, 1>(p, c, st);
+  else launch_product<1, 1>(p, c, st);
   return check_launch(what);
 }
 

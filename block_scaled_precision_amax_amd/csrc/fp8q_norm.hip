@@ -339,11 +339,14 @@ static void dispatch_bwd(const NormBwd& p, int64_t parts, hipStream_t st) {
   else launch_bwd<DT, 1024, 8>(p, parts, st);
 }
 
-int launch_rmsnorm_bwd(const NormBwd& p, hipStream_t st) {
-  const int64_t parts = rmsnorm_bwd_parts(p.rows, p.cols);
+int launch_rmsnorm_bwd(const NormBwd& q, hipStream_t st) {
+  const int64_t parts = rmsnorm_bwd_parts(q.rows, q.cols);
+  NormBwd p = q;
+  const bool direct = parts == 1 && ((uintptr_t)p.dw & 15) == 0;
+  if (direct && p.dw) p.ws = p.dw;  // the one row of partial sums is the result
   if (p.dt == FP8Q_F32) dispatch_bwd<FP8Q_F32>(p, parts, st);
   else dispatch_bwd<FP8Q_BF16>(p, parts, st);
-  if (p.dw)
+  if (p.dw && !direct)
     hipLaunchKernelGGL(k_norm_dw, dim3((unsigned)(p.cols / 64)), dim3(256), 0, st, p.ws, parts, p.cols, p.dw);
   return check_launch("rmsnorm_bwd");
 }

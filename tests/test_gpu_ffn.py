@@ -330,7 +330,7 @@ def test_glu_halves_of_one_matrix_and_scale_strides(fq, gpu):
         assert torch.equal(h, want)
 
 
-@pytest.mark.parametrize("M,F,K", [(2305, 4000, 256), (1025, 6100, 384), (1281, 18400, 128)])
+@pytest.mark.parametrize("M,F,K", [(2305, 4000, 256), (1025, 6100, 384), (1281, 18400, 128), (2305, 4000, 2048)])
 def test_glu_many_tiles(fq, orc, gpu, M, F, K):
     """Up to several tiles per compute unit, of either height, a ragged edge both ways, checked on sampled rows."""
     A, sA, B, sB = operands(gpu, M, F, K, seed=4)
@@ -393,6 +393,19 @@ def test_fast_product_is_the_same_on_either_tile(fq, gpu, M, N, K, fa):
         for out, rows, ld in ((C, M, N + 5), (D, A.shape[0], N)):
             fq.fp8q_gemm_blockscaled_fast(A, fa, K, sA, K // 128, 1, B[0], E4, K, sB[0], 2, K // 128, 1, out, ld, rows, N, K)
         assert torch.equal(C[:, :N], D[:M]) and (C[:, N:] == 7).all()
+
+
+def test_fast_product_of_uneven_rounds(fq, gpu):
+    """A product cut into whole rounds of 256-row tiles and the halves of the rest equals, bit for bit, the products of its
+    first 2048 rows (256-row tiles alone) and of its last 257 (128-row tiles alone)."""
+    M, N, K = 2305, 8000, 2048
+    A, sA, B, sB = operands(gpu, M, N, K, seed=8)
+    for dt in (torch.float32, torch.bfloat16):
+        C, D = (torch.full((M, N), float("nan"), dtype=dt, device=gpu) for _ in range(2))
+        for out, r0, r1 in ((C, 0, M), (D, 0, 2048), (D, 2048, M)):
+            fq.fp8q_gemm_blockscaled_fast(A[r0:], E4, K, sA[r0:], K // 128, 1, B[0], E4, K, sB[0], 2, K // 128, 1, out[r0:], N,
+                                          r1 - r0, N, K)
+        assert C.isfinite().all() and torch.equal(C, D)
 
 
 # ------------------------------------------------------------------ gradient of the gated projection
