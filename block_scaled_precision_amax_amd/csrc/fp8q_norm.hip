@@ -12,7 +12,9 @@
 //
 // Both directions are HBM streams: every element is read once and written
 // once, a row stays in registers between its sum and its output, and the
-// block maximum of eight elements a lane is four DPP steps.
+// block maximum of eight elements a lane is four DPP steps.  16384 x 7168 bf16
+// with residual: forward 137 us (6.0 TB/s), gradients 171 us (5.5 TB/s); a
+// row alone is 3.8 us, most of it the launch.
 #include "fp8q_ffn.h"
 
 namespace fp8q {
