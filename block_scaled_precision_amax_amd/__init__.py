@@ -186,6 +186,19 @@ def _stream(stream, t=None) -> int | None:
     return torch.cuda.current_stream(dev).cuda_stream
 
 
+def _workspace(nbytes, handle, stream, t):
+    """Scratch memory on t's device from the pool of the stream that uses it: the allocator hands a block out again as
+    soon as its own stream's work is enqueued, so one of another stream's may still be in use there."""
+    import torch
+
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
+    if isinstance(stream, int):  # handle 0 is no external stream to torch
+        stream = torch.cuda.ExternalStream(handle, device=t.device) if handle else torch.cuda.default_stream(t.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
+
+
 def _check(rc: int) -> None:
     if rc != OK:
         raise Fp8qError(rc, lib().fp8q_last_error().decode(errors="replace"))
@@ -341,11 +354,7 @@ def fp8q_glu_blockscaled_q(A, fa, lda, sA, sA_sm, sA_skb, Bg, Bu, fb, ldb, sBg, 
     if ws is None:
         ws_bytes = lib().fp8q_glu_blockscaled_q_workspace(M, F)
         if ws_bytes:
-            import torch
-
-            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=Hq.device)
-            if stream is not None:  # the allocator may hand it out again only behind that stream's work
-                ws.record_stream(torch.cuda.ExternalStream(handle, device=Hq.device))
+            ws = _workspace(ws_bytes, handle, stream, Hq)
     _check(lib().fp8q_glu_blockscaled_q(_ptr(A), fa, lda, _ptr(sA), sA_sm, sA_skb, _ptr(Bg), _ptr(Bu), fb, ldb,
                                         _ptr(sBg), _ptr(sBu), sB_sn, sB_skb, act, fc, eps, _ptr(Hq), ldhq, _ptr(Hs),
                                         ld_hs, _ptr(gu), ldgu, M, F, K, _ptr(ws), ws_bytes, handle))

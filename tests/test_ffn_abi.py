@@ -140,3 +140,73 @@ def test_mixed_dtypes_are_refused_by_the_binding(fq):
     with pytest.raises(TypeError):
         fq.fp8q_glu_bwd_q(x.half(), 128, 1, 256, 0, 0, 1e-12, 1, 256, 1, 2, None, 0, None, 0, 0, None, 0, None, 0, 2, 128,
                           stream=0)
+
+
+class _Recorder:
+    """Stands in for the library and for torch's stream calls: which stream was current when memory was taken."""
+
+    def __init__(self, fq, monkeypatch):
+        self.taken, self.current, self.call = [], ["current"], None
+        rec = self
+
+        class Lib:
+            def fp8q_glu_blockscaled_q_workspace(self, M, F):
+                return 512
+
+            def fp8q_glu_blockscaled_q(self, *args):
+                rec.call = args
+                return fq.OK
+
+        class On:
+            def __init__(self, stream):
+                self.stream = stream
+
+            def __enter__(self):
+                rec.current.append(self.stream)
+
+            def __exit__(self, *e):
+                rec.current.pop()
+
+        class Block:
+            def data_ptr(self):
+                return FAKE
+
+            def record_stream(self, stream):
+                pass
+
+        def empty(n, dtype, device):
+            rec.taken.append((n, str(device), rec.current[-1]))
+            return Block()
+
+        monkeypatch.setattr(fq, "lib", lambda: Lib())
+        monkeypatch.setattr(torch, "empty", empty)
+        monkeypatch.setattr(torch.cuda, "stream", On)
+        monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, device=None: ("external", h, str(device)))
+        monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: ("default", str(device)))
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+
+
+def _glu_q(fq, A, out, stream):
+    s = torch.zeros(2, 1)
+    fq.fp8q_glu_blockscaled_q(A, 0, 128, s, 1, 1, FAKE, FAKE, 0, 128, s, s, 1, 1, 0, 0, 1e-12, out, 128, s, 1, None, 0, 2, 128,
+                              128, stream=stream)
+
+
+@pytest.mark.parametrize("handle,want", [(0x7700, ("external", 0x7700, "cpu")), (0, ("default", "cpu"))])
+def test_workspace_is_taken_on_the_stream_that_uses_it(fq, monkeypatch, handle, want):
+    """A block from another stream's pool may still be read or written by that stream's pending work."""
+    rec = _Recorder(fq, monkeypatch)
+    A = torch.zeros(2, 128, dtype=torch.uint8)
+    _glu_q(fq, A, A, handle)
+    assert rec.taken == [(512, "cpu", want)]
+    assert rec.call[-1] == handle and rec.call[-2] == 512
+
+
+def test_workspace_on_a_stream_object(fq, monkeypatch):
+    class Stream:
+        cuda_stream, device = 0x7700, torch.device("cpu")
+
+    rec = _Recorder(fq, monkeypatch)
+    A = torch.zeros(2, 128, dtype=torch.uint8)
+    _glu_q(fq, A, A, Stream)
+    assert [t[2] for t in rec.taken] == [Stream] and rec.call[-1] == 0x7700
