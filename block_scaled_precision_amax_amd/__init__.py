@@ -187,16 +187,18 @@ def _stream(stream, t=None) -> int | None:
 
 
 def _workspace(nbytes, handle, stream, t):
-    """Scratch memory on t's device from the pool of the stream that uses it: the allocator hands a block out again as
-    soon as its own stream's work is enqueued, so one of another stream's may still be in use there."""
+    """Scratch memory on t's device (the current one for a raw pointer) from the pool of the stream that uses it: the
+    allocator hands a block out again as soon as its own stream's work is enqueued, so one of another stream's may still
+    be in use there."""
     import torch
 
+    dev = torch.device("cuda", torch.cuda.current_device()) if isinstance(t, int) else t.device
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
     if isinstance(stream, int):  # handle 0 is no external stream to torch
-        stream = torch.cuda.ExternalStream(handle, device=t.device) if handle else torch.cuda.default_stream(t.device)
+        stream = torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
     with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
 
 def _check(rc: int) -> None:
@@ -354,7 +356,7 @@ def fp8q_glu_blockscaled_q(A, fa, lda, sA, sA_sm, sA_skb, Bg, Bu, fb, ldb, sBg, 
     if ws is None:
         ws_bytes = lib().fp8q_glu_blockscaled_q_workspace(M, F)
         if ws_bytes:
-            ws = _workspace(ws_bytes, handle, stream, Hq)
+            ws = _workspace(ws_bytes, handle, stream, A)
     _check(lib().fp8q_glu_blockscaled_q(_ptr(A), fa, lda, _ptr(sA), sA_sm, sA_skb, _ptr(Bg), _ptr(Bu), fb, ldb,
                                         _ptr(sBg), _ptr(sBu), sB_sn, sB_skb, act, fc, eps, _ptr(Hq), ldhq, _ptr(Hs),
                                         ld_hs, _ptr(gu), ldgu, M, F, K, _ptr(ws), ws_bytes, handle))

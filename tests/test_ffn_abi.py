@@ -210,3 +210,13 @@ def test_workspace_on_a_stream_object(fq, monkeypatch):
     A = torch.zeros(2, 128, dtype=torch.uint8)
     _glu_q(fq, A, A, Stream)
     assert [t[2] for t in rec.taken] == [Stream] and rec.call[-1] == 0x7700
+
+
+def test_workspace_with_raw_pointers(fq, monkeypatch):
+    """Outputs given as addresses: the device is the first operand's, or the current one."""
+    rec = _Recorder(fq, monkeypatch)
+    A = torch.zeros(2, 128, dtype=torch.uint8)
+    _glu_q(fq, A, FAKE, 0x7700)
+    _glu_q(fq, FAKE, FAKE, 0x7700)
+    assert [t[1] for t in rec.taken] == ["cpu", "cuda:3"]
+    assert rec.taken[1][2] == ("external", 0x7700, "cuda:3") and rec.call[0] == FAKE
