@@ -166,6 +166,48 @@ def _dt(t) -> int:
     return d
 
 
+# Operands whose element type is fixed: a narrower tensor's end would be passed, another type misread.  Each kind's
+# torch dtypes are filled in by the first check.
+_FLOAT: list = []
+_BFLOAT: list = []
+_CODES: list = []
+
+
+def _refuse(t, kind, name) -> None:
+    if not kind:
+        import torch
+
+        _FLOAT.append(torch.float32)
+        _BFLOAT.extend((torch.bfloat16, torch.int16, torch.uint16))
+        _CODES.extend((torch.uint8, torch.int8, torch.float8_e4m3fn, torch.float8_e5m2))
+    if t.dtype not in kind:
+        raise TypeError(f"this operand is {name}, got {t.dtype}")
+
+
+def _f32(t) -> int | None:
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype not in _FLOAT:
+        _refuse(t, _FLOAT, "float32")
+    return t.data_ptr()
+
+
+def _bf16(t) -> int | None:
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype not in _BFLOAT:
+        _refuse(t, _BFLOAT, "bfloat16")
+    return t.data_ptr()
+
+
+def _codes(t) -> int | None:
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype not in _CODES:
+        _refuse(t, _CODES, "FP8 codes")
+    return t.data_ptr()
+
+
 _raw_stream = None
 
 
@@ -316,8 +358,8 @@ def _same_dt(t, *others) -> int:
 def fp8q_rmsnorm_1x128(x, ldx, res, ldr, w, rows, cols, norm_eps, z, ldz, y, ldy, f, eps, q, ldq, scales, ld_s,
                        rstd=None, stream=None) -> None:
     _check(lib().fp8q_rmsnorm_1x128(_ptr(x), _same_dt(x, res, z, y), ldx, _ptr(res), ldr, _ptr(w), _dt(w), rows, cols,
-                                    norm_eps, _ptr(z), ldz, _ptr(y), ldy, f, eps, _ptr(q), ldq, _ptr(scales), ld_s,
-                                    _ptr(rstd), _stream(stream, x)))
+                                    norm_eps, _ptr(z), ldz, _ptr(y), ldy, f, eps, _codes(q), ldq, _f32(scales), ld_s,
+                                    _f32(rstd), _stream(stream, x)))
 
 
 def fp8q_rmsnorm_bwd_workspace(rows, cols) -> int:
@@ -326,22 +368,22 @@ def fp8q_rmsnorm_bwd_workspace(rows, cols) -> int:
 
 def fp8q_rmsnorm_bwd(dy, lddy, z, ldz, w, rstd, dres, lddr, rows, cols, dx, lddx, dw=None, ws=None, ws_bytes=0,
                      stream=None) -> None:
-    _check(lib().fp8q_rmsnorm_bwd(_ptr(dy), _same_dt(dy, z, dres, dx), lddy, _ptr(z), ldz, _ptr(w), _dt(w), _ptr(rstd),
-                                  _ptr(dres), lddr, rows, cols, _ptr(dx), lddx, _ptr(dw), _ptr(ws), ws_bytes,
+    _check(lib().fp8q_rmsnorm_bwd(_ptr(dy), _same_dt(dy, z, dres, dx), lddy, _ptr(z), ldz, _ptr(w), _dt(w), _f32(rstd),
+                                  _ptr(dres), lddr, rows, cols, _ptr(dx), lddx, _f32(dw), _ptr(ws), ws_bytes,
                                   _stream(stream, dy)))
 
 
 def fp8q_glu_blockscaled(A, fa, lda, sA, sA_sm, sA_skb, Bg, Bu, fb, ldb, sBg, sBu, sB_sn, sB_skb, act, H, ldh, gu, ldgu,
                          M, F, K, stream=None) -> None:
-    _check(lib().fp8q_glu_blockscaled(_ptr(A), fa, lda, _ptr(sA), sA_sm, sA_skb, _ptr(Bg), _ptr(Bu), fb, ldb, _ptr(sBg),
-                                      _ptr(sBu), sB_sn, sB_skb, act, _ptr(H), _dt(H), ldh, _ptr(gu), ldgu, M, F, K,
+    _check(lib().fp8q_glu_blockscaled(_codes(A), fa, lda, _f32(sA), sA_sm, sA_skb, _codes(Bg), _codes(Bu), fb, ldb, _f32(sBg),
+                                      _f32(sBu), sB_sn, sB_skb, act, _ptr(H), _dt(H), ldh, _bf16(gu), ldgu, M, F, K,
                                       _stream(stream, A)))
 
 
 def fp8q_glu_blockscaled_fast(A, fa, lda, sA, sA_sm, sA_skb, Bg, Bu, fb, ldb, sBg, sBu, sB_sn, sB_skb, act, H, ldh, gu,
                               ldgu, M, F, K, stream=None) -> None:
-    _check(lib().fp8q_glu_blockscaled_fast(_ptr(A), fa, lda, _ptr(sA), sA_sm, sA_skb, _ptr(Bg), _ptr(Bu), fb, ldb,
-                                           _ptr(sBg), _ptr(sBu), sB_sn, sB_skb, act, _ptr(H), _dt(H), ldh, _ptr(gu),
+    _check(lib().fp8q_glu_blockscaled_fast(_codes(A), fa, lda, _f32(sA), sA_sm, sA_skb, _codes(Bg), _codes(Bu), fb, ldb,
+                                           _f32(sBg), _f32(sBu), sB_sn, sB_skb, act, _ptr(H), _dt(H), ldh, _bf16(gu),
                                            ldgu, M, F, K, _stream(stream, A)))
 
 
@@ -357,19 +399,19 @@ def fp8q_glu_blockscaled_q(A, fa, lda, sA, sA_sm, sA_skb, Bg, Bu, fb, ldb, sBg, 
         ws_bytes = lib().fp8q_glu_blockscaled_q_workspace(M, F)
         if ws_bytes:
             ws = _workspace(ws_bytes, handle, stream, A)
-    _check(lib().fp8q_glu_blockscaled_q(_ptr(A), fa, lda, _ptr(sA), sA_sm, sA_skb, _ptr(Bg), _ptr(Bu), fb, ldb,
-                                        _ptr(sBg), _ptr(sBu), sB_sn, sB_skb, act, fc, eps, _ptr(Hq), ldhq, _ptr(Hs),
-                                        ld_hs, _ptr(gu), ldgu, M, F, K, _ptr(ws), ws_bytes, handle))
+    _check(lib().fp8q_glu_blockscaled_q(_codes(A), fa, lda, _f32(sA), sA_sm, sA_skb, _codes(Bg), _codes(Bu), fb, ldb,
+                                        _f32(sBg), _f32(sBu), sB_sn, sB_skb, act, fc, eps, _codes(Hq), ldhq, _f32(Hs),
+                                        ld_hs, _bf16(gu), ldgu, M, F, K, _ptr(ws), ws_bytes, handle))
 
 
 def fp8q_glu_bwd_q(dH, lddh, gu, ldgu, act, fc, eps, Dq, lddq, Ds, ld_ds, Dt, lddt, Dst, ld_dst, fh, Ht, ldht, Hst,
                    ld_hst, M, F, stream=None) -> None:
-    _check(lib().fp8q_glu_bwd_q(_ptr(dH), _dt(dH), lddh, _ptr(gu), ldgu, act, fc, eps, _ptr(Dq), lddq, _ptr(Ds), ld_ds,
-                                _ptr(Dt), lddt, _ptr(Dst), ld_dst, fh, _ptr(Ht), ldht, _ptr(Hst), ld_hst, M, F,
+    _check(lib().fp8q_glu_bwd_q(_ptr(dH), _dt(dH), lddh, _bf16(gu), ldgu, act, fc, eps, _codes(Dq), lddq, _f32(Ds), ld_ds,
+                                _codes(Dt), lddt, _f32(Dst), ld_dst, fh, _codes(Ht), ldht, _f32(Hst), ld_hst, M, F,
                                 _stream(stream, dH)))
 
 
 def fp8q_gemm_blockscaled_few(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, gb, sB_sn, sB_skb, C, ldc, M, N, K,
                               stream=None) -> None:
-    _check(lib().fp8q_gemm_blockscaled_few(_ptr(A), fa, lda, _ptr(sA), sA_sm, sA_skb, _ptr(B), fb, ldb, _ptr(sB), gb,
+    _check(lib().fp8q_gemm_blockscaled_few(_codes(A), fa, lda, _f32(sA), sA_sm, sA_skb, _codes(B), fb, ldb, _f32(sB), gb,
                                            sB_sn, sB_skb, _ptr(C), _dt(C), ldc, M, N, K, _stream(stream, A)))

@@ -220,3 +220,58 @@ def test_workspace_with_raw_pointers(fq, monkeypatch):
     _glu_q(fq, FAKE, FAKE, 0x7700)
     assert [t[1] for t in rec.taken] == ["cpu", "cuda:3"]
     assert rec.taken[1][2] == ("external", 0x7700, "cuda:3") and rec.call[0] == FAKE
+
+
+F32, B16, U8 = (torch.zeros(4, 256, dtype=d) for d in (torch.float32, torch.bfloat16, torch.uint8))
+
+
+def _norm(fq, x=B16, w=F32, q=U8, s=F32, rstd=F32):
+    fq.fp8q_rmsnorm_1x128(x, 256, None, 0, w, 0, 256, 1e-6, None, 0, None, 0, 0, 1e-12, q, 256, s, 2, rstd, stream=0)
+
+
+def _norm_bwd(fq, x=B16, rstd=F32, dw=F32):
+    fq.fp8q_rmsnorm_bwd(x, 256, x, 256, F32, rstd, None, 0, 0, 256, x, 256, dw, F32, 4096, stream=0)
+
+
+def _glu(fq, name="fp8q_glu_blockscaled", A=U8, sA=F32, Bg=U8, Bu=U8, sBg=F32, sBu=F32, gu=B16):
+    getattr(fq, name)(A, 0, 256, sA, 2, 1, Bg, Bu, 0, 256, sBg, sBu, 2, 1, 0, F32, 128, gu, 256, 0, 128, 256, stream=0)
+
+
+def _glu_fast(fq, **kw):
+    _glu(fq, "fp8q_glu_blockscaled_fast", **kw)
+
+
+def _glu_codes(fq, A=U8, sA=F32, Bg=U8, Bu=U8, sBg=F32, sBu=F32, H=U8, Hs=F32, gu=B16):
+    fq.fp8q_glu_blockscaled_q(A, 0, 256, sA, 2, 1, Bg, Bu, 0, 256, sBg, sBu, 2, 1, 0, 0, 1e-12, H, 128, Hs, 1, gu, 256, 0, 128,
+                              256, F32, 4096, stream=0)
+
+
+def _glu_bwd(fq, gu=B16, D=U8, Ds=F32, Dt=U8, Dst=F32, Ht=U8, Hst=F32):
+    fq.fp8q_glu_bwd_q(B16, 128, gu, 256, 0, 0, 1e-12, D, 256, Ds, 2, Dt, 128, Dst, 1, 0, Ht, 128, Hst, 1, 0, 128, stream=0)
+
+
+def _few(fq, A=U8, sA=F32, B=U8, sB=F32):
+    fq.fp8q_gemm_blockscaled_few(A, 0, 256, sA, 2, 1, B, 0, 256, sB, 2, 2, 1, F32, 128, 0, 128, 256, stream=0)
+
+
+TYPED = [(_norm, dict(f4=("s", "rstd"), u8=("q",))), (_norm_bwd, dict(f4=("rstd", "dw"))),
+         (_glu, dict(f4=("sA", "sBg", "sBu"), u8=("A", "Bg", "Bu"), b2=("gu",))),
+         (_glu_fast, dict(f4=("sA", "sBg", "sBu"), u8=("A", "Bg", "Bu"), b2=("gu",))),
+         (_glu_codes, dict(f4=("sA", "sBg", "sBu", "Hs"), u8=("A", "Bg", "Bu", "H"), b2=("gu",))),
+         (_glu_bwd, dict(f4=("Ds", "Dst", "Hst"), u8=("D", "Dt", "Ht"), b2=("gu",))),
+         (_few, dict(f4=("sA", "sB"), u8=("A", "B")))]
+WRONG = dict(f4=(B16, F32.double(), F32.half()), u8=(B16, F32), b2=(F32, F32.half(), U8))
+
+
+@pytest.mark.parametrize("call,arg,kind", [(c, a, k) for c, kinds in TYPED for k, args in kinds.items() for a in args])
+def test_operands_of_a_fixed_type(fq, call, arg, kind):
+    """An fp32 output given as a narrower tensor would be written past its end, another type misread: the binding refuses
+    it.  Every call here has no rows, which the library answers (EINVAL) once the types pass."""
+    for wrong in WRONG[kind]:
+        with pytest.raises(TypeError):
+            call(fq, **{arg: wrong})
+    right = dict(f4=(F32, FAKE), u8=(U8, U8.view(torch.int8), U8.view(torch.float8_e4m3fn), U8.view(torch.float8_e5m2), FAKE),
+                 b2=(B16, B16.view(torch.int16), FAKE))
+    for ok in right[kind]:
+        with pytest.raises(fq.Fp8qError):
+            call(fq, **{arg: ok})
