@@ -162,7 +162,9 @@ static void launch_f(const GluBwd& p, hipStream_t st) {
 }
 
 int launch_glu_bwd(const GluBwd& p, hipStream_t st) {
-  if (p.F / 128 * ((p.M + 127) / 128) > 0x7FFFFFFF) return fail(FP8Q_ESHAPE, "glu_bwd_q: more than 2^31-1 tiles");
+  // a launch holds fewer than 2^32 threads
+  if (p.F / 128 * ((p.M + 127) / 128) > 0xFFFFFFFFll / 512)
+    return fail(FP8Q_ESHAPE, "glu_bwd_q: more than 2^23-1 tiles of 128 x 128");
   if (p.dh_dt == FP8Q_F32) launch_f<FP8Q_F32>(p, st);
   else launch_f<FP8Q_BF16>(p, st);
   return check_launch("glu_bwd_q");

@@ -275,3 +275,11 @@ def test_operands_of_a_fixed_type(fq, call, arg, kind):
     for ok in right[kind]:
         with pytest.raises(fq.Fp8qError):
             call(fq, **{arg: ok})
+
+
+def test_glu_bwd_tiles_of_one_launch(fq):
+    """A launch holds fewer than 2^32 threads; at 512 a tile that is 2^23 - 1 tiles."""
+    F, M = 128 * 4096, 128 * 2048
+    kw = dict(lddh=F, ldgu=2 * F, lddq=2 * F, ld_ds=F // 64, Dt=None, Dst=None, Ht=None, Hst=None, F=F, M=M)
+    rc, msg = _call(fq, "fp8q_glu_bwd_q", GLU_BWD, kw)
+    assert rc == fq.ESHAPE and "tiles" in msg, (rc, msg)
