@@ -540,6 +540,7 @@ static void launch_f(const Proj& p, bool fast, const Cut& c, hipStream_t st) {
 static bool few_rows(int64_t M, int64_t F, bool fast) {
   const int64_t cu = grid_size();
   const int64_t groups = (M + 63) / 64, tiles = ((M + groups - 1) / groups + 15) / 16;
+  if (groups > 65535) return false;  // the second dimension of a launch
   int64_t wgs = groups * ((F + 15) / 16);
   if (wgs < cu) wgs = cu;
   return wgs * (120 + 58 * tiles) < cut_tiles(M, fast ? 256 : 128, (F + 127) / 128, 0).cost * cu;

@@ -34,3 +34,24 @@ def test_glu_q_on_an_explicit_stream_without_workspace(fq, gpu):
     with torch.cuda.stream(side):
         assert torch.empty(4 * M * F, dtype=torch.uint8, device=gpu).data_ptr() == p
     torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ very many rows
+def test_glu_of_very_many_rows_and_few_columns(fq, gpu):
+    """More groups of 64 rows than the 65535 a launch's second dimension holds: the rows repeat every 4096."""
+    F, K, n = 16, 128, 4096
+    M = 64 * 65535 + 65
+    base, sbase, B, sB = operands(gpu, n, F, K, seed=6)
+    A, sA = base.repeat(-(-M // n), 1)[:M], sbase.repeat(-(-M // n), 1)[:M]
+    a = base.view(torch.float8_e4m3fn).double() * sbase.double()
+    w = [b.view(torch.float8_e4m3fn).double() * s.double() for b, s in zip(B, sB)]
+    (g, Dg), (u, Du) = [(a @ x.t(), a.abs() @ x.abs().t()) for x in w]
+    want = g * torch.sigmoid(g) * u
+    for fn, rel in (("fp8q_glu_blockscaled", 1e-5), ("fp8q_glu_blockscaled_fast", 2.0 ** -10)):
+        h = torch.full((M, F), float("nan"), device=gpu)
+        glu_call(fq, fn, A, E4, sA, B, E4, sB, 0, h, None, M, F, K)
+        # as test_glu: |silu'| <= 1.13
+        tol = 1.13 * rel * Dg * (u.abs() + rel * Du) + (g * torch.sigmoid(g)).abs() * rel * Du + want.abs() * 600 * 2.0 ** -24
+        assert ((h[:n].double() - want).abs() <= tol + 1e-30).all()
+        full = M // n * n
+        assert (h[:full].view(-1, n, F) == h[:n]).all() and torch.equal(h[full:], h[:M - full])
