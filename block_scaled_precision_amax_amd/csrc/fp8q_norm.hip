@@ -112,12 +112,24 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_rmsnorm_1x128(const N
   }
 }
 
+// A launch holds fewer than 2^32 threads: more rows take several, one after
+// another (four rows a workgroup of 256: from 67 million rows on).
 template <int DT, int WDT, int TPR, int V>
 static void launch_fwd(const NormFwd& p, hipStream_t st) {
   constexpr int TH = TPR < 256 ? 256 : TPR, R = TH / TPR;
-  const dim3 grid((unsigned)((p.rows + R - 1) / R)), block(TH);
-  if (p.res) hipLaunchKernelGGL((k_rmsnorm_1x128<DT, WDT, TPR, V, true>), grid, block, 0, st, p);
-  else hipLaunchKernelGGL((k_rmsnorm_1x128<DT, WDT, TPR, V, false>), grid, block, 0, st, p);
+  constexpr int64_t most = 0xFFFFFFFFll / TH * R;
+  auto at = [](const void* v, int64_t bytes) { return v ? (char*)v + bytes : nullptr; };
+  for (int64_t r = 0; r < p.rows; r += most) {
+    NormFwd c = p;
+    const int es = DT == FP8Q_F32 ? 4 : 2;
+    c.rows = p.rows - r < most ? p.rows - r : most;
+    c.x = at(p.x, r * p.ldx * es), c.res = at(p.res, r * p.ldr * es);
+    c.z = at(p.z, r * p.ldz * es), c.y = at(p.y, r * p.ldy * es);
+    c.q = (uint8_t*)at(p.q, r * p.ldq), c.scales = (float*)at(p.scales, r * p.ld_s * 4), c.rstd = (float*)at(p.rstd, r * 4);
+    const dim3 grid((unsigned)((c.rows + R - 1) / R)), block(TH);
+    if (p.res) hipLaunchKernelGGL((k_rmsnorm_1x128<DT, WDT, TPR, V, true>), grid, block, 0, st, c);
+    else hipLaunchKernelGGL((k_rmsnorm_1x128<DT, WDT, TPR, V, false>), grid, block, 0, st, c);
+  }
 }
 
 template <int DT, int WDT>

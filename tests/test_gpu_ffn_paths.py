@@ -55,3 +55,24 @@ def test_glu_of_very_many_rows_and_few_columns(fq, gpu):
         assert ((h[:n].double() - want).abs() <= tol + 1e-30).all()
         full = M // n * n
         assert (h[:full].view(-1, n, F) == h[:n]).all() and torch.equal(h[full:], h[:M - full])
+
+
+def test_norm_of_very_many_rows(fq, gpu):
+    """More rows than one launch has threads for (four rows and 256 threads a workgroup, 2^32 threads): the rows repeat
+    every 4096, and so do their outputs."""
+    cols, n = 128, 4096
+    rows = (1 << 26) + 5
+    base = W.activation(n, cols, seed=3, factor=5.0, device=gpu, dtype=torch.bfloat16)
+    x = base.repeat(-(-rows // n), 1)[:rows]
+    w = 1 + W.normal((cols,), seed=6, device=gpu, std=0.1, dtype=torch.float32)
+
+    def run(x):
+        r = x.shape[0]
+        z, y = torch.zeros_like(x), torch.zeros_like(x)
+        q, s, rstd = torch.zeros(r, cols, dtype=torch.uint8, device=gpu), torch.zeros(r, 1, device=gpu), torch.zeros(r, device=gpu)
+        fq.fp8q_rmsnorm_1x128(x, cols, x, cols, w, r, cols, NEPS, z, cols, y, cols, E4, EPS, q, cols, s, 1, rstd)
+        return z, y, q, s, rstd
+
+    full = rows // n * n
+    for got, want in zip(run(x), run(base)):
+        assert (got[:full].view(-1, *want.shape) == want).all() and torch.equal(got[full:], want[:rows - full])
