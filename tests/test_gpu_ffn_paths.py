@@ -1,11 +1,12 @@
 """GPU checks of the feed-forward operators' paths that small shapes do not reach: explicit streams, the tiled kernels'
 epilogues, long reductions, many token blocks, very many rows.  Tolerances as in test_gpu_ffn.py.
 """
+import numpy as np
 import pytest
 import torch
 
 from block_scaled_precision_amax_amd import workloads as W
-from test_gpu_ffn import E4, E5, EPS, NEPS, glu_call, operands
+from test_gpu_ffn import BF, E4, E5, EPS, NEPS, U, act64, bwd_call, glu_call, operands
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +77,170 @@ def test_norm_of_very_many_rows(fq, gpu):
     full = rows // n * n
     for got, want in zip(run(x), run(base)):
         assert (got[:full].view(-1, *want.shape) == want).all() and torch.equal(got[full:], want[:rows - full])
+
+
+# ------------------------------------------------------------------ gated projection on tiles
+# Low tiles throughout, whole rounds of tall ones, and tall ones with the halves of the rest, ragged both ways.
+TILED = [(200, 4000, 512), (129, 4224, 384), (1025, 6144, 128), (2000, 4500, 1280), (300, 4097, 256), (513, 8191, 640)]
+
+
+def on_tiles(fq, M, F):
+    """The few-row kernel's output goes through a workspace, the tiles' does not."""
+    return fq.fp8q_glu_blockscaled_q_workspace(M, -(-F // 128) * 128) == 0
+
+
+@pytest.mark.parametrize("M,F,K", TILED)
+@pytest.mark.parametrize("fa", [E4, E5])
+@pytest.mark.parametrize("fb", [E4, E5])
+def test_glu_on_tiles(fq, orc, gpu, M, F, K, fa, fb):
+    assert on_tiles(fq, M, F)
+    i = TILED.index((M, F, K))
+    act, pad, Kb, Fb = (i + fa) % 2, 16 * ((i + fb) % 2), K // 128, -(-F // 128)
+    A, sA, B, sB = operands(gpu, M, F, K, fa, fb, pad, seed=M + F)
+    if i % 2:  # scales [K/128, rows]
+        sc = (sA.t().contiguous(), 1, M), (sB[0].t().contiguous(), sB[1].t().contiguous(), 1, Fb)
+    else:
+        sc = (sA, Kb, 1), (sB[0], sB[1], Kb, 1)
+    if pad:  # one matrix, passed as its halves
+        both = torch.cat(B)
+        W0, W1 = both, both[F:]
+    else:
+        W0, W1 = B
+    rows = np.array([r for r in (0, 1, 15, 63, 64, 127, 128, 191, 199, 255, 256, 299, 512, 1023, 1024, 1791, 1792, 1999) if r < M])
+    An, Bn = A[:, :K].cpu().numpy(), [b[:, :K].cpu().numpy() for b in B]
+    (g, Dg), (u, Du) = [orc.gemm_blockscaled(An, fa, sA.cpu().numpy(), Bn[j], fb, sB[j].cpu().numpy(), orc.GRAN_128x128, rows=rows)
+                        for j in (0, 1)]
+    g, u, Dg, Du = map(torch.from_numpy, (g, u, Dg, Du))
+    a64 = act64(act, g)
+    outs = []
+    for fn, rel in (("fp8q_glu_blockscaled", 1e-5), ("fp8q_glu_blockscaled_fast", 2.0 ** -10)):
+
+        def call(dt, ld, ldgu):
+            h = torch.full((M, ld), 7.0, dtype=dt, device=gpu)
+            gu = torch.full((M, ldgu), 7.0, dtype=torch.bfloat16, device=gpu) if ldgu else None
+            getattr(fq, fn)(A, fa, A.stride(0), *sc[0], W0, W1, fb, W0.stride(0), *sc[1], act, h, ld, gu, ldgu, M, F, K)
+            assert (h[:, F:] == 7).all() and (gu is None or (gu[:, 2 * F:] == 7).all())
+            return h[:, :F], None if gu is None else gu[:, :2 * F]
+
+        up8 = -(-F // 8) * 8
+        h, gu = call(torch.float32, F + 3 - F % 2, 2 * F + 5)  # rows of no alignment
+        for dt, ld, ldgu in ((torch.float32, up8, 2 * up8 + 8), (torch.bfloat16, up8, 0), (torch.bfloat16, F + 3 - F % 2, 2 * F)):
+            h2, gu2 = call(dt, ld, ldgu)
+            assert torch.equal(h2, h.to(dt)) and (gu2 is None or torch.equal(gu2, gu))
+        # as test_glu: |act'| <= 1.13, the exponential's argument is off by a few u of at most 176
+        tol = 1.13 * rel * Dg * (u.abs() + rel * Du) + a64.abs() * rel * Du + (a64 * u).abs() * 600 * U + 1e-30
+        assert ((h[rows].cpu().double() - a64 * u).abs() <= tol).all()
+        for k, (x, D) in enumerate(((g, Dg), (u, Du))):
+            assert ((gu[rows, k * F:(k + 1) * F].cpu().double() - x).abs() <= BF * x.abs() + 1.01 * rel * D).all()
+        assert h.isfinite().all() and gu.isfinite().all()
+        outs.append(h)
+    assert not torch.equal(*outs)  # the few-row kernel would give both forms the same bits
+
+
+@pytest.mark.parametrize("M,F,K", [(200, 4096, 256), (129, 4224, 384), (1025, 6144, 128), (2000, 4608, 1280)])
+@pytest.mark.parametrize("fc", [E4, E5])
+@pytest.mark.parametrize("fa,fb", [(E4, E4), (E5, E4), (E4, E5), (E5, E5)])
+def test_glu_q_on_tiles(fq, gpu, M, F, K, fc, fa, fb):
+    """The codes leave the tiles as the quantizer makes them of the fp32 output: zero blocks, blocks whose scale takes the
+    IEEE division and infinite ones among them, rows aligned to 16 bytes and to 4."""
+    assert on_tiles(fq, M, F)
+    A, sA, B, sB = operands(gpu, M, F, K, fa, fb, seed=M + fc)
+    A[7] = 0
+    sA[9] *= 1e-12
+    sA[M - 1] *= 1e15
+    sA[40] *= 1e22
+    act = (fa + fc) % 2
+    h, gu = torch.empty(M, F, device=gpu), torch.empty(M, 2 * F, dtype=torch.bfloat16, device=gpu)
+    glu_call(fq, "fp8q_glu_blockscaled", A, fa, sA, B, fb, sB, act, h, gu, M, F, K)
+    want, ws = torch.empty(M, F, dtype=torch.uint8, device=gpu), torch.empty(M, F // 128, device=gpu)
+    fq.fp8q_quantize_1x128(h, M, F, F, fc, EPS, want, F, ws, F // 128)
+    assert (want[7] & 0x7F == 0).all() and (ws[M - 1] > 2.0 ** 80).any() and ws[40].isinf().any()
+    for off, save in ((0, True), (4, False)):
+        q = torch.full((M, F + 16 + off), 0xAA, dtype=torch.uint8, device=gpu)
+        s = torch.full((M, F // 128 + 1), -7.0, device=gpu)
+        gu2 = torch.empty_like(gu) if save else None
+        glu_call(fq, None, A, fa, sA, B, fb, sB, act, q[:, off:], gu2, M, F, K, q=(fc, s))
+        assert torch.equal(q[:, off:off + F], want) and torch.equal(s[:, :-1], ws)
+        assert gu2 is None or torch.equal(gu2, gu)
+        assert (q[:, :off] == 0xAA).all() and (q[:, off + F:] == 0xAA).all() and (s[:, -1] == -7).all()
+
+
+@pytest.mark.parametrize("M,F,K", [(200, 4096, 256), (1025, 6144, 128)])
+def test_a_nan_on_tiles_stays_in_its_row_and_column(fq, gpu, M, F, K):
+    assert on_tiles(fq, M, F)
+    A, sA, B, sB = operands(gpu, M, F, K, seed=1)
+    A2, B2 = A.clone(), [b.clone() for b in B]
+    A2[3, 100] = 0x7F
+    B2[1][130, 5] = 0x7F  # up: column 130 alone
+    rows, cols = torch.arange(M, device=gpu) != 3, torch.arange(F, device=gpu) != 130
+    for fn in ("fp8q_glu_blockscaled", "fp8q_glu_blockscaled_fast"):
+        h0, h1 = torch.empty(M, F, device=gpu), torch.empty(M, F, device=gpu)
+        glu_call(fq, fn, A, E4, sA, B, E4, sB, 0, h0, None, M, F, K)
+        glu_call(fq, fn, A2, E4, sA, B2, E4, sB, 0, h1, None, M, F, K)
+        assert h1[3].isnan().all() and h1[:, 130].isnan().all() and torch.equal(h0[rows][:, cols], h1[rows][:, cols])
+    q, s = torch.empty(M, F, dtype=torch.uint8, device=gpu), torch.empty(M, F // 128, device=gpu)
+    glu_call(fq, None, A2, E4, sA, B2, E4, sB, 0, q, None, M, F, K, q=(E4, s))
+    blocks = torch.arange(F // 128, device=gpu) != 1
+    assert (q[3] == 0x7F).all() and s[3].isnan().all()
+    assert (q[:, 128:256] == 0x7F).all() and s[:, 1].isnan().all() and s[rows][:, blocks].isfinite().all()
+
+
+# ------------------------------------------------------------------ long reductions, many token blocks, the re-tiled product
+@pytest.mark.parametrize("M", [1, 20, 50])
+@pytest.mark.parametrize("fa,fb", [(E4, E4), (E5, E4), (E4, E5)])
+def test_few_rows_with_a_long_reduction(fq, orc, gpu, M, fa, fb):
+    """More K blocks than the few-row kernel keeps A scales for in LDS (160)."""
+    N, K, Kb = 40, 20608, 161
+    A, sA, B, sB = operands(gpu, M, N, K, fa, fb, pad=16, seed=M)
+    sb = (sB[0].repeat_interleave(128, 0)[:N] * torch.linspace(0.5, 2.0, N, device=gpu)[:, None]).contiguous()
+    An, Bn = A[:, :K].cpu().numpy(), [b[:, :K].cpu().numpy() for b in B]
+    for gb, s in ((2, sB[0]), (1, sb)):
+        C = torch.full((M, N), float("nan"), device=gpu)
+        fq.fp8q_gemm_blockscaled_few(A, fa, A.stride(0), sA, Kb, 1, B[0], fb, B[0].stride(0), s, gb, Kb, 1, C, N, M, N, K)
+        ref, D = orc.gemm_blockscaled(An, fa, sA.cpu().numpy(), Bn[0], fb, s.cpu().numpy(), gb)
+        assert (np.abs(C.cpu().numpy().astype(np.float64) - ref) <= 1e-5 * D).all()
+    h, gu = torch.full((M, N), float("nan"), device=gpu), torch.empty(M, 2 * N, dtype=torch.bfloat16, device=gpu)
+    glu_call(fq, "fp8q_glu_blockscaled", A, fa, sA, B, fb, sB, 1, h, gu, M, N, K)
+    (g, Dg), (u, Du) = [orc.gemm_blockscaled(An, fa, sA.cpu().numpy(), Bn[j], fb, sB[j].cpu().numpy(), orc.GRAN_128x128)
+                        for j in (0, 1)]
+    g, u, Dg, Du = map(torch.from_numpy, (g, u, Dg, Du))
+    a64, rel = act64(1, g), 1e-5
+    tol = 1.13 * rel * Dg * (u.abs() + rel * Du) + a64.abs() * rel * Du + (a64 * u).abs() * 600 * U + 1e-30
+    assert ((h.cpu().double() - a64 * u).abs() <= tol).all()
+    for k, (x, D) in enumerate(((g, Dg), (u, Du))):
+        assert ((gu[:, k * N:(k + 1) * N].cpu().double() - x).abs() <= BF * x.abs() + 1.01 * rel * D).all()
+
+
+@pytest.mark.parametrize("M,F", [(2177, 384), (2200, 512), (4100, 128)])
+def test_glu_bwd_of_many_token_blocks(fq, orc, gpu, M, F):
+    """More than the sixteen token blocks that are walked together, the last group ragged; exact values as in
+    test_glu_bwd_exact_values."""
+    g = torch.Generator().manual_seed(M)
+    dh = torch.randn(M, F, generator=g).bfloat16()
+    u = (torch.randn(M, F, generator=g) * 3).bfloat16()
+    gu = torch.cat([torch.full((M, F), 40.0, dtype=torch.bfloat16), u], 1)
+    D, Ds, Dt, Dts, Ht, Hts = bwd_call(fq, dh.to(gpu), gu.to(gpu), 0, E5, E4, M, F, pad=16)
+    d = torch.cat([dh.float() * u.float(), dh.float() * 40], 1)
+    padt = lambda t: np.ascontiguousarray(torch.nn.functional.pad(t.t(), (0, Dt.shape[1] - M)).numpy())  # noqa: E731
+    for q, s, v, fmt in ((D, Ds, d.numpy(), E5), (Dt, Dts, padt(d), E5), (Ht, Hts, padt(40 * u.float()), E4)):
+        wq, ws = orc.quantize_blocks(v, 1, 128, fmt)
+        assert np.array_equal(q.cpu().numpy(), wq) and np.array_equal(s.cpu().numpy(), ws)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1, 128), (100, 300, 256), (129, 4096, 384), (1000, 2200, 640)])
+@pytest.mark.parametrize("fa,fb", [(E4, E5), (E5, E5), (E5, E4)])
+@pytest.mark.parametrize("any_code", [False, True])
+def test_fast_product_is_the_same_on_either_tile_in_every_format(fq, gpu, M, N, K, fa, fb, any_code):
+    """Rows on 128-row tiles equal, bit for bit, those of a product with so many rows that it runs on 256-row tiles; with
+    every code among the operands, NaN and infinities are where they are there."""
+    big = 256 * (256 // -(-N // 256))
+    A, sA, B, sB = operands(gpu, max(M, big - 99), N, K, fa, fb, seed=N)
+    if any_code:
+        A, B = A.random_(0, 256), [b.random_(0, 256) for b in B]
+        A[M // 2:M // 2 + 1] = A[M // 2:M // 2 + 1] & 0x3F  # a row without either
+        B[0][N // 2:N // 2 + 1] = B[0][N // 2:N // 2 + 1] & 0x3F
+    C, D = torch.full((M, N), 7.0, device=gpu), torch.full((A.shape[0], N), 7.0, device=gpu)
+    for out, rows in ((C, M), (D, A.shape[0])):
+        fq.fp8q_gemm_blockscaled_fast(A, fa, K, sA, K // 128, 1, B[0], fb, K, sB[0], 2, K // 128, 1, out, N, rows, N, K)
+    assert torch.equal(C.isnan(), D[:M].isnan()) and torch.equal(C.nan_to_num(nan=0.5), D[:M].nan_to_num(nan=0.5))
+    assert C[M // 2, N // 2].isfinite() and (any_code or C.isfinite().all())
