@@ -1,5 +1,5 @@
 """GPU checks of the feed-forward operators' paths that small shapes do not reach: explicit streams, the tiled kernels'
-epilogues, long reductions, many token blocks, very many rows.  Tolerances as in test_gpu_ffn.py.
+epilogues, long reductions, many token blocks, very many rows, far rows.  Tolerances as in test_gpu_ffn.py.
 """
 import numpy as np
 import pytest
@@ -244,3 +244,73 @@ def test_fast_product_is_the_same_on_either_tile_in_every_format(fq, gpu, M, N, 
         fq.fp8q_gemm_blockscaled_fast(A, fa, K, sA, K // 128, 1, B[0], fb, K, sB[0], 2, K // 128, 1, out, N, rows, N, K)
     assert torch.equal(C.isnan(), D[:M].isnan()) and torch.equal(C.nan_to_num(nan=0.5), D[:M].nan_to_num(nan=0.5))
     assert C[M // 2, N // 2].isfinite() and (any_code or C.isfinite().all())
+
+
+# ------------------------------------------------------------------ offsets past 31 and 32 bits
+def far(t, ld, buf, at=0):
+    """t's rows `ld` elements apart in buf, from element `at` on."""
+    v = buf.view(t.dtype)[at:].as_strided(t.shape, (ld, 1))
+    v.copy_(t)
+    return v
+
+
+def test_products_of_operands_just_under_4_gib(fq, gpu):
+    """Rows so far apart that the operands span almost 4 GiB, outputs more: the results are those of adjacent rows."""
+    F, K, Kb = 4096, 256, 2
+    ldb, ldo = (0xFFFFFFFF - K) // (F - 1) // 16 * 16, 1 << 23
+    buf, out = torch.empty(1 << 32, dtype=torch.uint8, device=gpu), torch.empty(200 * ldo, dtype=torch.float32, device=gpu)
+    for M in (3, 200):
+        A, sA, B, sB = operands(gpu, M, F, K, seed=M)
+        lda = (0xFFFFFFFF - K) // (M - 1) // 16 * 16
+        assert (F - 1) * ldb > 0xF0000000 and (M - 1) * lda > 0xF0000000
+        Bf = [far(b, ldb, buf, j * K) for j, b in enumerate(B)]  # side by side in one buffer
+        Af = far(A, lda, torch.empty(1 << 32, dtype=torch.uint8, device=gpu))
+        for fn in ("fp8q_glu_blockscaled", "fp8q_glu_blockscaled_fast"):
+            h, hf = torch.empty(M, F, device=gpu), out.as_strided((M, F), (ldo, 1))
+            glu_call(fq, fn, A, E4, sA, B, E4, sB, 0, h, None, M, F, K)
+            glu_call(fq, fn, Af, E4, sA, Bf, E4, sB, 0, hf, None, M, F, K)
+            assert torch.equal(h, hf)
+        for name in ("fp8q_gemm_blockscaled_fast", "fp8q_gemm_blockscaled_few")[:1 if M > 64 else 2]:
+            C, Cf = torch.empty(M, F, device=gpu), out.as_strided((M, F), (ldo, 1))
+            for a, b, c in ((A, B[0], C), (Af, Bf[0], Cf)):
+                getattr(fq, name)(a, E4, a.stride(0), sA, Kb, 1, b, E4, b.stride(0), sB[0], 2, Kb, 1, c, c.stride(0), M, F, K)
+            assert torch.equal(C, Cf)
+        del Af
+
+
+def test_norm_and_gradients_of_rows_far_apart(fq, gpu):
+    """Row offsets past 2^32 bytes in every operand: the results are those of adjacent rows."""
+    rows, cols, ld = 300, 256, 1 << 23  # 5 GB of bf16
+    bufs = [torch.empty(rows * ld, dtype=torch.bfloat16, device=gpu) for _ in range(4)]
+    x, r, dy = (W.normal((rows, cols), seed=i, device=gpu, dtype=torch.bfloat16) for i in range(3))
+    w = torch.ones(cols, device=gpu)
+    xf, rf, zf, yf = (far(t, ld, b) for t, b in zip((x, r, x, x), bufs))
+
+    def norm(x, r, z, y):
+        q, s, rstd = torch.empty(rows, cols, dtype=torch.uint8, device=gpu), torch.empty(rows, 2, device=gpu), torch.empty(rows, device=gpu)
+        n = [t.stride(0) for t in (x, r, z, y)]
+        fq.fp8q_rmsnorm_1x128(x, n[0], r, n[1], w, rows, cols, NEPS, z, n[2], y, n[3], E4, EPS, q, cols, s, 2, rstd)
+        return z, y, q, s, rstd
+
+    got, want = norm(xf, rf, zf, yf), norm(x, r, torch.empty_like(x), torch.empty_like(x))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    rstd, dyf = want[4], far(dy, ld, bufs[0])
+    ws = torch.empty(fq.fp8q_rmsnorm_bwd_workspace(rows, cols) // 4, device=gpu)
+
+    def bwd(dy, z, dres, dx):
+        dw = torch.empty(cols, device=gpu)
+        n = [t.stride(0) for t in (dy, z, dres, dx)]
+        fq.fp8q_rmsnorm_bwd(dy, n[0], z, n[1], w, rstd, dres, n[2], rows, cols, dx, n[3], dw, ws, ws.numel() * 4)
+        return dx, dw
+
+    assert all(torch.equal(a, b) for a, b in zip(bwd(dyf, zf, rf, yf), bwd(dy, want[0], r, torch.empty_like(x))))
+    # the gated projection's gradient: dh and gu far apart, and its transposed codes
+    M, F = rows, cols // 2
+    dh, gu = dy[:, :F].contiguous(), r
+    plain = bwd_call(fq, dh, gu, 0, E5, E4, M, F)
+    ldt = 1 << 24
+    T = torch.empty(2 * F * ldt, dtype=torch.uint8, device=gpu).as_strided((2 * F, 384), (ldt, 1))
+    D, Ds, s = torch.empty(M, 2 * F, dtype=torch.uint8, device=gpu), torch.empty(M, 2, device=gpu), torch.empty(2 * F, 3, device=gpu)
+    dhf, guf = far(dh, ld, bufs[2]), far(gu, ld, bufs[3])
+    fq.fp8q_glu_bwd_q(dhf, ld, guf, ld, 0, E5, EPS, D, 2 * F, Ds, 2, T, ldt, s, 3, E4, None, 0, None, 0, M, F)
+    assert all(torch.equal(a, b) for a, b in zip((D, Ds, T, s), plain))
