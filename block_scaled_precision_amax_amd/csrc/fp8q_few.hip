@@ -8,7 +8,10 @@
 // With M <= 64 rows the weight's bytes are the work: each is read once, at
 // 2 M flop a byte, so the kernel is a stream of B through the matrix cores
 // (beyond 64 rows each group of up to 64 reads it again).  7168 x 18432: 22 us at
-// one row (6 TB/s), 37 at 48; the gated 18432 x 7168 at one row: 41 us.
+// one row (6 TB/s), 37 at 48; the gated 18432 x 7168 at one row: 41 us.  Every
+// workgroup reads all of A, from the L2, for its 16 or 32 columns: up to 32 rows
+// that is at most what it reads of B, at 48 it is half as much again, and there
+// 7168 columns also make 224 workgroups for 256 compute units.
 // A wavefront takes 16 rows of B (of Bg and of Bu) and a share of the blocks
 // of 128 K.  A compute unit asks for one 128-byte line at a time, whole or in
 // part, and a load that touches sixteen half lines costs sixteen requests

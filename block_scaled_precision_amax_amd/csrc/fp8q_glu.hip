@@ -17,7 +17,7 @@
 // tiles of 16 x 16: column tiles 0, 1 of g and 2, 3 of u.  Every P_kb is
 // folded into fp32 accumulators with one FMA per element.
 //
-// Measured at 16384 x 18432 x 7168: fast 3.55 ms (2440 TFLOP/s), 3.69 ms with g
+// Measured at 16384 x 18432 x 7168: fast 3.58 ms (2420 TFLOP/s), 3.74 ms with g
 // and u kept; the tiles' 56 blocks take 95 us of a tile's 103, bound by MFMA
 // and LDS issue, the rest is the epilogue.  Exact 4096 x 18432 x 7168: 1.81 ms
 // (1196 TFLOP/s), bound by the decodes beside the bf16 MFMAs.

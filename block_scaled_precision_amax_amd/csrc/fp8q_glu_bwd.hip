@@ -9,9 +9,9 @@
 // dW = [dg du]^T X) and, recomputed, the codes of h^T along tokens (the
 // operand of the down projection's weight gradient).  Nothing wide is
 // written: 6 bytes are read and 5 written per element of dh (bf16).  8192 x
-// 18432: 366 us, 4.5 TB/s; 65 vector instructions an element keep the ALUs
-// busy for 62% of that, and two workgroups a compute unit (their registers)
-// overlap only so much of the rest.
+// 18432: 390 us, 4.3 TB/s; 65 vector instructions an element keep the ALUs
+// busy for some 60% of that, and two workgroups a compute unit (their
+// registers and LDS) overlap only so much of the rest.
 //
 // A workgroup of 512 threads takes 128 tokens x 128 features, so both kinds
 // of block lie inside it.  Thread (rg, cl) holds tokens 4rg .. 4rg + 3 and

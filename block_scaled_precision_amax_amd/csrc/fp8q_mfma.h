@@ -59,10 +59,11 @@ __device__ __forceinline__ v4f mfma32(typename Op<H16>::v8 a, typename Op<H16>::
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// 1 / (1 + e^-x) by the hardware's base-2 exponential and reciprocal (each
-// within an fp32 step): off by at most (|x| + 3) 2^-24 of its value, where
-// the rounding of x log2(e) gives the first term.  e^-x passes to Inf below
-// x = -88 and the result to 0, its limit.
+// 1 / (1 + e^-x) by the hardware's base-2 exponential and reciprocal, each
+// within an fp32 step, 2 * 2^-24 of its value.  The product x log2(e) and its
+// rounded constant are off by 1.23 |x| 2^-24 in the exponent, the sum by
+// 2^-24: together (1.25 |x| + 5) 2^-24 of the result where that is normal
+// (x > -87).  Below, e^-x passes to Inf and the result to 0, its limit.
 __device__ __forceinline__ float sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.4426950408889634f));
 }

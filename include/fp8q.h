@@ -371,14 +371,16 @@ int fp8q_gemm_mx(const uint8_t* A, fp8q_format fa, int64_t lda, const uint8_t* s
  * cols % 128 == 0, cols <= 65536 (else FP8Q_ESHAPE); norm_eps > 0; every
  * pointer and row 16-B aligned (scales, rstd 4-B).  A row that holds a NaN
  * gives NaN scales and codes 0x7F; the fp32 sum of squares overflows to Inf
- * where |v| passes about 1e19, and such a row gives zeros (NaN at an Inf). */
+ * where its root passes 1.8e19, and such a row gives zeros (NaN at an Inf).
+ * Rows beyond what one launch has threads for (67 million up to 2048
+ * columns, 4 to 16 million beyond) take several launches; at most 2^31-1. */
 int fp8q_rmsnorm_1x128(const void* x, fp8q_dtype dt, int64_t ldx, const void* res, int64_t ldr, const void* w,
                        fp8q_dtype wdt, int64_t rows, int64_t cols, float norm_eps, void* z, int64_t ldz, void* y,
                        int64_t ldy, fp8q_format f, float eps, uint8_t* q, int64_t ldq, float* scales, int64_t ld_s,
                        float* rstd, void* stream);
 
 /* Bytes of workspace fp8q_rmsnorm_bwd needs for the weight's gradient (at
- * most 4096 bytes per column; 0 for sizes it refuses). */
+ * most 2048 bytes per column; 0 for sizes it refuses). */
 int64_t fp8q_rmsnorm_bwd_workspace(int64_t rows, int64_t cols);
 
 /* Gradients of fp8q_rmsnorm_1x128 (the quantization passed straight through):
@@ -406,7 +408,8 @@ int fp8q_rmsnorm_bwd(const void* dy, fp8q_dtype dt, int64_t lddy, const void* z,
  * its two halves.  H: M x F fp32 or bf16 at H[m*ldh + n].  gu (nullable):
  * g and u rounded to bf16 for the backward pass, M x 2F at gu[m*ldgu + n]
  * and gu[m*ldgu + F + n], ldgu >= 2F; H is made from the unrounded ones.
- * K % 128 == 0 (else FP8Q_ESHAPE); M, F >= 1; alignment as the GEMM. */
+ * K % 128 == 0 (else FP8Q_ESHAPE); M, F >= 1; alignment as the GEMM.  A, Bg
+ * and Bu each span less than 4 GiB (else FP8Q_ESHAPE), in the forms below too. */
 int fp8q_glu_blockscaled(const uint8_t* A, fp8q_format fa, int64_t lda, const float* sA, int64_t sA_sm,
                          int64_t sA_skb, const uint8_t* Bg, const uint8_t* Bu, fp8q_format fb, int64_t ldb,
                          const float* sBg, const float* sBu, int64_t sB_sn, int64_t sB_skb, fp8q_act act, void* H,
@@ -453,7 +456,8 @@ int64_t fp8q_glu_blockscaled_q_workspace(int64_t M, int64_t F);
  *     down projection's weight gradient.
  * Mp is M rounded up to a multiple of 128: the padding is written as zero
  * codes, so any M can be reduced over.  fc: format of D (E4M3FN or E5M2);
- * eps the amax clamp.  F % 128 == 0 (else FP8Q_ESHAPE); lddt, ldht >= Mp;
+ * eps the amax clamp.  F % 128 == 0 and fewer than 2^23 blocks of 128 x 128
+ * (else FP8Q_ESHAPE); lddt, ldht >= Mp;
  * dH, gu, Dq, Dt, Ht and their rows 16-B aligned. */
 int fp8q_glu_bwd_q(const void* dH, fp8q_dtype dt, int64_t lddh, const uint16_t* gu, int64_t ldgu, fp8q_act act,
                    fp8q_format fc, float eps, uint8_t* Dq, int64_t lddq, float* Ds, int64_t ld_ds, uint8_t* Dt,
@@ -462,7 +466,8 @@ int fp8q_glu_bwd_q(const void* dH, fp8q_dtype dt, int64_t lddh, const uint16_t* 
 
 /* fp8q_gemm_blockscaled for a few rows (1 <= M <= 64: single tokens, decoding
  * batches), where the bytes of B are the work.  Arguments, layout and error
- * bound as fp8q_gemm_blockscaled; more rows are FP8Q_ESHAPE. */
+ * bound as fp8q_gemm_blockscaled; more rows are FP8Q_ESHAPE, and so is an
+ * operand that spans 4 GiB or more. */
 int fp8q_gemm_blockscaled_few(const uint8_t* A, fp8q_format fa, int64_t lda, const float* sA, int64_t sA_sm,
                               int64_t sA_skb, const uint8_t* B, fp8q_format fb, int64_t ldb, const float* sB,
                               fp8q_gran gb, int64_t sB_sn, int64_t sB_skb, void* C, fp8q_dtype out_dt, int64_t ldc,
