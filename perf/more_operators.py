@@ -440,8 +440,8 @@ def _exact_act(x, act):
     if act == "relu":
         return torch.clamp(x, min=0), torch.sign(torch.clamp(x, min=0))
     if act == "gelu_erf":
-        # the normal distribution function and its density
-        p = torch.special.ndtr(x)
+        # the normal distribution function (by erfc: 1 + erf cancels in the lower tail) and its density
+        p = torch.erfc(-x / math.sqrt(2)) / 2
         return x * p, p + x * torch.exp(-x * x / 2) / math.sqrt(2 * math.pi)
     if act == "silu":
         p, dk = torch.sigmoid(x), 1.0
