@@ -21,7 +21,7 @@ OK, EINVAL, ESHAPE, EALIGN, EHIP, ENOTIMPL = range(6)
 F32, BF16 = 0, 1
 E4M3FN, E5M2 = 0, 1
 GRAN_TENSOR, GRAN_1x128, GRAN_128x128 = 0, 1, 2
-ACT_SILU, ACT_GELU = 0, 1
+ACT_SILU, ACT_GELU, ACT_NONE, ACT_RELU, ACT_GELU_ERF = range(5)
 MAX_FINITE = {E4M3FN: 448.0, E5M2: 57344.0}
 
 # every exported symbol declared in include/fp8q.h
@@ -56,6 +56,16 @@ SYMBOLS = (
     "fp8q_glu_blockscaled_q_workspace",
     "fp8q_glu_bwd_q",
     "fp8q_gemm_blockscaled_few",
+    "fp8q_layernorm_1x128",
+    "fp8q_layernorm_bwd_workspace",
+    "fp8q_layernorm_bwd",
+    "fp8q_linear_blockscaled",
+    "fp8q_linear_blockscaled_fast",
+    "fp8q_linear_blockscaled_q",
+    "fp8q_linear_blockscaled_q_fast",
+    "fp8q_linear_blockscaled_workspace",
+    "fp8q_linear_bwd_q_workspace",
+    "fp8q_linear_bwd_q",
 )
 
 
@@ -133,6 +143,22 @@ def lib() -> ctypes.CDLL:
                                      i64, vp, i64, i64, i64, vp]),
             "fp8q_gemm_blockscaled_few": (i32, [vp, i32, i64, vp, i64, i64, vp, i32, i64, vp, i32, i64, i64, vp, i32,
                                                 i64, i64, i64, i64, vp]),
+            "fp8q_layernorm_1x128": (i32, [vp, i32, i64, vp, i64, vp, vp, i32, i64, i64, f32, vp, i64, vp, i64, i32, f32,
+                                           vp, i64, vp, i64, vp, vp, vp]),
+            "fp8q_layernorm_bwd_workspace": (i64, [i64, i64]),
+            "fp8q_layernorm_bwd": (i32, [vp, i32, i64, vp, i64, vp, i32, vp, vp, vp, i64, i64, i64, vp, i64, vp, vp, vp,
+                                         i64, vp]),
+            "fp8q_linear_blockscaled_workspace": (i64, [i32, i32, i64, i64, i64]),
+            "fp8q_linear_bwd_q_workspace": (i64, [i64, i64]),
+            "fp8q_linear_bwd_q": (i32, [vp, i32, i64, vp, i64, i32, i32, f32, vp, i64, vp, i64, vp, i64, vp, i64, i32, vp,
+                                        i64, vp, i64, vp, i64, i64, vp, i64, vp]),
+            **{f"fp8q_linear_blockscaled{form}": (i32, [vp, i32, i64, vp, i64, i64, vp, i32, i64, vp, i64, i64, vp, i32, i32,
+                                                        vp, i64, vp, i32, i64, vp, i64, i64, i64, i64, vp, i64, vp])
+               for form in ("", "_fast")},
+            **{f"fp8q_linear_blockscaled_q{form}": (i32, [vp, i32, i64, vp, i64, i64, vp, i32, i64, vp, i64, i64, vp, i32,
+                                                          i32, i32, f32, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp, i64,
+                                                          vp])
+               for form in ("", "_fast")},
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -415,3 +441,123 @@ def fp8q_gemm_blockscaled_few(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, gb,
                               stream=None) -> None:
     _check(lib().fp8q_gemm_blockscaled_few(_codes(A), fa, lda, _f32(sA), sA_sm, sA_skb, _codes(B), fb, ldb, _f32(sB), gb,
                                            sB_sn, sB_skb, _ptr(C), _dt(C), ldc, M, N, K, _stream(stream, A)))
+
+
+
+_get_device = None
+
+
+def _place(stream, *operands):
+    """The device of the operands that are tensors (-1: all are raw pointers) and the stream's handle.  A host tensor's
+    address, or one of another device, would fault in the kernel: both are refused."""
+    dev, first = -1, operands[0]
+    for t in operands:
+        if t is None or isinstance(t, int):
+            continue
+        d = t.get_device()
+        if d < 0:
+            raise ValueError("this operand is not on a GPU")
+        if dev < 0:
+            dev, first = d, t
+        elif d != dev:
+            raise ValueError(f"these operands share one device, got cuda:{dev} and cuda:{d}")
+    return dev, _stream(stream, first)
+
+
+def _on(dev, call):
+    """call() with `dev` as the current device, on which kernels are launched."""
+    global _get_device
+    if _get_device is None:
+        import torch
+
+        _get_device = torch._C._cuda_getDevice
+    if dev < 0 or _get_device() == dev:
+        return call()
+    import torch
+
+    with torch.cuda.device(dev):
+        return call()
+
+
+def fp8q_layernorm_1x128(x, ldx, res, ldr, w, b, rows, cols, norm_eps, z, ldz, y, ldy, f, eps, q, ldq, scales, ld_s,
+                         mean=None, rstd=None, stream=None) -> None:
+    """w and b, of one dtype, may each be None (ones, zeros)."""
+    wdt = F32 if w is None and b is None else _same_dt(b if w is None else w, b)
+    args = (_ptr(x), _same_dt(x, res, z, y), ldx, _ptr(res), ldr, _ptr(w), _ptr(b), wdt, rows, cols, norm_eps, _ptr(z), ldz,
+            _ptr(y), ldy, f, eps, _codes(q), ldq, _f32(scales), ld_s, _f32(mean), _f32(rstd))
+    dev, handle = _place(stream, x, res, w, b, z, y, q, scales, mean, rstd)
+    _check(_on(dev, lambda: lib().fp8q_layernorm_1x128(*args, handle)))
+
+
+def fp8q_layernorm_bwd_workspace(rows, cols) -> int:
+    return lib().fp8q_layernorm_bwd_workspace(rows, cols)
+
+
+def fp8q_layernorm_bwd(dy, lddy, z, ldz, w, mean, rstd, dres, lddr, rows, cols, dx, lddx, dw=None, db=None, ws=None,
+                       ws_bytes=0, stream=None) -> None:
+    args = (_ptr(dy), _same_dt(dy, z, dres, dx), lddy, _ptr(z), ldz, _ptr(w), F32 if w is None else _dt(w), _f32(mean),
+            _f32(rstd), _ptr(dres), lddr, rows, cols, _ptr(dx), lddx, _f32(dw), _f32(db), _ptr(ws), ws_bytes)
+    dev, handle = _place(stream, dy, z, w, mean, rstd, dres, dx, dw, db, ws)
+    _check(_on(dev, lambda: lib().fp8q_layernorm_bwd(*args, handle)))
+
+
+def fp8q_linear_blockscaled_workspace(fast, codes, M, N, K) -> int:
+    return lib().fp8q_linear_blockscaled_workspace(fast, codes, M, N, K)
+
+
+def _linear(fn, fast, codes, args, sizes, ws, ws_bytes, stream, operands) -> None:
+    """A linear layer's call: args up to its sizes; without `ws`, what it needs comes from torch's allocator."""
+    dev, handle = _place(stream, *operands, ws)
+
+    def call():
+        w, n = ws, ws_bytes
+        if w is None:
+            n = lib().fp8q_linear_blockscaled_workspace(fast, codes, *sizes)
+            if n:
+                w = _workspace(n, handle, stream, next((t for t in operands if t is not None and not isinstance(t, int)), 0))
+        return fn(*args, *sizes, _ptr(w), n, handle)
+
+    _check(_on(dev, call))
+
+
+def fp8q_linear_blockscaled(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, sB_sn, sB_skb, bias, act, res, ldr, C, ldc, pre,
+                            ldpre, M, N, K, ws=None, ws_bytes=0, stream=None) -> None:
+    """Without `ws`, the workspace of a call of few tiles comes from torch's allocator; so in the forms below."""
+    args = (_codes(A), fa, lda, _f32(sA), sA_sm, sA_skb, _codes(B), fb, ldb, _f32(sB), sB_sn, sB_skb, _ptr(bias),
+            F32 if bias is None else _dt(bias), act, _ptr(res), ldr, _ptr(C), _same_dt(C, res), ldc, _bf16(pre), ldpre)
+    _linear(lib().fp8q_linear_blockscaled, 0, 0, args, (M, N, K), ws, ws_bytes, stream, (A, sA, B, sB, bias, res, C, pre))
+
+
+def fp8q_linear_blockscaled_fast(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, sB_sn, sB_skb, bias, act, res, ldr, C, ldc,
+                                 pre, ldpre, M, N, K, ws=None, ws_bytes=0, stream=None) -> None:
+    args = (_codes(A), fa, lda, _f32(sA), sA_sm, sA_skb, _codes(B), fb, ldb, _f32(sB), sB_sn, sB_skb, _ptr(bias),
+            F32 if bias is None else _dt(bias), act, _ptr(res), ldr, _ptr(C), _same_dt(C, res), ldc, _bf16(pre), ldpre)
+    _linear(lib().fp8q_linear_blockscaled_fast, 1, 0, args, (M, N, K), ws, ws_bytes, stream,
+            (A, sA, B, sB, bias, res, C, pre))
+
+
+def fp8q_linear_blockscaled_q(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, sB_sn, sB_skb, bias, act, fc, eps, Cq, ldcq, Cs,
+                              ld_cs, pre, ldpre, M, N, K, ws=None, ws_bytes=0, stream=None) -> None:
+    args = (_codes(A), fa, lda, _f32(sA), sA_sm, sA_skb, _codes(B), fb, ldb, _f32(sB), sB_sn, sB_skb, _ptr(bias),
+            F32 if bias is None else _dt(bias), act, fc, eps, _codes(Cq), ldcq, _f32(Cs), ld_cs, _bf16(pre), ldpre)
+    _linear(lib().fp8q_linear_blockscaled_q, 0, 1, args, (M, N, K), ws, ws_bytes, stream, (A, sA, B, sB, bias, Cq, Cs, pre))
+
+
+def fp8q_linear_blockscaled_q_fast(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, sB_sn, sB_skb, bias, act, fc, eps, Cq,
+                                   ldcq, Cs, ld_cs, pre, ldpre, M, N, K, ws=None, ws_bytes=0, stream=None) -> None:
+    args = (_codes(A), fa, lda, _f32(sA), sA_sm, sA_skb, _codes(B), fb, ldb, _f32(sB), sB_sn, sB_skb, _ptr(bias),
+            F32 if bias is None else _dt(bias), act, fc, eps, _codes(Cq), ldcq, _f32(Cs), ld_cs, _bf16(pre), ldpre)
+    _linear(lib().fp8q_linear_blockscaled_q_fast, 1, 1, args, (M, N, K), ws, ws_bytes, stream,
+            (A, sA, B, sB, bias, Cq, Cs, pre))
+
+
+def fp8q_linear_bwd_q_workspace(M, N) -> int:
+    return lib().fp8q_linear_bwd_q_workspace(M, N)
+
+
+def fp8q_linear_bwd_q(dC, lddc, pre, ldpre, act, fc, eps, Dq, lddq, Ds, ld_ds, Dt, lddt, Dst, ld_dst, fh, Ht, ldht, Hst,
+                      ld_hst, dbias, M, N, ws=None, ws_bytes=0, stream=None) -> None:
+    args = (_ptr(dC), _dt(dC), lddc, _bf16(pre), ldpre, act, fc, eps, _codes(Dq), lddq, _f32(Ds), ld_ds, _codes(Dt), lddt,
+            _f32(Dst), ld_dst, fh, _codes(Ht), ldht, _f32(Hst), ld_hst, _f32(dbias), M, N, _ptr(ws), ws_bytes)
+    dev, handle = _place(stream, dC, pre, Dq, Ds, Dt, Dst, Ht, Hst, dbias, ws)
+    _check(_on(dev, lambda: lib().fp8q_linear_bwd_q(*args, handle)))

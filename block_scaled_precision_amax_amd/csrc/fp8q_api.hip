@@ -83,6 +83,15 @@ int check_norm(const char* fn, int dt, int wdt, int64_t rows, int64_t cols) {
   if (rows > 0x7FFFFFFF) return fail(FP8Q_ESHAPE, "%s: more than 2^31-1 rows", fn);
   return FP8Q_OK;
 }
+int check_layernorm(const char* fn, int dt, int wdt, int64_t rows, int64_t cols) {
+  if (!valid_dt(dt) || !valid_dt(wdt)) return fail(FP8Q_EINVAL, "%s: bad dtype", fn);
+  if (rows <= 0 || cols <= 0) return fail(FP8Q_EINVAL, "%s: rows and cols must be positive", fn);
+  if (cols % 8 != 0 || cols > kNormMaxCols)
+    return fail(FP8Q_ESHAPE, "%s: cols (%lld) must be a multiple of 8, at most %lld", fn, (long long)cols,
+                (long long)kNormMaxCols);
+  if (rows > 0x7FFFFFFF) return fail(FP8Q_ESHAPE, "%s: more than 2^31-1 rows", fn);
+  return FP8Q_OK;
+}
 struct NormRow {
   const void* p;
   int64_t ld;
@@ -115,6 +124,25 @@ int check_proj(const char* fn, const uint8_t* A, int fa, int64_t lda, const floa
     return fail(FP8Q_ESHAPE, "%s: an operand spans 4 GiB or more", fn);
   return FP8Q_OK;
 }
+// Shared checks of the linear layer's forms, C aside.
+int check_linear(const char* fn, bool fast, bool codes, const void* bias, int bias_dt, int act, const uint16_t* pre,
+                 int64_t ldpre, int64_t M, int64_t N, int64_t K, const void* ws, int64_t ws_bytes) {
+  if (act < FP8Q_ACT_SILU || act > FP8Q_ACT_GELU_ERF) return fail(FP8Q_EINVAL, "%s: bad activation", fn);
+  if (bias && !valid_dt(bias_dt)) return fail(FP8Q_EINVAL, "%s: bad dtype of the bias", fn);
+  if (pre && ldpre < N) return fail(FP8Q_EINVAL, "%s: leading dimension too small", fn);
+  if (!aligned(pre, 2) || (bias && !aligned(bias, esize(bias_dt)))) return fail(FP8Q_EALIGN, "%s: misaligned bias or pre", fn);
+  const int64_t need = linear_workspace(fast, codes, M, N, K);
+  if (need && (!ws || ws_bytes < need)) return fail(FP8Q_EINVAL, "%s: the workspace needs %lld bytes", fn, (long long)need);
+  if (need && !aligned(ws, 16)) return fail(FP8Q_EALIGN, "%s: ws must be 16-byte aligned", fn);
+  return FP8Q_OK;
+}
+bool rows_aligned(const void* p, int64_t row_bytes) { return aligned(p, 16) && row_bytes % 16 == 0; }
+Epilogue make_epilogue(const void* bias, int bias_dt, int act, uint16_t* pre, int64_t ldpre) {
+  Epilogue e = {};
+  e.bias = bias, e.bdt = bias_dt, e.act = act, e.pre = pre, e.ldpre = ldpre;
+  e.vp = rows_aligned(pre, 2 * ldpre);
+  return e;
+}
 int check_gu(const char* fn, int act, const uint16_t* gu, int64_t ldgu, int64_t F) {
   if (act != FP8Q_ACT_SILU && act != FP8Q_ACT_GELU) return fail(FP8Q_EINVAL, "%s: bad activation", fn);
   if (gu && ldgu < 2 * F) return fail(FP8Q_EINVAL, "%s: leading dimension too small", fn);
@@ -143,6 +171,42 @@ int glu_entry(const char* fn, bool fast, const uint8_t* A, int fa, int64_t lda, 
   Proj p = make_proj(A, fa, lda, sA, sA_sm, sA_skb, Bg, Bu, fb, ldb, sBg, sBu, FP8Q_GRAN_128x128, sB_sn, sB_skb, M, F, K);
   p.out = H, p.ldo = ldh, p.out_dt = out_dt, p.act = act, p.gu = gu, p.ldgu = ldgu;
   return launch_glu(p, fast, fn, S(stream));
+}
+int linear_entry(const char* fn, bool fast, const uint8_t* A, int fa, int64_t lda, const float* sA, int64_t sA_sm,
+                 int64_t sA_skb, const uint8_t* B, int fb, int64_t ldb, const float* sB, int64_t sB_sn, int64_t sB_skb,
+                 const void* bias, int bias_dt, int act, const void* res, int64_t ldr, void* C, int out_dt, int64_t ldc,
+                 uint16_t* pre, int64_t ldpre, int64_t M, int64_t N, int64_t K, void* ws, int64_t ws_bytes, void* stream) {
+  if (!C) return fail(FP8Q_EINVAL, "%s: null pointer", fn);
+  if (!valid_dt(out_dt)) return fail(FP8Q_EINVAL, "%s: bad dtype", fn);
+  if (int rc = check_proj(fn, A, fa, lda, sA, sA_sm, sA_skb, B, B, fb, ldb, sB, sB, sB_sn, sB_skb, M, N, K)) return rc;
+  if (ldc < N || (res && ldr < N)) return fail(FP8Q_EINVAL, "%s: leading dimension too small", fn);
+  const int64_t es = esize(out_dt);
+  if (!aligned(C, es) || !aligned(res, es)) return fail(FP8Q_EALIGN, "%s: misaligned C or residual", fn);
+  if (int rc = check_linear(fn, fast, false, bias, bias_dt, act, pre, ldpre, M, N, K, ws, ws_bytes)) return rc;
+  Proj p = make_proj(A, fa, lda, sA, sA_sm, sA_skb, B, nullptr, fb, ldb, sB, nullptr, FP8Q_GRAN_128x128, sB_sn, sB_skb, M, N, K);
+  p.out = C, p.ldo = ldc, p.out_dt = out_dt, p.ws = (float*)ws;
+  Epilogue e = make_epilogue(bias, bias_dt, act, pre, ldpre);
+  e.res = res, e.ldr = ldr;
+  e.vo = rows_aligned(C, ldc * es), e.vr = rows_aligned(res, ldr * es);
+  return launch_linear(p, e, fast, fn, S(stream));
+}
+int linear_q_entry(const char* fn, bool fast, const uint8_t* A, int fa, int64_t lda, const float* sA, int64_t sA_sm,
+                   int64_t sA_skb, const uint8_t* B, int fb, int64_t ldb, const float* sB, int64_t sB_sn, int64_t sB_skb,
+                   const void* bias, int bias_dt, int act, int fc, float eps, uint8_t* Cq, int64_t ldcq, float* Cs,
+                   int64_t ld_cs, uint16_t* pre, int64_t ldpre, int64_t M, int64_t N, int64_t K, void* ws,
+                   int64_t ws_bytes, void* stream) {
+  if (!Cq || !Cs) return fail(FP8Q_EINVAL, "%s: null pointer", fn);
+  if (!valid_fmt(fc)) return fail(FP8Q_EINVAL, "%s: bad format", fn);
+  if (!(eps > 0.0f) || !isfinite(eps)) return fail(FP8Q_EINVAL, "%s: eps must be finite and > 0", fn);
+  if (int rc = check_proj(fn, A, fa, lda, sA, sA_sm, sA_skb, B, B, fb, ldb, sB, sB, sB_sn, sB_skb, M, N, K)) return rc;
+  if (N % 128 != 0) return fail(FP8Q_ESHAPE, "%s: N (%lld) must be a multiple of 128", fn, (long long)N);
+  if (ldcq < N || ld_cs < N / 128) return fail(FP8Q_EINVAL, "%s: leading dimension too small", fn);
+  if (!aligned(Cq, 16) || ldcq % 16 != 0 || !aligned(Cs, 4))
+    return fail(FP8Q_EALIGN, "%s: Cq and its rows must be 16-byte aligned, Cs 4-byte", fn);
+  if (int rc = check_linear(fn, fast, true, bias, bias_dt, act, pre, ldpre, M, N, K, ws, ws_bytes)) return rc;
+  Proj p = make_proj(A, fa, lda, sA, sA_sm, sA_skb, B, nullptr, fb, ldb, sB, nullptr, FP8Q_GRAN_128x128, sB_sn, sB_skb, M, N, K);
+  p.out = Cq, p.ldo = ldcq, p.scales = Cs, p.ld_s = ld_cs, p.fc = fc, p.eps = eps, p.ws = (float*)ws;
+  return launch_linear(p, make_epilogue(bias, bias_dt, act, pre, ldpre), fast, fn, S(stream));
 }
 
 }  // namespace
@@ -573,7 +637,145 @@ int fp8q_gemm_blockscaled_few(const uint8_t* A, fp8q_format fa, int64_t lda, con
   if (!aligned(C, out_dt == FP8Q_F32 ? 4 : 2)) return fail(FP8Q_EALIGN, "%s: misaligned C", fn);
   Proj p = make_proj(A, fa, lda, sA, sA_sm, sA_skb, B, nullptr, fb, ldb, sB, nullptr, gb, sB_sn, sB_skb, M, N, K);
   p.out = C, p.ldo = ldc, p.out_dt = out_dt;
-  return launch_few(p, fn, S(stream));
+  return launch_few(p, nullptr, fn, S(stream));
+}
+
+int fp8q_layernorm_1x128(const void* x, fp8q_dtype dt, int64_t ldx, const void* res, int64_t ldr, const void* w,
+                         const void* b, fp8q_dtype wdt, int64_t rows, int64_t cols, float norm_eps, void* z, int64_t ldz,
+                         void* y, int64_t ldy, fp8q_format f, float eps, uint8_t* q, int64_t ldq, float* scales,
+                         int64_t ld_s, float* mean, float* rstd, void* stream) {
+  const char* fn = "layernorm_1x128";
+  if (!x || (!q && !y)) return fail(FP8Q_EINVAL, "%s: null pointer", fn);
+  if ((q == nullptr) != (scales == nullptr)) return fail(FP8Q_EINVAL, "%s: q and scales go together", fn);
+  if (!valid_fmt(f)) return fail(FP8Q_EINVAL, "%s: bad format", fn);
+  if (!(eps > 0.0f) || !isfinite(eps)) return fail(FP8Q_EINVAL, "%s: eps must be finite and > 0", fn);
+  if (!(norm_eps > 0.0f) || !isfinite(norm_eps)) return fail(FP8Q_EINVAL, "%s: norm_eps must be finite and > 0", fn);
+  if (int rc = check_layernorm(fn, dt, wdt, rows, cols)) return rc;
+  if (q && cols % 128 != 0) return fail(FP8Q_ESHAPE, "%s: cols (%lld) must be a multiple of 128 for codes", fn, (long long)cols);
+  const NormRow r[] = {{x, ldx}, {res, ldr}, {z, ldz}, {y, ldy}};
+  if (int rc = check_norm_rows(fn, r, 4, dt, cols)) return rc;
+  if (q && (ldq < cols || ld_s < cols / 128)) return fail(FP8Q_EINVAL, "%s: leading dimension smaller than the row", fn);
+  if (!aligned(w, 16) || !aligned(b, 16) || (q && (!aligned(q, 16) || ldq % 16 != 0)))
+    return fail(FP8Q_EALIGN, "%s: w, b, q and the rows of q must be 16-byte aligned", fn);
+  if (!aligned(scales, 4) || !aligned(mean, 4) || !aligned(rstd, 4))
+    return fail(FP8Q_EALIGN, "%s: scales, mean and rstd must be 4-byte aligned", fn);
+  LayerNormFwd p;
+  p.x = x, p.res = res, p.w = w, p.b = b, p.z = z, p.y = y, p.q = q, p.scales = scales, p.mean = mean, p.rstd = rstd;
+  p.ldx = ldx, p.ldr = ldr, p.ldz = ldz, p.ldy = ldy, p.ldq = ldq, p.ld_s = ld_s, p.rows = rows, p.cols = cols;
+  p.neps = norm_eps, p.qeps = eps, p.dt = dt, p.wdt = wdt, p.fmt = f;
+  return launch_layernorm_1x128(p, S(stream));
+}
+
+int64_t fp8q_layernorm_bwd_workspace(int64_t rows, int64_t cols) {
+  if (rows <= 0 || rows > 0x7FFFFFFF || cols <= 0 || cols % 8 != 0 || cols > kNormMaxCols) return 0;
+  return 8 * cols * layernorm_bwd_parts(rows, cols);
+}
+
+int fp8q_layernorm_bwd(const void* dy, fp8q_dtype dt, int64_t lddy, const void* z, int64_t ldz, const void* w,
+                       fp8q_dtype wdt, const float* mean, const float* rstd, const void* dres, int64_t lddr, int64_t rows,
+                       int64_t cols, void* dx, int64_t lddx, float* dw, float* db, void* ws, int64_t ws_bytes,
+                       void* stream) {
+  const char* fn = "layernorm_bwd";
+  if (!dy || !z || !mean || !rstd || !dx) return fail(FP8Q_EINVAL, "%s: null pointer", fn);
+  if (int rc = check_layernorm(fn, dt, wdt, rows, cols)) return rc;
+  const NormRow r[] = {{dy, lddy}, {z, ldz}, {dres, lddr}, {dx, lddx}};
+  if (int rc = check_norm_rows(fn, r, 4, dt, cols)) return rc;
+  const int64_t need = dw || db ? fp8q_layernorm_bwd_workspace(rows, cols) : 0;
+  if (need && (!ws || ws_bytes < need)) return fail(FP8Q_EINVAL, "%s: the workspace needs %lld bytes", fn, (long long)need);
+  if (!aligned(w, 16) || (need && !aligned(ws, 16))) return fail(FP8Q_EALIGN, "%s: w and ws must be 16-byte aligned", fn);
+  if (!aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dw, 4) || !aligned(db, 4))
+    return fail(FP8Q_EALIGN, "%s: mean, rstd, dw and db must be 4-byte aligned", fn);
+  LayerNormBwd p = {};
+  p.dy = dy, p.z = z, p.w = w, p.dres = dres, p.mean = mean, p.rstd = rstd, p.dx = dx, p.dw = dw, p.db = db;
+  p.ws = (float*)ws, p.lddy = lddy, p.ldz = ldz, p.lddr = lddr, p.lddx = lddx, p.rows = rows, p.cols = cols;
+  p.dt = dt, p.wdt = wdt;
+  return launch_layernorm_bwd(p, S(stream));
+}
+
+int fp8q_linear_blockscaled(const uint8_t* A, fp8q_format fa, int64_t lda, const float* sA, int64_t sA_sm, int64_t sA_skb,
+                            const uint8_t* B, fp8q_format fb, int64_t ldb, const float* sB, int64_t sB_sn, int64_t sB_skb,
+                            const void* bias, fp8q_dtype bias_dt, fp8q_act act, const void* res, int64_t ldr, void* C,
+                            fp8q_dtype out_dt, int64_t ldc, uint16_t* pre, int64_t ldpre, int64_t M, int64_t N, int64_t K,
+                            void* ws, int64_t ws_bytes, void* stream) {
+  return linear_entry("linear_blockscaled", false, A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, sB_sn, sB_skb, bias,
+                      bias_dt, act, res, ldr, C, out_dt, ldc, pre, ldpre, M, N, K, ws, ws_bytes, stream);
+}
+
+int fp8q_linear_blockscaled_fast(const uint8_t* A, fp8q_format fa, int64_t lda, const float* sA, int64_t sA_sm,
+                                 int64_t sA_skb, const uint8_t* B, fp8q_format fb, int64_t ldb, const float* sB,
+                                 int64_t sB_sn, int64_t sB_skb, const void* bias, fp8q_dtype bias_dt, fp8q_act act,
+                                 const void* res, int64_t ldr, void* C, fp8q_dtype out_dt, int64_t ldc, uint16_t* pre,
+                                 int64_t ldpre, int64_t M, int64_t N, int64_t K, void* ws, int64_t ws_bytes, void* stream) {
+  return linear_entry("linear_blockscaled_fast", true, A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, sB_sn, sB_skb, bias,
+                      bias_dt, act, res, ldr, C, out_dt, ldc, pre, ldpre, M, N, K, ws, ws_bytes, stream);
+}
+
+int fp8q_linear_blockscaled_q(const uint8_t* A, fp8q_format fa, int64_t lda, const float* sA, int64_t sA_sm,
+                              int64_t sA_skb, const uint8_t* B, fp8q_format fb, int64_t ldb, const float* sB,
+                              int64_t sB_sn, int64_t sB_skb, const void* bias, fp8q_dtype bias_dt, fp8q_act act,
+                              fp8q_format fc, float eps, uint8_t* Cq, int64_t ldcq, float* Cs, int64_t ld_cs,
+                              uint16_t* pre, int64_t ldpre, int64_t M, int64_t N, int64_t K, void* ws, int64_t ws_bytes,
+                              void* stream) {
+  return linear_q_entry("linear_blockscaled_q", false, A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, sB_sn, sB_skb, bias,
+                        bias_dt, act, fc, eps, Cq, ldcq, Cs, ld_cs, pre, ldpre, M, N, K, ws, ws_bytes, stream);
+}
+
+int fp8q_linear_blockscaled_q_fast(const uint8_t* A, fp8q_format fa, int64_t lda, const float* sA, int64_t sA_sm,
+                                   int64_t sA_skb, const uint8_t* B, fp8q_format fb, int64_t ldb, const float* sB,
+                                   int64_t sB_sn, int64_t sB_skb, const void* bias, fp8q_dtype bias_dt, fp8q_act act,
+                                   fp8q_format fc, float eps, uint8_t* Cq, int64_t ldcq, float* Cs, int64_t ld_cs,
+                                   uint16_t* pre, int64_t ldpre, int64_t M, int64_t N, int64_t K, void* ws,
+                                   int64_t ws_bytes, void* stream) {
+  return linear_q_entry("linear_blockscaled_q_fast", true, A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, sB_sn, sB_skb,
+                        bias, bias_dt, act, fc, eps, Cq, ldcq, Cs, ld_cs, pre, ldpre, M, N, K, ws, ws_bytes, stream);
+}
+
+int64_t fp8q_linear_blockscaled_workspace(int fast, int codes, int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0 || K % 128 != 0 || (codes && N % 128 != 0)) return 0;
+  if ((M - 1) * K + K > 0xFFFFFFFFll || (N - 1) * K + K > 0xFFFFFFFFll) return 0;
+  return linear_workspace(fast != 0, codes != 0, M, N, K);
+}
+
+int64_t fp8q_linear_bwd_q_workspace(int64_t M, int64_t N) {
+  if (M <= 0 || N <= 0 || N % 128 != 0 || M > (int64_t)1 << 31 || N > (int64_t)1 << 31) return 0;
+  const int64_t nm = (M + 127) / 128;
+  return nm > 1 ? 4 * nm * N : 0;
+}
+
+int fp8q_linear_bwd_q(const void* dC, fp8q_dtype dt, int64_t lddc, const uint16_t* pre, int64_t ldpre, fp8q_act act,
+                      fp8q_format fc, float eps, uint8_t* Dq, int64_t lddq, float* Ds, int64_t ld_ds, uint8_t* Dt,
+                      int64_t lddt, float* Dst, int64_t ld_dst, fp8q_format fh, uint8_t* Ht, int64_t ldht, float* Hst,
+                      int64_t ld_hst, float* dbias, int64_t M, int64_t N, void* ws, int64_t ws_bytes, void* stream) {
+  const char* fn = "linear_bwd_q";
+  if (!dC || !Dq || !Ds) return fail(FP8Q_EINVAL, "%s: null pointer", fn);
+  if ((Dt == nullptr) != (Dst == nullptr) || (Ht == nullptr) != (Hst == nullptr))
+    return fail(FP8Q_EINVAL, "%s: a transposed output needs both its codes and its scales (or neither)", fn);
+  if (!valid_dt(dt) || !valid_fmt(fc) || !valid_fmt(fh)) return fail(FP8Q_EINVAL, "%s: bad dtype or format", fn);
+  if (act < FP8Q_ACT_SILU || act > FP8Q_ACT_GELU_ERF) return fail(FP8Q_EINVAL, "%s: bad activation", fn);
+  if (!pre && (act != FP8Q_ACT_NONE || Ht))
+    return fail(FP8Q_EINVAL, "%s: an activation's gradient and its output need the pre-activations", fn);
+  if (!(eps > 0.0f) || !isfinite(eps)) return fail(FP8Q_EINVAL, "%s: eps must be finite and > 0", fn);
+  if (M <= 0 || N <= 0) return fail(FP8Q_EINVAL, "%s: M and N must be positive", fn);
+  if (N % 128 != 0) return fail(FP8Q_ESHAPE, "%s: N (%lld) must be a multiple of 128", fn, (long long)N);
+  // checked here too: the workspace's size is computed from them
+  if (M > (int64_t)1 << 31 || N > (int64_t)1 << 31) return fail(FP8Q_ESHAPE, "%s: more than 2^31 tokens or features", fn);
+  const int64_t Mp = (M + 127) / 128 * 128;
+  if (lddc < N || (pre && ldpre < N) || lddq < N || ld_ds < N / 128 || (Dt && (lddt < Mp || ld_dst < Mp / 128)) ||
+      (Ht && (ldht < Mp || ld_hst < Mp / 128)))
+    return fail(FP8Q_EINVAL, "%s: leading dimension too small", fn);
+  if (!rows_aligned(dC, lddc * esize(dt)) || (pre && !rows_aligned(pre, 2 * ldpre)) || !rows_aligned(Dq, lddq) ||
+      (Dt && !rows_aligned(Dt, lddt)) || (Ht && !rows_aligned(Ht, ldht)))
+    return fail(FP8Q_EALIGN, "%s: dC, pre, Dq, Dt, Ht and their rows must be 16-byte aligned", fn);
+  if (!aligned(Ds, 4) || !aligned(Dst, 4) || !aligned(Hst, 4) || !aligned(dbias, 4))
+    return fail(FP8Q_EALIGN, "%s: misaligned scales or bias gradient", fn);
+  const int64_t need = dbias ? fp8q_linear_bwd_q_workspace(M, N) : 0;
+  if (need && (!ws || ws_bytes < need)) return fail(FP8Q_EINVAL, "%s: the workspace needs %lld bytes", fn, (long long)need);
+  if (need && !aligned(ws, 16)) return fail(FP8Q_EALIGN, "%s: ws must be 16-byte aligned", fn);
+  LinearBwd p;
+  p.dc = dC, p.pre = pre, p.d = Dq, p.dt_ = Dt, p.ht = Ht, p.ds = Ds, p.dts = Dst, p.hts = Hst, p.dbias = dbias;
+  p.ws = (float*)ws, p.lddc = lddc, p.ldpre = ldpre, p.ldd = lddq, p.ld_ds = ld_ds, p.lddt = lddt, p.ld_dts = ld_dst;
+  p.ldht = ldht, p.ld_hts = ld_hst, p.M = M, p.N = N, p.eps = eps, p.dc_dt = dt, p.act = act, p.fc = fc, p.fh = fh;
+  return launch_linear_bwd(p, S(stream));
 }
 
 }  // extern "C"

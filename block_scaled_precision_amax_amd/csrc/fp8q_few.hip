@@ -47,7 +47,7 @@ static constexpr int kScaleBlocks = 160;
 // same 16 of u (GLU, NJ = 2), or 16 NJ columns.  RT tiles of 16 rows.  OUT:
 // FP8Q_F32 or FP8Q_BF16.
 template <int FA, int FB, int GB, bool GLU, int OUT, int NJ, int RT>
-__global__ __launch_bounds__(64 * kWaves) void k_few(const Proj p) {
+__global__ __launch_bounds__(64 * kWaves) void k_few(const Proj p, const Epilogue ep) {
   constexpr bool H16 = FA == FP8Q_E5M2 || FB == FP8Q_E5M2;
   constexpr int NS = GB == FP8Q_GRAN_1x128 ? 4 : 1;  // B scales of a lane's four columns
   using V8 = typename Op<H16>::v8;
@@ -210,6 +210,39 @@ __global__ __launch_bounds__(64 * kWaves) void k_few(const Proj p) {
     });
   }
   using T = std::conditional_t<OUT == FP8Q_F32, float, uint16_t>;
+  if constexpr (!GLU) {
+    // a linear layer's epilogue; four columns a lane, whatever their alignment
+    if (ep.bias) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int64_t c = clampn(col + 16 * j + e);
+          o[j][e] += ep.bdt == FP8Q_F32 ? ((const float*)ep.bias)[c] : bf_lo(((const uint16_t*)ep.bias)[c]);
+        }
+    }
+    if (ep.pre) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        if (col + 16 * j < p.N) store_row4(ep.pre + row * ep.ldpre + col + 16 * j, o[j], p.N - col - 16 * j, ep.vp);
+    }
+    with_linear_act(ep.act, [&](auto act) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][e] = linear_act<decltype(act)::value>(o[j][e]);
+    });
+    if (ep.res) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const T r = ((const T*)ep.res)[row * ep.ldr + clampn(col + 16 * j + e)];
+          if constexpr (OUT == FP8Q_F32) o[j][e] += r;
+          else o[j][e] += bf_lo(r);
+        }
+    }
+  }
   const bool vec = ((((uintptr_t)p.out) | (uintptr_t)(sizeof(T) * p.ldo)) & (4 * sizeof(T) - 1)) == 0;
 #pragma unroll
   for (int j = 0; j < (GLU ? 1 : NJ); ++j)
@@ -217,45 +250,48 @@ __global__ __launch_bounds__(64 * kWaves) void k_few(const Proj p) {
 }
 
 template <int FA, int FB, int GB, bool GLU, int OUT, int NJ, int RT>
-static void launch_rt(const Proj& p, hipStream_t st) {
+static void launch_rt(const Proj& p, const Epilogue& e, hipStream_t st) {
   constexpr int COLS = GLU ? 16 : 16 * NJ, ROWS = 16 * RT;
   hipLaunchKernelGGL((k_few<FA, FB, GB, GLU, OUT, NJ, RT>),
                      dim3((unsigned)((p.N + COLS - 1) / COLS), (unsigned)((p.M + ROWS - 1) / ROWS)), dim3(64 * kWaves), 0,
-                     st, p);
+                     st, p, e);
 }
 
 template <int FA, int FB, int GB, bool GLU, int OUT>
-static void launch_m(const Proj& p, hipStream_t st) {
+static void launch_m(const Proj& p, const Epilogue& e, hipStream_t st) {
   // a plain product of more than 16 rows shares each tile of A among 32
   // columns; beyond 64 rows, equal groups of up to 64 each read the weight
   const int64_t groups = (p.M + 63) / 64, rows = (p.M + groups - 1) / groups;
-  if (p.M <= 16) launch_rt<FA, FB, GB, GLU, OUT, GLU ? 2 : 1, 1>(p, st);
-  else if (rows <= 32) launch_rt<FA, FB, GB, GLU, OUT, 2, 2>(p, st);
-  else if (rows <= 48) launch_rt<FA, FB, GB, GLU, OUT, 2, 3>(p, st);
-  else launch_rt<FA, FB, GB, GLU, OUT, 2, 4>(p, st);
+  if (p.M <= 16) launch_rt<FA, FB, GB, GLU, OUT, GLU ? 2 : 1, 1>(p, e, st);
+  else if (rows <= 32) launch_rt<FA, FB, GB, GLU, OUT, 2, 2>(p, e, st);
+  else if (rows <= 48) launch_rt<FA, FB, GB, GLU, OUT, 2, 3>(p, e, st);
+  else launch_rt<FA, FB, GB, GLU, OUT, 2, 4>(p, e, st);
 }
 
 template <int FA, int FB>
-static void launch_f(const Proj& p, hipStream_t st) {
+static void launch_f(const Proj& p, const Epilogue& e, hipStream_t st) {
   constexpr int BLK = FP8Q_GRAN_128x128;
   const bool f32 = p.out_dt == FP8Q_F32;
   if (p.B1) {
-    if (f32) launch_m<FA, FB, BLK, true, FP8Q_F32>(p, st);
-    else launch_m<FA, FB, BLK, true, FP8Q_BF16>(p, st);
+    if (f32) launch_m<FA, FB, BLK, true, FP8Q_F32>(p, e, st);
+    else launch_m<FA, FB, BLK, true, FP8Q_BF16>(p, e, st);
   } else if (p.gb == FP8Q_GRAN_1x128) {
-    if (f32) launch_m<FA, FB, FP8Q_GRAN_1x128, false, FP8Q_F32>(p, st);
-    else launch_m<FA, FB, FP8Q_GRAN_1x128, false, FP8Q_BF16>(p, st);
+    if (f32) launch_m<FA, FB, FP8Q_GRAN_1x128, false, FP8Q_F32>(p, e, st);
+    else launch_m<FA, FB, FP8Q_GRAN_1x128, false, FP8Q_BF16>(p, e, st);
   } else {
-    if (f32) launch_m<FA, FB, BLK, false, FP8Q_F32>(p, st);
-    else launch_m<FA, FB, BLK, false, FP8Q_BF16>(p, st);
+    if (f32) launch_m<FA, FB, BLK, false, FP8Q_F32>(p, e, st);
+    else launch_m<FA, FB, BLK, false, FP8Q_BF16>(p, e, st);
   }
 }
 
-int launch_few(const Proj& p, const char* what, hipStream_t st) {
-  if (p.fa == FP8Q_E4M3FN && p.fb == FP8Q_E4M3FN) launch_f<0, 0>(p, st);
-  else if (p.fa == FP8Q_E5M2 && p.fb == FP8Q_E4M3FN) launch_f<1, 0>(p, st);
-  else if (p.fa == FP8Q_E4M3FN) launch_f<0, 1>(p, st);
-  else launch_f<1, 1>(p, st);
+int launch_few(const Proj& p, const Epilogue* ep, const char* what, hipStream_t st) {
+  Epilogue e = {};
+  e.act = FP8Q_ACT_NONE;
+  if (ep) e = *ep;
+  if (p.fa == FP8Q_E4M3FN && p.fb == FP8Q_E4M3FN) launch_f<0, 0>(p, e, st);
+  else if (p.fa == FP8Q_E5M2 && p.fb == FP8Q_E4M3FN) launch_f<1, 0>(p, e, st);
+  else if (p.fa == FP8Q_E4M3FN) launch_f<0, 1>(p, e, st);
+  else launch_f<1, 1>(p, e, st);
   return check_launch(what);
 }
 

@@ -1,5 +1,6 @@
 // Declarations and device helpers shared by the feed-forward operators
-// (fp8q_norm.hip, fp8q_glu.hip, fp8q_glu_bwd.hip, fp8q_few.hip).
+// (fp8q_norm.hip, fp8q_layernorm.hip, fp8q_glu.hip, fp8q_linear.hip,
+// fp8q_glu_bwd.hip, fp8q_linear_bwd.hip, fp8q_few.hip).
 #pragma once
 
 #include "fp8q_internal.h"
@@ -130,6 +131,35 @@ int launch_rmsnorm_bwd(const NormBwd& p, hipStream_t st);
 // rows and columns writes (each a row of `cols` floats of the workspace).
 int64_t rmsnorm_bwd_parts(int64_t rows, int64_t cols);
 
+// w, b: nullable (ones, zeros), both of type wdt.
+struct LayerNormFwd {
+  const void *x, *res, *w, *b;
+  void *z, *y;
+  uint8_t* q;
+  float *scales, *mean, *rstd;
+  int64_t ldx, ldr, ldz, ldy, ldq, ld_s, rows, cols;
+  float neps, qeps;
+  int dt, wdt, fmt;
+};
+// pw, pb, ldp: where the kernel leaves each workgroup's column sums (set by
+// the launch).
+struct LayerNormBwd {
+  const void *dy, *z, *w, *dres;
+  const float *mean, *rstd;
+  void* dx;
+  float *dw, *db, *ws, *pw, *pb;
+  int64_t lddy, ldz, lddr, lddx, rows, cols, ldp;
+  int dt, wdt;
+};
+int launch_layernorm_1x128(const LayerNormFwd& p, hipStream_t st);
+int launch_layernorm_bwd(const LayerNormBwd& p, hipStream_t st);
+// Partial rows of both column sums (2 * cols floats each) that a backward
+// call writes.
+int64_t layernorm_bwd_parts(int64_t rows, int64_t cols);
+// Column sums of a table of `parts` rows of `cols` floats (a multiple of
+// four), 16-byte aligned: the first `split` columns to a, the rest to b.
+void launch_column_sums(const float* ws, int64_t parts, int64_t cols, int64_t split, float* a, float* b, hipStream_t st);
+
 // A gated projection (B1 the second matrix, act) or, with B1 null, a plain
 // product; N output columns.  The output is out_dt elements, or codes of
 // format fc with scales when `scales` is given (ws: see glu_q_workspace); gu
@@ -144,9 +174,24 @@ struct Proj {
   float eps;
   int fa, fb, gb, act, out_dt, fc;
 };
+// What a linear layer adds to its product, each part optional: a bias (bdt) of
+// any element alignment, an activation, the pre-activations kept as bf16 and a
+// residual of the output's type.  vo, vp, vr: whether the rows of the output,
+// of pre and of the residual are 16-byte aligned.
+struct Epilogue {
+  const void *bias, *res;
+  uint16_t* pre;
+  int64_t ldr, ldpre;
+  int bdt, act;
+  bool vo, vp, vr;
+};
 // Rows the product of a few rows takes at most.
 static constexpr int64_t kFewRows = 64;
-int launch_few(const Proj& p, const char* what, hipStream_t st);
+// e (nullable, plain products only): a linear layer's epilogue.
+int launch_few(const Proj& p, const Epilogue* e, const char* what, hipStream_t st);
+// The linear layer: p.out as out_dt, or codes and p.scales; p.ws as the workspace.
+int launch_linear(const Proj& p, const Epilogue& e, bool fast, const char* what, hipStream_t st);
+int64_t linear_workspace(bool fast, bool codes, int64_t M, int64_t N, int64_t K);
 int launch_glu(const Proj& p, bool fast, const char* what, hipStream_t st);
 // Bytes of fp32 workspace the quantized gated projection takes: its output
 // where the few-row kernel makes it, none otherwise.
@@ -167,5 +212,16 @@ struct GluBwd {
   int dh_dt, act, fc, fh;
 };
 int launch_glu_bwd(const GluBwd& p, hipStream_t st);
+
+struct LinearBwd {
+  const void* dc;
+  const uint16_t* pre;
+  uint8_t *d, *dt_, *ht;
+  float *ds, *dts, *hts, *dbias, *ws;
+  int64_t lddc, ldpre, ldd, ld_ds, lddt, ld_dts, ldht, ld_hts, M, N;
+  float eps;
+  int dc_dt, act, fc, fh;
+};
+int launch_linear_bwd(const LinearBwd& p, hipStream_t st);
 
 }  // namespace fp8q

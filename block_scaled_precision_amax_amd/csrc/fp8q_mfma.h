@@ -92,8 +92,74 @@ __device__ __forceinline__ float activation(float g) {
   float unused;
   return activation<ACT, false>(g, unused);
 }
+
+// The linear layer's activations: those two, none, ReLU, and GELU itself,
+// g * P(g) with P the normal distribution function.  For a = |g| and
+// Q(a) = 1 - P(a): Q = exp(-a^2/2) t poly(t), t = 1 / (1 + 0.3 a), where the
+// polynomial is fitted to Q exp(a^2/2) / t for 0 <= a <= 14 (relative error
+// 2^-22.7, least maximum; Q is 0 in fp32 from 13.2 on), and P(g) = Q for g < 0, 1 - Q
+// otherwise, so neither tail cancels.  With the hardware's exponential and
+// reciprocal Q is off by (1.5 g^2 + 16) 2^-24 of its value: g^2 log2(e)/2 is
+// rounded twice and its constant once, the rest are a dozen roundings.
+//
+// Where an activation passes nothing on (ReLU's negative side) its gradient is
+// 0 whatever arrives, Inf and NaN included; NaN pre-activations stay NaN.
+// linear_act gives act(g); linear_act_bwd dc * act'(g), and h = act(g).
+__device__ __forceinline__ float normal_cdf(float g, float& e) {
+  const float a = __builtin_fabsf(g), t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3f, a, 1.0f));
+  e = __builtin_amdgcn_exp2f(g * g * -0.72134752044448170f);
+  float r = 0.03567475825548172f;
+  r = __builtin_fmaf(r, t, -0.15720301866531372f);
+  r = __builtin_fmaf(r, t, 0.20635339617729187f);
+  r = __builtin_fmaf(r, t, -0.05368354171514511f);
+  r = __builtin_fmaf(r, t, 0.1285615712404251f);
+  r = __builtin_fmaf(r, t, 0.09991350769996643f);
+  r = __builtin_fmaf(r, t, 0.1207539513707161f);
+  r = __builtin_fmaf(r, t, 0.11962930113077164f);
+  const float q = e * (r * t);
+  return g < 0.0f ? q : 1.0f - q;
+}
+template <int ACT>
+__device__ __forceinline__ float linear_act(float g) {
+  if constexpr (ACT == FP8Q_ACT_NONE) return g;
+  else if constexpr (ACT == FP8Q_ACT_RELU) return g <= 0.0f ? 0.0f : g;
+  else if constexpr (ACT == FP8Q_ACT_GELU_ERF) {
+    float e;
+    return g * normal_cdf(g, e);
+  } else return activation<ACT>(g);
+}
+template <int ACT>
+__device__ __forceinline__ float linear_act_bwd(float dc, float g, float& h) {
+  if constexpr (ACT == FP8Q_ACT_NONE) {
+    h = g;
+    return dc;
+  } else if constexpr (ACT == FP8Q_ACT_RELU) {
+    h = linear_act<ACT>(g);
+    return g <= 0.0f ? 0.0f : dc;
+  } else if constexpr (ACT == FP8Q_ACT_GELU_ERF) {
+    float e;
+    const float p = normal_cdf(g, e), d = e * 0.3989422804014327f;
+    h = g * p;
+    return dc * (d == 0.0f ? p : __builtin_fmaf(g, d, p));  // g may be Inf where the density is 0
+  } else {
+    float da;
+    h = activation<ACT, true>(g, da);
+    return dc * da;
+  }
+}
 // f with the activation as a constant: the choice is made once around a
 // loop, so that the exponentials of its elements overlap.
+template <typename F>
+__device__ __forceinline__ void with_linear_act(int act, F f) {
+  switch (act) {
+    case FP8Q_ACT_SILU: f(std::integral_constant<int, FP8Q_ACT_SILU>{}); break;
+    case FP8Q_ACT_GELU: f(std::integral_constant<int, FP8Q_ACT_GELU>{}); break;
+    case FP8Q_ACT_RELU: f(std::integral_constant<int, FP8Q_ACT_RELU>{}); break;
+    case FP8Q_ACT_GELU_ERF: f(std::integral_constant<int, FP8Q_ACT_GELU_ERF>{}); break;
+    default: f(std::integral_constant<int, FP8Q_ACT_NONE>{}); break;
+  }
+}
+// The same for the gated projection's two.
 template <typename F>
 __device__ __forceinline__ void with_activation(int act, F f) {
   if (act == FP8Q_ACT_SILU) f(std::integral_constant<int, FP8Q_ACT_SILU>{});

@@ -60,9 +60,17 @@ typedef enum { FP8Q_GRAN_TENSOR = 0, FP8Q_GRAN_1x128 = 1, FP8Q_GRAN_128x128 = 2 
  * average smoothing the amax, as Transformer Engine does; [A] 4.3). */
 typedef enum { FP8Q_STAT_MAX = 0, FP8Q_STAT_MEAN = 1, FP8Q_STAT_EMA = 2 } fp8q_window_stat;
 
-/* Activation of the gated projection: SiLU g / (1 + e^-g), or GELU in its
- * tanh form g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2. */
-typedef enum { FP8Q_ACT_SILU = 0, FP8Q_ACT_GELU = 1 } fp8q_act;
+/* Activations: SiLU g / (1 + e^-g) and GELU in its tanh form
+ * g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 (the gated projection and
+ * the linear layer); none, ReLU and GELU itself, g (1 + erf(g / sqrt(2))) / 2
+ * (the linear layer alone). */
+typedef enum {
+  FP8Q_ACT_SILU = 0,
+  FP8Q_ACT_GELU = 1,
+  FP8Q_ACT_NONE = 2,
+  FP8Q_ACT_RELU = 3,
+  FP8Q_ACT_GELU_ERF = 4
+} fp8q_act;
 
 /* Delayed-scaling state ([A] 4.2 DelayedScaler): a window of the last
  * `window` amax values and the scale derived from them.  Device-resident,
@@ -472,6 +480,142 @@ int fp8q_gemm_blockscaled_few(const uint8_t* A, fp8q_format fa, int64_t lda, con
                               int64_t sA_skb, const uint8_t* B, fp8q_format fb, int64_t ldb, const float* sB,
                               fp8q_gran gb, int64_t sB_sn, int64_t sB_skb, void* C, fp8q_dtype out_dt, int64_t ldc,
                               int64_t M, int64_t N, int64_t K, void* stream);
+
+/* Layer norm with the residual's addition and a 1x128 FP8 output, the input
+ * of the next block-scaled product ([A] 5.1: casts through a wide type between
+ * FP8 operations eat the gain; the statistics are fp32, [H] precision per op):
+ *   v = x + res (res NULL: v = x);  mean = mean_c(v);
+ *   rstd = 1 / sqrt(mean_c((v - mean)^2) + norm_eps);
+ *   y = (v - mean) * rstd * w + b;  q, scales = fp8q_quantize_1x128(y).
+ * v, both sums and y are fp32; z and y are rounded once, to the nearest even,
+ * when they are stored, and neither the norm nor the codes read the rounded
+ * values.
+ * x, res, z, y: rows x cols of dtype dt (row strides ldx, ldr, ldz, ldy).
+ * res, z, y, mean, rstd nullable; z is v (the residual stream), and may be x
+ * or res itself.  w (nullable: ones), b (nullable: zeros): cols elements of
+ * dtype wdt.  q nullable together with scales (y is then required): codes of
+ * format f at q[r*ldq + c], fp32 scales at scales[r*ld_s + c/128], ld_s >=
+ * cols/128; eps is their amax clamp.  mean, rstd: rows fp32, what
+ * fp8q_layernorm_bwd takes.
+ * cols % 8 == 0, with codes cols % 128 == 0, cols <= 65536 (else FP8Q_ESHAPE);
+ * norm_eps > 0; every pointer and row 16-B aligned (scales, mean, rstd 4-B).
+ * A row that holds an Inf or a NaN gives NaN throughout (codes 0x7F, NaN
+ * scales); where the fp32 sum of squares overflows (distances from the mean
+ * whose root sum of squares passes 1.8e19) rstd is 0 and y is b.  At most 2^31-1 rows. */
+int fp8q_layernorm_1x128(const void* x, fp8q_dtype dt, int64_t ldx, const void* res, int64_t ldr, const void* w,
+                         const void* b, fp8q_dtype wdt, int64_t rows, int64_t cols, float norm_eps, void* z, int64_t ldz,
+                         void* y, int64_t ldy, fp8q_format f, float eps, uint8_t* q, int64_t ldq, float* scales,
+                         int64_t ld_s, float* mean, float* rstd, void* stream);
+
+/* Bytes of workspace fp8q_layernorm_bwd needs for the gradients of weight and
+ * bias (at most 4096 bytes per column; 0 for sizes it refuses). */
+int64_t fp8q_layernorm_bwd_workspace(int64_t rows, int64_t cols);
+
+/* Gradients of fp8q_layernorm_1x128 (the quantization passed straight
+ * through):
+ *   xh = (z - mean) * rstd, t = dy * w,
+ *   dx = rstd * (t - mean_c(t) - xh * mean_c(t * xh)) + dres,
+ *   dw[c] = sum_r dy * xh,  db[c] = sum_r dy.
+ * dx is the gradient of x and of res alike.  dy, z, dres, dx: rows x cols of
+ * dtype dt; z is the forward's z (x itself without a residual), mean and rstd
+ * its statistics, w its weight (nullable: ones).  dres (nullable): the gradient
+ * that reaches v past the norm, on the residual stream; dx may be dy or dres
+ * itself.  dw, db: cols fp32, overwritten; each NULL skips it (both: ws is
+ * unused).  ws: ws_bytes >= fp8q_layernorm_bwd_workspace, 16-B aligned,
+ * overwritten; calls in flight must not share it.  Sums are fp32, in an order
+ * fixed by rows and cols alone.  Sizes and alignment as fp8q_layernorm_1x128
+ * without codes. */
+int fp8q_layernorm_bwd(const void* dy, fp8q_dtype dt, int64_t lddy, const void* z, int64_t ldz, const void* w,
+                       fp8q_dtype wdt, const float* mean, const float* rstd, const void* dres, int64_t lddr, int64_t rows,
+                       int64_t cols, void* dx, int64_t lddx, float* dw, float* db, void* ws, int64_t ws_bytes,
+                       void* stream);
+
+/* Linear layer: the product of fp8q_gemm_blockscaled with what a layer does
+ * to it in the same kernel,
+ *   v[m,n] = (A B^T)[m,n] + bias[n],   C[m,n] = act(v[m,n]) + res[m,n].
+ * A: M x K codes, 1x128 scales, B: N x K codes, 128x128 scales at
+ * [(n/128)*sB_sn + kb*sB_skb], as fp8q_gemm_blockscaled.  bias (nullable): N
+ * elements of dtype bias_dt (ignored without one), of any element alignment.
+ * act: any fp8q_act.  res (nullable): M x N of C's dtype, row stride ldr; C
+ * may be res itself (the residual stream updated in place).  C: M x N fp32 or
+ * bf16 at C[m*ldc + n].  pre (nullable): v rounded to bf16 for
+ * fp8q_linear_bwd_q, M x N, row stride ldpre >= N; C is made from the unrounded v.
+ * Everything behind the product is fp32; C is rounded once.  ReLU keeps NaN;
+ * SiLU and both GELUs give NaN at -Inf.
+ * ws: ws_bytes >= fp8q_linear_blockscaled_workspace, 16-B aligned,
+ * overwritten; NULL where that is 0.  Calls in flight must not share it.
+ * The order of every sum is fixed by M, N and K alone.
+ * K % 128 == 0 (else FP8Q_ESHAPE); M, N >= 1; alignment as the GEMM; C, res
+ * and pre aligned to their elements.  A and B each span less than 4 GiB (else
+ * FP8Q_ESHAPE), in the forms below too. */
+int fp8q_linear_blockscaled(const uint8_t* A, fp8q_format fa, int64_t lda, const float* sA, int64_t sA_sm, int64_t sA_skb,
+                            const uint8_t* B, fp8q_format fb, int64_t ldb, const float* sB, int64_t sB_sn, int64_t sB_skb,
+                            const void* bias, fp8q_dtype bias_dt, fp8q_act act, const void* res, int64_t ldr, void* C,
+                            fp8q_dtype out_dt, int64_t ldc, uint16_t* pre, int64_t ldpre, int64_t M, int64_t N, int64_t K,
+                            void* ws, int64_t ws_bytes, void* stream);
+
+/* The same on the FP8 matrix cores (twice the rate), the product within the
+ * bound of fp8q_gemm_blockscaled_fast; a few rows, which the weight's bytes
+ * bound, may be computed exactly here too. */
+int fp8q_linear_blockscaled_fast(const uint8_t* A, fp8q_format fa, int64_t lda, const float* sA, int64_t sA_sm,
+                                 int64_t sA_skb, const uint8_t* B, fp8q_format fb, int64_t ldb, const float* sB,
+                                 int64_t sB_sn, int64_t sB_skb, const void* bias, fp8q_dtype bias_dt, fp8q_act act,
+                                 const void* res, int64_t ldr, void* C, fp8q_dtype out_dt, int64_t ldc, uint16_t* pre,
+                                 int64_t ldpre, int64_t M, int64_t N, int64_t K, void* ws, int64_t ws_bytes, void* stream);
+
+/* fp8q_linear_blockscaled with act(v) as 1x128 codes of format fc, the input
+ * of the next product: what fp8q_quantize_1x128 makes of the fp32 act(v).
+ * Cq: M x N codes (ldcq >= N), Cs: [M, N/128] fp32 (ld_cs >= N/128); eps the
+ * amax clamp.  N % 128 == 0 as well (else FP8Q_ESHAPE); Cq and its rows 16-B
+ * aligned. */
+int fp8q_linear_blockscaled_q(const uint8_t* A, fp8q_format fa, int64_t lda, const float* sA, int64_t sA_sm,
+                              int64_t sA_skb, const uint8_t* B, fp8q_format fb, int64_t ldb, const float* sB,
+                              int64_t sB_sn, int64_t sB_skb, const void* bias, fp8q_dtype bias_dt, fp8q_act act,
+                              fp8q_format fc, float eps, uint8_t* Cq, int64_t ldcq, float* Cs, int64_t ld_cs,
+                              uint16_t* pre, int64_t ldpre, int64_t M, int64_t N, int64_t K, void* ws, int64_t ws_bytes,
+                              void* stream);
+
+/* The same on the FP8 matrix cores, as fp8q_linear_blockscaled_fast. */
+int fp8q_linear_blockscaled_q_fast(const uint8_t* A, fp8q_format fa, int64_t lda, const float* sA, int64_t sA_sm,
+                                   int64_t sA_skb, const uint8_t* B, fp8q_format fb, int64_t ldb, const float* sB,
+                                   int64_t sB_sn, int64_t sB_skb, const void* bias, fp8q_dtype bias_dt, fp8q_act act,
+                                   fp8q_format fc, float eps, uint8_t* Cq, int64_t ldcq, float* Cs, int64_t ld_cs,
+                                   uint16_t* pre, int64_t ldpre, int64_t M, int64_t N, int64_t K, void* ws,
+                                   int64_t ws_bytes, void* stream);
+
+/* Bytes of workspace the linear layer's forms need: `fast` (0 or 1) for the
+ * _fast forms, `codes` for the _q forms.  0 for many rows, and for sizes they
+ * refuse.  The answer holds on the device that is current when it is asked. */
+int64_t fp8q_linear_blockscaled_workspace(int fast, int codes, int64_t M, int64_t N, int64_t K);
+
+/* Bytes of workspace fp8q_linear_bwd_q needs for the bias's gradient: 4*N for
+ * each 128 tokens, 0 up to 128 tokens (and for sizes it refuses). */
+int64_t fp8q_linear_bwd_q_workspace(int64_t M, int64_t N);
+
+/* Gradient of the linear layer at its pre-activations, quantized for the
+ * products that follow, with the bias's gradient and the layer's output again:
+ *   D = dC * act'(pre),  dbias[n] = sum_m D[m,n],  H = act(pre)   (fp32).
+ * (The residual's gradient is dC itself.)  From dC (M x N of dtype dt) and the
+ * forward's pre (may be NULL for FP8Q_ACT_NONE without Ht):
+ *   Dq, Ds: D as 1x128 codes along features, codes at Dq[m*lddq + n], scales
+ *     [M, N/128] (ld_ds): dA = D B is fp8q_gemm_blockscaled of Dq and the
+ *     weight stored [K, N];
+ *   Dt, Dst (nullable together): D^T as 1x128 codes along tokens, N x Mp at
+ *     Dt[n*lddt + m], scales [N, Mp/128] (ld_dst): dB = D^T A;
+ *   Ht, Hst (nullable together): H^T likewise, N x Mp, of format fh, for the
+ *     next layer's weight gradient;
+ *   dbias (nullable): N fp32, overwritten; sums in an order fixed by M and N.
+ * Mp is M rounded up to a multiple of 128: the padding is written as zero
+ * codes, so any M can be reduced over.  fc: format of D; eps the amax clamp.
+ * ReLU's gradient is 0 where pre <= 0, whatever dC holds there.
+ * ws: ws_bytes >= fp8q_linear_bwd_q_workspace where dbias is given, 16-B
+ * aligned, overwritten; calls in flight must not share it.
+ * N % 128 == 0 and fewer than 2^23 blocks of 128 x 128 (else FP8Q_ESHAPE);
+ * lddt, ldht >= Mp; dC, pre, Dq, Dt, Ht and their rows 16-B aligned. */
+int fp8q_linear_bwd_q(const void* dC, fp8q_dtype dt, int64_t lddc, const uint16_t* pre, int64_t ldpre, fp8q_act act,
+                      fp8q_format fc, float eps, uint8_t* Dq, int64_t lddq, float* Ds, int64_t ld_ds, uint8_t* Dt,
+                      int64_t lddt, float* Dst, int64_t ld_dst, fp8q_format fh, uint8_t* Ht, int64_t ldht, float* Hst,
+                      int64_t ld_hst, float* dbias, int64_t M, int64_t N, void* ws, int64_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
