@@ -255,15 +255,16 @@ def _run_own(st):
            "gelu_erf": fq.ACT_GELU_ERF}[c["act"]]
     M, N = c["M"], c["N"]
     if op == "linear":
-        K = c["K"]
+        # FP8 matrix instructions serve bf16 outputs: their sums drop products 2^-14 below their neighbours, which a value
+        # held in fp32 (a block's scale too) shows, so those come from the exact product
+        K, fast = c["K"], c["form"] == "fast" and c["dtype"] == "bf16"
         a = (st["A"], fq.E4M3FN, K, st["sA"], K // 128, 1, st["W"], fq.E4M3FN, K, st["sW"], K // 128, 1, st["bias"], act)
         pre = (st["pre"], st["pre"].stride(0) if c["save"] else 0)
         if c["form"].startswith("q"):
-            f = fq.fp8q_linear_blockscaled_q if c["form"] == "q" else fq.fp8q_linear_blockscaled_q_fast
-            f(*a, fq.E4M3FN, QEPS, st["h"], N, st["hs"], N // 128, *pre, M, N, K)
+            fq.fp8q_linear_blockscaled_q(*a, fq.E4M3FN, QEPS, st["h"], N, st["hs"], N // 128, *pre, M, N, K)
             r = {"h": st["h"].view(F8["e4m3"]), "s": st["hs"]}
         else:
-            f = fq.fp8q_linear_blockscaled if c["form"] == "exact" else fq.fp8q_linear_blockscaled_fast
+            f = fq.fp8q_linear_blockscaled_fast if fast else fq.fp8q_linear_blockscaled
             ld = st["h"].stride(0)
             f(*a, st["res"], ld, st["h"], ld, *pre, M, N, K)
             r = {"h": st["h"]}
