@@ -5,20 +5,22 @@
 //   P_kb   = sum over the 128 k of a block of dec(a) dec(b),
 //   C = act(v) + res  or  s, q = 1x128 codes of act(v);  pre = bf16(v) on request
 //
-// Three ways, by the cost of each: tiles with the epilogue behind their last
-// block; the same tiles with K cut into parts whose sums go to a workspace,
-// joined by a second kernel with the same epilogue, where there are too few
-// tiles for the compute units; and the few-row kernel (fp8q_few.hip).
+// Two ways, by the cost of each: the few-row kernel (fp8q_few.hip), and tiles
+// with the epilogue behind their last block, where the tiles that do not fill a
+// round of the compute units may have K cut into parts: their sums go to a
+// workspace and a second kernel joins them, with the same epilogue.
 #include "fp8q_tiles.h"
 
 namespace fp8q {
 
-// OUT of the kernels below: FP8Q_F32, FP8Q_BF16, 2 + format (1x128 codes) or
-// kPart, the bare sums as fp32 in the workspace.
-static constexpr int kPart = 4;
+// OUT of the kernels below: FP8Q_F32, FP8Q_BF16 or 2 + format (1x128 codes).
 
-// Row stride of a plane of the workspace.
-__host__ __device__ constexpr int64_t plane_ld(int64_t N) { return (N + 7) / 8 * 8; }
+// The tiles of a call: the first `full` of the ntm x ntn grid go through all of
+// K, the others (`rest`) in `parts` parts of it.
+struct Split {
+  int64_t ntm, ntn, full, rest;
+  int parts;
+};
 
 // Bias of eight columns, zeros past the last one or without a bias.
 __device__ __forceinline__ void load_bias8(const Epilogue& e, int64_t col, int64_t N, float (&b)[8]) {
@@ -89,45 +91,55 @@ __device__ __forceinline__ void finish8(const Proj& p, const Epilogue& e, int64_
   }
 }
 
-// Tiles of BM rows x 256 columns; with kPart, of `splits` parts of K.  The
-// sums pass through LDS as fp32, 128 columns at a time where both halves do
-// not fit, so that a lane then holds eight consecutive columns: its loads
-// and stores are 16 bytes and a block of codes lies in 16 lanes.  Chunk c
-// (four floats) of row r sits in slot c ^ (r & 15), free of bank conflicts
-// both ways.
+// Tiles of BM rows x 256 columns.  The sums of a whole tile pass through LDS as
+// fp32, 128 columns at a time where both halves do not fit, so that a lane then
+// holds eight consecutive columns: its loads and stores are 16 bytes and a
+// block of codes lies in 16 lanes.  Chunk c (four floats) of row r sits in slot
+// c ^ (r & 15), free of bank conflicts both ways.  The sums of a part leave as
+// the lanes hold them, a register of a wavefront in 1 KB of its tile's plane.
 template <int FA, int FB, int OUT, bool FAST, int TI_>
 __global__ __launch_bounds__(kThreads, 1) void k_linear(const Proj p, const float* __restrict__ s0,
-                                                        const float* __restrict__ s1, const Part t, const Epilogue ep,
-                                                        const int splits) {
+                                                        const float* __restrict__ s1, const Split t, const Epilogue ep) {
   using S = Shape<FAST, TI_>;
   constexpr int TI = S::TI, BM = S::BM, NST = S::NST;
   constexpr int HALF = BM * 128 * 4, AT_ONCE = 2 * HALF <= S::LDS ? 2 : 1;
   static_assert(HALF <= S::LDS, "a half of the tile's sums fits the stages");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::LDS];
   __shared__ __attribute__((aligned(16))) float lds_sa[NST][BM];
-  const int64_t M = p.M, N = p.N, nkb = p.K / BK;
+  const int64_t M = p.M, N = p.N, nkb = p.K / BK, count = t.full + t.rest * t.parts;
 
-  for (int64_t tile = blockIdx.x; tile < t.count; tile += gridDim.x) {
+  for (int64_t tile = blockIdx.x; tile < count; tile += gridDim.x) {
     // derived again for every tile: hoisted, it all stays live and spills
     int tid = threadIdx.x;
     asm volatile("" : "+v"(tid));
     const int lane = tid & 63, lr = lane & 15, lq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
-    int64_t tm, tn, part = 0, kb0 = 0, kb1 = nkb, id = tile;
-    if constexpr (OUT == kPart) {
-      const int64_t tiles = t.ntm * t.ntn;
-      part = id / tiles, id -= part * tiles;
-      kb0 = part * nkb / splits, kb1 = (part + 1) * nkb / splits;
+    const bool whole = tile < t.full;
+    int64_t id = tile, kb0 = 0, kb1 = nkb;
+    if (!whole) {
+      const int64_t part = (tile - t.full) / t.rest;
+      id = tile - part * t.rest;
+      kb0 = part * nkb / t.parts, kb1 = (part + 1) * nkb / t.parts;
     }
-    tile_of(t.first + (t.halves ? id >> 1 : id), t.ntm * t.ntn, t.ntm, t.ntn, tm, tn);
-    const int64_t m0 = t.halves ? (2 * tm + (id & 1)) * BM : tm * BM, n0 = tn * 256;
-    if (m0 >= M) continue;  // the lower half of a ragged tile
+    int64_t tm, tn;
+    tile_of(id, t.ntm * t.ntn, t.ntm, t.ntn, tm, tn);
+    const int64_t m0 = tm * BM, n0 = tn * 256;
 
     v4f acc[TI][TJ];
     tile_product<FA, FB, FAST, TI, false>(p, s0, s1, lds, lds_sa, tid, m0, n0, kb0, kb1, acc);
 
     __syncthreads();  // every wavefront has read its last stage
+    if (!whole) {
+      float* plane = p.ws + (tile - t.full) * (BM * 256) + wave * (TI * TJ * 256) + lane * 4;
+#pragma unroll
+      for (int i = 0; i < TI; ++i) {
+        if (m0 + (wm * TI + i) * 16 >= M) break;  // the join reads no row past M
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) *(v4f*)(plane + (i * TJ + j) * 256) = acc[i][j];
+      }
+      continue;
+    }
 #pragma unroll
     for (int h0 = 0; h0 < 2; h0 += AT_ONCE) {
 #pragma unroll
@@ -145,7 +157,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_linear(const Proj p, const floa
         const int c = 2 * (tid & 15);
         const int64_t col = n0 + 128 * h + 4 * c;
         float b[8];
-        if constexpr (OUT != kPart) load_bias8(ep, col, N, b);
+        load_bias8(ep, col, N, b);
         if (col < N) {
 #pragma unroll 2
           for (int it = 0; it < BM / 32; ++it) {
@@ -155,14 +167,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_linear(const Proj p, const floa
             const uint8_t* at = lds + (h - h0) * HALF + r * 512;
             const v4f x = *(const v4f*)(at + 16 * (c ^ (r & 15))), y = *(const v4f*)(at + 16 * ((c + 1) ^ (r & 15)));
             float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-            if constexpr (OUT == kPart) {
-              // whole groups of eight: a plane's rows hold them; plain stores, the join reads them next
-              float* w = p.ws + (part * M + row) * plane_ld(N) + col;
-              *(v4f*)w = x;
-              *(v4f*)(w + 4) = y;
-            } else {
-              finish8<OUT>(p, ep, row, col, v, b);
-            }
+            finish8<OUT>(p, ep, row, col, v, b);
           }
         }
       }
@@ -171,102 +176,126 @@ __global__ __launch_bounds__(kThreads, 1) void k_linear(const Proj p, const floa
   }
 }
 
-// The planes' sum and the epilogue: eight columns a lane, the planes added in
-// their order.
-template <int OUT>
-__global__ __launch_bounds__(256) void k_linear_join(const Proj p, const Epilogue ep, const int planes) {
-  const int64_t N = p.N, nb = (N + 127) / 128, ld = plane_ld(N);
-  const int64_t g = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);  // a row's 128 columns
-  const int64_t row = g / nb, col = (g - row * nb) * 128 + 8 * (threadIdx.x & 15);
-  if (row >= p.M || col >= N) return;
-  float b[8], v[8];
-  load_bias8(ep, col, N, b);
-  const float* w = p.ws + row * ld + col;
-  const int64_t plane = p.M * ld;
-  Raw8<FP8Q_F32> x;
-  x.load(w, 0);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = x[k];
+// The parts' sum and the epilogue: 16 rows x 128 columns of a tile of 32 TI rows
+// a workgroup, eight columns a lane, the parts added in their order.
+template <int OUT, int TI>
+__global__ __launch_bounds__(256) void k_linear_join(const Proj p, const Epilogue ep, const Split t) {
+  constexpr int BM = 32 * TI, PER = 2 * (BM / 16);  // workgroups of a tile
+  const int64_t at = blockIdx.x / PER;              // of the tiles in parts
+  const int g = blockIdx.x % PER, i = g >> 1, h = g & 1, lr = threadIdx.x >> 4, c = 8 * (threadIdx.x & 15);
+  int64_t tm, tn;
+  tile_of(t.full + at, t.ntm * t.ntn, t.ntm, t.ntn, tm, tn);
+  const int64_t row = tm * BM + 16 * i + lr, col = tn * 256 + 128 * h + c;
+  if (row >= p.M || col >= p.N) return;
+  float b[8];
+  load_bias8(ep, col, p.N, b);
+  // wavefront, register and lane that held columns c .. c + 3; the next four are 16 lanes on
+  const int wave = 4 * (i / TI) + c / 32, reg = (i % TI) * TJ + 2 * h + (c / 16 & 1), lane = 16 * (c / 4 & 3) + lr;
+  const float* w = p.ws + at * (BM * 256) + wave * (TI * TJ * 256) + reg * 256 + lane * 4;
+  v4f x = *(const v4f*)w, y = *(const v4f*)(w + 64);
 #pragma unroll 4
-  for (int s = 1; s < planes; ++s) {
-    x.load(w, s * plane);
+  for (int k = 1; k < t.parts; ++k) {
+    w += t.rest * (BM * 256);
+    const v4f u = *(const v4f*)w, z = *(const v4f*)(w + 64);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] += x[k];
+    for (int e = 0; e < 4; ++e) x[e] += u[e], y[e] += z[e];
   }
+  float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
   finish8<OUT>(p, ep, row, col, v, b);
 }
 
-static int launch_join(const Proj& p, const Epilogue& e, int planes, const char* what, hipStream_t st) {
-  const int64_t wgs = (p.M * ((p.N + 127) / 128) + 15) / 16;
-  const dim3 grid((unsigned)wgs), block(256);
-  if (p.scales) {
-    if (p.fc == FP8Q_E4M3FN) hipLaunchKernelGGL((k_linear_join<2 + FP8Q_E4M3FN>), grid, block, 0, st, p, e, planes);
-    else hipLaunchKernelGGL((k_linear_join<2 + FP8Q_E5M2>), grid, block, 0, st, p, e, planes);
-  } else if (p.out_dt == FP8Q_F32) {
-    hipLaunchKernelGGL((k_linear_join<FP8Q_F32>), grid, block, 0, st, p, e, planes);
-  } else {
-    hipLaunchKernelGGL((k_linear_join<FP8Q_BF16>), grid, block, 0, st, p, e, planes);
-  }
-  return check_launch(what);
+// The epilogue alone, on sums that lie as M x N in the workspace (the few-row
+// kernel's, where codes are asked for).
+template <int OUT>
+__global__ __launch_bounds__(256) void k_linear_finish(const Proj p, const Epilogue ep) {
+  const int64_t nb = p.N / 128, g = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);  // a row's 128 columns
+  const int64_t row = g / nb, col = (g - row * nb) * 128 + 8 * (threadIdx.x & 15);
+  if (row >= p.M) return;
+  float b[8], v[8];
+  load_bias8(ep, col, p.N, b);
+  Raw8<FP8Q_F32> x;
+  x.load(p.ws, row * p.N + col);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = x[k];
+  finish8<OUT>(p, ep, row, col, v, b);
 }
 
-// How a call goes.  few: the few-row kernel; parts > 1: tiles of so many parts
-// of K and the join; otherwise tiles by `cut`.
+// How a call goes, and its cost in nanoseconds.  Measured, the codes of either
+// operand in HBM:
+//   a block of K of a tile, all compute units at work: exact 1050 (64 rows) and
+//   1680 (128), FP8-MFMA 980 (128) and 1600 (256); its start and end 2500 and
+//   5000; a join 4000 and its bytes, written and read, at 4 TB/s;
+//   a workgroup of the few-row kernel, a block of K: 80 with 16 rows and columns,
+//   85 + 44 for each 16 rows with 32 columns; its start and end 1500.
+// A round is a workgroup per compute unit.
+//   exact 48 x 7168 x 18432: few rows 37.5 us, 8 parts 36.1, whole tiles 139;
+//   200 x 7168 x 18432: 4 parts 80, whole 143, few rows 159;
+//   256 x 2048 x 7168: few rows 18.6, 8 parts 22.2, whole 54.
 struct Plan {
-  bool few;
-  int parts;
-  Cut cut;
+  bool few, low;  // low: tiles of half the rows
+  Split split;
+  int64_t cost;
 };
+static constexpr int kMaxParts = 16;
+
 static Plan plan_linear(bool fast, int64_t M, int64_t N, int64_t K) {
-  Plan r = {};
-  r.few = M <= 64;
-  r.parts = 1;
-  r.cut = cut_tiles(M, fast ? 256 : 128, (N + 255) / 256, second_launch(K));
-  return r;
+  const int64_t cu = grid_size(), nkb = K / BK, ntn = (N + 255) / 256;
+  Plan best = {};
+  best.cost = INT64_MAX;
+  const int64_t groups = (M + 63) / 64, rt = ((M + groups - 1) / groups + 15) / 16;
+  if (groups <= 65535) {  // the second dimension of a launch
+    const int64_t cols = M <= 16 ? 16 : 32, wgs = groups * ((N + cols - 1) / cols);
+    best.few = true;
+    best.cost = (wgs + cu - 1) / cu * (nkb * (M <= 16 ? 80 : 85 + 44 * rt) + 1500);
+  }
+  for (int low = 0; low < 2; ++low) {
+    const int64_t bm = (fast ? 256 : 128) >> low, ntm = (M + bm - 1) / bm, tiles = ntm * ntn;
+    const int64_t block = fast ? (low ? 980 : 1600) : (low ? 1050 : 1680), ends = low ? 2500 : 5000;
+    auto take = [&](int64_t full, int parts, int64_t cost) {
+      if (cost < best.cost) best = {false, low == 1, {ntm, ntn, full, tiles - full, parts}, cost};
+    };
+    take(tiles, 1, (tiles + cu - 1) / cu * (nkb * block + ends));
+    const int64_t full = tiles / cu * cu, rest = tiles - full;
+    for (int parts = 2; rest > 0 && parts <= kMaxParts && parts <= nkb; ++parts)
+      take(full, parts, full / cu * (nkb * block + ends) + (rest * parts + cu - 1) / cu * ((nkb + parts - 1) / parts * block + ends) +
+                            4000 + 2 * rest * parts * bm * 256 * 4 / 4000);
+  }
+  return best;
 }
 
 int64_t linear_workspace(bool fast, bool codes, int64_t M, int64_t N, int64_t K) {
   const Plan c = plan_linear(fast, M, N, K);
-  if (c.few) return codes ? 4 * M * plane_ld(N) : 0;
-  return c.parts > 1 ? 4 * c.parts * M * plane_ld(N) : 0;
+  if (c.few) return codes ? 4 * M * N : 0;
+  return c.split.rest * c.split.parts * (((fast ? 256 : 128) >> c.low) * 256 * 4);
 }
 
 template <int FA, int FB, int OUT, bool FAST, int TI>
-static void launch_tiles(const Proj& p, const Epilogue& e, const Part& t, int parts, hipStream_t st) {
-  const int64_t g = grid_size();
-  hipLaunchKernelGGL((k_linear<FA, FB, OUT, FAST, TI>), dim3((unsigned)(t.count < g ? t.count : g)), dim3(kThreads), 0, st, p,
-                     p.s0, p.s1, t, e, parts);
+static void launch_tiles(const Proj& p, const Epilogue& e, const Split& t, hipStream_t st) {
+  const int64_t g = grid_size(), count = t.full + t.rest * t.parts;
+  hipLaunchKernelGGL((k_linear<FA, FB, OUT, FAST, TI>), dim3((unsigned)(count < g ? count : g)), dim3(kThreads), 0, st, p, p.s0,
+                     p.s1, t, e);
+  if (t.rest)
+    hipLaunchKernelGGL((k_linear_join<OUT, TI>), dim3((unsigned)(t.rest * 4 * TI)), dim3(256), 0, st, p, e, t);
 }
 
-template <int FA, int FB, int OUT, bool FAST>
-static void launch_cut(const Proj& p, const Epilogue& e, const Plan& c, hipStream_t st) {
-  constexpr int TALL = FAST ? 8 : 4, LOW = TALL / 2;
-  const int64_t ntn = (p.N + 255) / 256;
-  const int64_t ntm = (p.M + 32 * TALL - 1) / (32 * TALL), ltm = (p.M + 32 * LOW - 1) / (32 * LOW);
-  if constexpr (OUT == kPart) {
-    launch_tiles<FA, FB, OUT, FAST, LOW>(p, e, {ltm, ntn, 0, ltm * ntn * c.parts, false}, c.parts, st);
-  } else if (c.cut.low) {
-    launch_tiles<FA, FB, OUT, FAST, LOW>(p, e, {ltm, ntn, 0, ltm * ntn, false}, 1, st);
+template <int FA, int FB, int OUT>
+static void launch_rows(const Proj& p, const Epilogue& e, bool fast, const Plan& c, hipStream_t st) {
+  if (fast) {
+    if (c.low) launch_tiles<FA, FB, OUT, true, 4>(p, e, c.split, st);
+    else launch_tiles<FA, FB, OUT, true, 8>(p, e, c.split, st);
   } else {
-    launch_tiles<FA, FB, OUT, FAST, TALL>(p, e, {ntm, ntn, 0, c.cut.tall, false}, 1, st);
-    if (c.cut.split) launch_tiles<FA, FB, OUT, FAST, LOW>(p, e, {ntm, ntn, c.cut.tall, 2 * c.cut.split, true}, 1, st);
+    if (c.low) launch_tiles<FA, FB, OUT, false, 2>(p, e, c.split, st);
+    else launch_tiles<FA, FB, OUT, false, 4>(p, e, c.split, st);
   }
-}
-
-template <int FA, int FB, bool FAST>
-static void launch_out(const Proj& p, const Epilogue& e, const Plan& c, hipStream_t st) {
-  if (c.parts > 1) launch_cut<FA, FB, kPart, FAST>(p, e, c, st);
-  else if (p.scales) {
-    if (p.fc == FP8Q_E4M3FN) launch_cut<FA, FB, 2 + FP8Q_E4M3FN, FAST>(p, e, c, st);
-    else launch_cut<FA, FB, 2 + FP8Q_E5M2, FAST>(p, e, c, st);
-  } else if (p.out_dt == FP8Q_F32) launch_cut<FA, FB, FP8Q_F32, FAST>(p, e, c, st);
-  else launch_cut<FA, FB, FP8Q_BF16, FAST>(p, e, c, st);
 }
 
 template <int FA, int FB>
 static void launch_f(const Proj& p, const Epilogue& e, bool fast, const Plan& c, hipStream_t st) {
-  if (fast) launch_out<FA, FB, true>(p, e, c, st);
-  else launch_out<FA, FB, false>(p, e, c, st);
+  if (p.scales) {
+    if (p.fc == FP8Q_E4M3FN) launch_rows<FA, FB, 2 + FP8Q_E4M3FN>(p, e, fast, c, st);
+    else launch_rows<FA, FB, 2 + FP8Q_E5M2>(p, e, fast, c, st);
+  } else if (p.out_dt == FP8Q_F32) launch_rows<FA, FB, FP8Q_F32>(p, e, fast, c, st);
+  else launch_rows<FA, FB, FP8Q_BF16>(p, e, fast, c, st);
 }
 
 int launch_linear(const Proj& q, const Epilogue& e, bool fast, const char* what, hipStream_t st) {
@@ -274,17 +303,19 @@ int launch_linear(const Proj& q, const Epilogue& e, bool fast, const char* what,
   Proj p = q;
   if (c.few) {
     if (!p.scales) return launch_few(p, &e, what, st);
-    p.out = p.ws, p.ldo = plane_ld(p.N), p.out_dt = FP8Q_F32, p.scales = nullptr;
+    p.out = p.ws, p.ldo = p.N, p.out_dt = FP8Q_F32, p.scales = nullptr;
     if (int rc = launch_few(p, nullptr, what, st)) return rc;
-    return launch_join(q, e, 1, what, st);
+    const dim3 grid((unsigned)((q.M * (q.N / 128) + 15) / 16)), block(256);
+    if (q.fc == FP8Q_E4M3FN) hipLaunchKernelGGL((k_linear_finish<2 + FP8Q_E4M3FN>), grid, block, 0, st, q, e);
+    else hipLaunchKernelGGL((k_linear_finish<2 + FP8Q_E5M2>), grid, block, 0, st, q, e);
+    return check_launch(what);
   }
   p.B1 = p.B0, p.s1 = p.s0;
   if (p.fa == FP8Q_E4M3FN && p.fb == FP8Q_E4M3FN) launch_f<0, 0>(p, e, fast, c, st);
   else if (p.fa == FP8Q_E5M2 && p.fb == FP8Q_E4M3FN) launch_f<1, 0>(p, e, fast, c, st);
   else if (p.fa == FP8Q_E4M3FN) launch_f<0, 1>(p, e, fast, c, st);
   else launch_f<1, 1>(p, e, fast, c, st);
-  if (int rc = check_launch(what)) return rc;
-  return c.parts > 1 ? launch_join(q, e, c.parts, what, st) : FP8Q_OK;
+  return check_launch(what);
 }
 
 }  // namespace fp8q
