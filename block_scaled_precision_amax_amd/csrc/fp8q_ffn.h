@@ -55,6 +55,14 @@ struct Raw8 {
 #pragma unroll
     for (int k = 0; k < (DT == FP8Q_F32 ? 2 : 1); ++k) v[k] = STREAM ? __builtin_nontemporal_load(q + k) : q[k];
   }
+  // the same value eight times (one that bf16 holds)
+  __device__ __forceinline__ void fill(float x) {
+    const uint32_t u = __float_as_uint(x);
+#pragma unroll
+    for (int k = 0; k < (DT == FP8Q_F32 ? 2 : 1); ++k)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[k][e] = DT == FP8Q_F32 ? u : (u >> 16) * 0x10001u;
+  }
   __device__ __forceinline__ float operator[](int e) const {
     if constexpr (DT == FP8Q_F32) return __uint_as_float(v[e >> 2][e & 3]);
     else return e & 1 ? bf_hi(v[0][e >> 1]) : bf_lo(v[0][e >> 1]);

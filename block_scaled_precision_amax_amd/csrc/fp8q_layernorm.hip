@@ -36,12 +36,64 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
   return v;
 }
 
+// Group c of the weight or bias, as loaded, or the constant that its absence
+// stands for.
+template <int WDT>
+__device__ __forceinline__ void load_or(Raw8<WDT>& r, const void* p, int c, float constant) {
+  if (p) r.template load<false>(p, 8 * c);
+  else r.fill(constant);
+}
+
+// Eight sums as they are stored, kept from before the mean is taken off.
+template <int DT>
+struct Sum8 {
+  float v[8];
+  __device__ __forceinline__ void set(const float (&x)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = x[e];
+  }
+  __device__ __forceinline__ void store(void* p, int64_t i) const { store8<DT>(p, i, v); }
+};
+template <>
+struct Sum8<FP8Q_BF16> {
+  u32x4 v;
+  __device__ __forceinline__ void set(const float (&x)[8]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = pk_bf16(x[2 * e], x[2 * e + 1]);
+  }
+  __device__ __forceinline__ void store(void* p, int64_t i) const {
+    __builtin_nontemporal_store(v, (u32x4*)((uint16_t*)p + i));
+  }
+};
+
+// The codes of group c of a row, m the largest |y| bits of the lane's eight.
+__device__ __forceinline__ void store_codes(const LayerNormFwd& p, int64_t row, int c, const float (&y)[8], uint32_t m) {
+  const float amax = __uint_as_float(canon_abs_bits(row16_max(m)));
+  const bool e4 = p.fmt == FP8Q_E4M3FN;
+  const float s = e4 ? block_scale7<FP8Q_E4M3FN>(amax, p.qeps) : block_scale7<FP8Q_E5M2>(amax, p.qeps);
+  const bool fast = scale_ok(s);
+  const float inv = 1.0f / s;
+  u32x2 q;
+  if (e4)
+    q = u32x2{encode4<FP8Q_E4M3FN>(y[0], y[1], y[2], y[3], s, inv, fast),
+              encode4<FP8Q_E4M3FN>(y[4], y[5], y[6], y[7], s, inv, fast)};
+  else
+    q = u32x2{encode4<FP8Q_E5M2>(y[0], y[1], y[2], y[3], s, inv, fast),
+              encode4<FP8Q_E5M2>(y[4], y[5], y[6], y[7], s, inv, fast)};
+  __builtin_nontemporal_store(q, (u32x2*)(p.q + row * p.ldq + 8 * c));
+  if ((threadIdx.x & 15) == 0) p.scales[row * p.ld_s + (c >> 4)] = s;
+}
+
 // One row per TPR threads, V groups of eight consecutive elements a thread:
 // group g of thread t is elements 8 * (g * TPR + t), so 16 neighbouring
-// lanes hold one 128-element block.  A row's loads are issued together,
-// without a branch (a thread past the last column reads the last group
-// again, and its elements count for nothing); weight and bias, which the
-// caches hold, after the first sum.
+// lanes hold one 128-element block.  Nothing branches around a load or a
+// store, so that each wait counts exactly what it needs: sixteen lanes past the
+// last column take the last block (without codes, a lane the last group) once
+// more, leave it out of the sums and store what its own lanes store.  A row's
+// loads are issued together; weight and bias, which the caches hold, after the
+// sums, a group ahead of its use and before the stores of the group at hand: a
+// load behind a store waits for it (all after the sums: 150 us and a third
+// fewer rows in flight; each with its group: 154).
 template <int DT, int WDT, int TPR, int V, bool RES>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_layernorm_1x128(const LayerNormFwd p) {
   constexpr int TH = TPR < 256 ? 256 : TPR;
@@ -57,7 +109,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_layernorm_1x128(const
 #pragma unroll
   for (int g = 0; g < V; ++g) {
     in[g] = g * TPR + t < nv;
-    cc[g] = in[g] ? g * TPR + t : nv - 1;
+    cc[g] = in[g] ? g * TPR + t : p.q ? nv - 16 + (t & 15) : nv - 1;
     x[g].load(p.x, row * p.ldx + 8 * cc[g]);
     if constexpr (RES) r[g].load(p.res, row * p.ldr + 8 * cc[g]);
   }
@@ -73,65 +125,140 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_layernorm_1x128(const
     }
     sum += in[g] ? s : 0.0f;
   }
+  Sum8<DT> z[V];
+#pragma unroll
+  for (int g = 0; g < V; ++g) z[g].set(v[g]);
   const float mean = row_sum<TPR>(sum, part[0]) / n;
-  Raw8<WDT> w[V], b[V];
-  if (p.w) {
-#pragma unroll
-    for (int g = 0; g < V; ++g) w[g].template load<false>(p.w, 8 * cc[g]);
-  }
-  if (p.b) {
-#pragma unroll
-    for (int g = 0; g < V; ++g) b[g].template load<false>(p.b, 8 * cc[g]);
-  }
   float ss = 0.0f;
 #pragma unroll
   for (int g = 0; g < V; ++g) {
     float s = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float d = v[g][e] - mean;
-      s = __builtin_fmaf(d, d, s);
+      v[g][e] -= mean;
+      s = __builtin_fmaf(v[g][e], v[g][e], s);
     }
     ss += in[g] ? s : 0.0f;
   }
+  Raw8<WDT> w[2], b[2];
+  auto load_affine = [&](int g) {
+    load_or(w[g & 1], p.w, cc[g], 1.0f);
+    load_or(b[g & 1], p.b, cc[g], 0.0f);
+  };
   ss = row_sum<TPR>(ss, part[1]);
+  load_affine(0);
   const float rstd = 1.0f / sqrtf(ss / n + p.neps);
-  if (t == 0) {
-    if (p.mean) p.mean[row] = mean;
-    if (p.rstd) p.rstd[row] = rstd;
-  }
 #pragma unroll
   for (int g = 0; g < V; ++g) {
-    if (!in[g]) continue;  // whole 16-lane rows where codes are made: cols is then a multiple of 128
+    if (g + 1 < V) load_affine(g + 1);
+    __builtin_amdgcn_sched_barrier(0);
     const int c = cc[g];
-    // the sum is stored in x's type; the norm goes on from the unrounded sum
-    if (p.z) store8<DT>(p.z, row * p.ldz + 8 * c, v[g]);
     float y[8];
     uint32_t m = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      y[e] = (v[g][e] - mean) * rstd;
-      if (p.w) y[e] *= w[g][e];
-      if (p.b) y[e] += b[g][e];
+      y[e] = __builtin_fmaf(v[g][e] * rstd, w[g & 1][e], b[g & 1][e]);
       m = max(m, abs_bits(y[e]));
     }
+    // the sum is stored in x's type; the norm goes on from the unrounded sum
+    if (p.z) z[g].store(p.z, row * p.ldz + 8 * c);
     if (p.y) store8<DT>(p.y, row * p.ldy + 8 * c, y);
-    if (p.q) {
-      const float amax = __uint_as_float(canon_abs_bits(row16_max(m)));
-      const bool e4 = p.fmt == FP8Q_E4M3FN;
-      const float s = e4 ? block_scale7<FP8Q_E4M3FN>(amax, p.qeps) : block_scale7<FP8Q_E5M2>(amax, p.qeps);
-      const bool fast = scale_ok(s);
-      const float inv = 1.0f / s;
-      u32x2 q;
-      if (e4)
-        q = u32x2{encode4<FP8Q_E4M3FN>(y[0], y[1], y[2], y[3], s, inv, fast),
-                  encode4<FP8Q_E4M3FN>(y[4], y[5], y[6], y[7], s, inv, fast)};
-      else
-        q = u32x2{encode4<FP8Q_E5M2>(y[0], y[1], y[2], y[3], s, inv, fast),
-                  encode4<FP8Q_E5M2>(y[4], y[5], y[6], y[7], s, inv, fast)};
-      __builtin_nontemporal_store(q, (u32x2*)(p.q + row * p.ldq + 8 * c));
-      if ((t & 15) == 0) p.scales[row * p.ld_s + (c >> 4)] = s;
+    if (p.q) store_codes(p, row, c, y, m);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  if (t == 0) {
+    if (p.mean) p.mean[row] = mean;
+    if (p.rstd) p.rstd[row] = rstd;
+  }
+}
+
+// The same for many rows: a workgroup walks rows block, block + blocks, ...
+// with its columns' weight and bias in registers and the next row's loads
+// issued before this row's sums are joined.
+template <int DT, int WDT, int TPR, int V, bool RES>
+__global__ __launch_bounds__(TPR) void k_layernorm_walk(const LayerNormFwd p) {
+  __shared__ float part[4][TPR / 64];
+  const int t = threadIdx.x, nv = (int)(p.cols / 8);
+  const float n = (float)p.cols;
+  int cc[V];
+  bool in[V];
+  Raw8<WDT> w[V], b[V];
+#pragma unroll
+  for (int g = 0; g < V; ++g) {
+    in[g] = g * TPR + t < nv;
+    cc[g] = in[g] ? g * TPR + t : p.q ? nv - 16 + (t & 15) : nv - 1;
+    load_or(w[g], p.w, cc[g], 1.0f);
+    load_or(b[g], p.b, cc[g], 0.0f);
+  }
+  struct Row {
+    Raw8<DT> x[V], r[V];
+  } even, odd;
+  auto load = [&](Row& a, int64_t row) {
+    if (row >= p.rows) row = p.rows - 1;  // read again for want of a next one
+#pragma unroll
+    for (int g = 0; g < V; ++g) {
+      a.x[g].load(p.x, row * p.ldx + 8 * cc[g]);
+      if constexpr (RES) a.r[g].load(p.res, row * p.ldr + 8 * cc[g]);
     }
+  };
+  int64_t row = blockIdx.x;
+  load(even, row);
+  auto one = [&](const Row& cur, Row& nxt, int slot) {
+    float v[V][8];
+    float sum = 0.0f;
+#pragma unroll
+    for (int g = 0; g < V; ++g) {
+      float s = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[g][e] = RES ? cur.x[g][e] + cur.r[g][e] : cur.x[g][e];
+        s += v[g][e];
+      }
+      sum += in[g] ? s : 0.0f;
+    }
+    load(nxt, row + gridDim.x);
+    Sum8<DT> z[V];
+#pragma unroll
+    for (int g = 0; g < V; ++g) z[g].set(v[g]);
+    const float mean = row_sum<TPR>(sum, part[slot]) / n;
+    float ss = 0.0f;
+#pragma unroll
+    for (int g = 0; g < V; ++g) {
+      float s = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[g][e] -= mean;
+        s = __builtin_fmaf(v[g][e], v[g][e], s);
+      }
+      ss += in[g] ? s : 0.0f;
+    }
+    ss = row_sum<TPR>(ss, part[slot + 1]);
+    const float rstd = 1.0f / sqrtf(ss / n + p.neps);
+#pragma unroll
+    for (int g = 0; g < V; ++g) {
+      const int c = cc[g];
+      float y[8];
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[e] = __builtin_fmaf(v[g][e] * rstd, w[g][e], b[g][e]);
+        m = max(m, abs_bits(y[e]));
+      }
+      if (p.z) z[g].store(p.z, row * p.ldz + 8 * c);
+      if (p.y) store8<DT>(p.y, row * p.ldy + 8 * c, y);
+      if (p.q) store_codes(p, row, c, y, m);
+    }
+    if (t == 0) {
+      if (p.mean) p.mean[row] = mean;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
+  };
+  // two rows' sums alternate between the slots: no wavefront still reads those written
+  for (; row < p.rows; row += gridDim.x) {
+    one(even, odd, 0);
+    row += gridDim.x;
+    if (row >= p.rows) break;
+    one(odd, even, 2);
   }
 }
 
@@ -156,10 +283,23 @@ static void launch_fwd(const LayerNormFwd& p, hipStream_t st) {
   }
 }
 
+template <int DT, int WDT, int TPR, int V>
+static void launch_walk(const LayerNormFwd& p, int64_t blocks, hipStream_t st) {
+  if (p.res) hipLaunchKernelGGL((k_layernorm_walk<DT, WDT, TPR, V, true>), dim3((unsigned)blocks), dim3(TPR), 0, st, p);
+  else hipLaunchKernelGGL((k_layernorm_walk<DT, WDT, TPR, V, false>), dim3((unsigned)blocks), dim3(TPR), 0, st, p);
+}
+
 template <int DT, int WDT>
 static void dispatch_fwd(const LayerNormFwd& p, hipStream_t st) {
   const int64_t c = p.cols;
-  if (c <= 64 * 8) launch_fwd<DT, WDT, 64, 1>(p, st);
+  const int64_t cu = device_cu_count();
+  // Walking pays where a row of fp32 or a wide one leaves few rows in flight:
+  // 8192 x 8192 fp32 with residual 158 us against 185, 2048 rows 44.5 against 49.0,
+  // 1024 rows the same; 7168 x 16384 bf16 143 against 150, 2048 rows 48.4 against
+  // 47.2.  16384 x 7168 bf16: 148 to 153 against 150.
+  if (DT == FP8Q_F32 && c > 512 * 8 && c <= 1024 * 8 && p.rows >= 8 * cu) launch_walk<DT, WDT, 1024, 1>(p, cu, st);
+  else if (c > 1024 * 8 && c <= 1024 * 8 * 2 && p.rows >= 16 * cu) launch_walk<DT, WDT, 1024, 2>(p, cu, st);
+  else if (c <= 64 * 8) launch_fwd<DT, WDT, 64, 1>(p, st);
   else if (c <= 64 * 8 * 2) launch_fwd<DT, WDT, 64, 2>(p, st);
   else if (c <= 64 * 8 * 4) launch_fwd<DT, WDT, 64, 4>(p, st);
   else if (c <= 256 * 8 * 2) launch_fwd<DT, WDT, 256, 2>(p, st);
@@ -181,26 +321,39 @@ int launch_layernorm_1x128(const LayerNormFwd& p, hipStream_t st) {
 }
 
 // ---------------------------------------------------------------- backward
-// Each TPR threads walk rows part, part + parts, ... and keep both column
-// sums of their columns in registers; at the end every workgroup writes
-// them as one row of the workspace ([dw | db]), and k_column_sums adds those
-// rows in a fixed order, so the result does not depend on timing.  The next
-// row's loads are issued before this row's sums are joined.  Parts: at most
-// two workgroups a compute unit (512); one per eight rows below that, but 256
-// as far as there are rows, so that every compute unit has one.
-static constexpr int64_t kParts = 512;
-
-int64_t layernorm_bwd_parts(int64_t rows, int64_t cols) {
-  const int64_t per = cols <= 2048 ? 4 : 1;  // rows a workgroup holds at once
-  const int64_t all = (rows + per - 1) / per;
-  int64_t g = rows / 8 < 256 ? 256 : rows / 8;
-  if (g > kParts) g = kParts;
-  return all < g ? all : g;
+// R groups of TPR threads walk rows, R rows at a time a workgroup, and keep both
+// column sums of their columns in registers; at the end every workgroup adds
+// its groups' and writes them as one row of the workspace ([dw | db]), and
+// k_column_sums adds those rows in a fixed order, so the result does not depend
+// on timing.  The next rows' loads are issued before these rows' sums are
+// joined.
+struct BwdShape {
+  int tpr, v, r;
+};
+static constexpr BwdShape bwd_shape(int64_t cols) {
+  return cols <= 64 * 8         ? BwdShape{64, 1, 4}
+         : cols <= 64 * 8 * 2   ? BwdShape{64, 2, 4}
+         : cols <= 64 * 8 * 4   ? BwdShape{64, 4, 4}
+         : cols <= 256 * 8 * 2  ? BwdShape{256, 2, 2}
+         : cols <= 512 * 8 * 2  ? BwdShape{512, 2, 1}
+         : cols <= 512 * 8 * 4  ? BwdShape{512, 4, 1}
+         : cols <= 1024 * 8 * 4 ? BwdShape{1024, 4, 1}
+                                : BwdShape{1024, 8, 1};
 }
 
-template <int DT, int TPR, int V, bool RES>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_layernorm_bwd(const LayerNormBwd p) {
-  constexpr int TH = TPR < 256 ? 256 : TPR, R = TH / TPR;
+// Workgroups: one a compute unit of 256, as few as take the same number of turns.
+// (Two a unit, where their registers let one and a half run: 16384 x 7168 bf16
+// with residual 169 us against 156; 2048 columns 62 against 57.)
+static constexpr int64_t kParts = 256;
+int64_t layernorm_bwd_parts(int64_t rows, int64_t cols) {
+  const int64_t all = (rows + bwd_shape(cols).r - 1) / bwd_shape(cols).r;
+  const int64_t turns = (all + kParts - 1) / kParts;
+  return (all + turns - 1) / turns;
+}
+
+template <int DT, int TPR, int V, int R, bool RES>
+__global__ __launch_bounds__(TPR* R) void k_layernorm_bwd(const LayerNormBwd p) {
+  constexpr int TH = TPR * R;
   // The weight waits in LDS (two planes of four, free of bank conflicts), as
   // far as it fits: a global read here would come back behind the next row's
   // loads.
@@ -208,7 +361,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_layernorm_bwd(const L
   constexpr bool WL = NW * 32 <= 128 * 1024;
   __shared__ float part[2][2][TH / 64];
   __shared__ float4 w_lds[2][WL ? NW : 1];
-  const int t = threadIdx.x % TPR;
+  const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
   const int nv = (int)(p.cols / 8);
   auto ones_or_w = [&](int c, float(&w)[8]) {
     if (p.w) {
@@ -234,11 +387,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_layernorm_bwd(const L
   const float rc = 1.0f / (float)p.cols;
   int flip = 0;
   const int64_t step = (int64_t)gridDim.x * R;
-  int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / TPR;
+  int64_t first = (int64_t)blockIdx.x * R;  // the workgroup's rows at hand: first .. first + R - 1
   // The loop has no branch around a load, so that each wait counts exactly
   // what it needs: a thread past the last column reads the last group again
-  // and its part of the sums is dropped, and the last row is read again for
-  // want of a next one (cache hits).
+  // and its part of the sums is dropped, and past the last row that row is
+  // read again (cache hits) and counts as zeros.
   int cc[V];
   bool in[V];
 #pragma unroll
@@ -262,7 +415,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_layernorm_bwd(const L
       w.z[g].load(p.z, r * p.ldz + 8 * cc[g]);
     }
   };
-  load(even, row);
+  load(even, first + group);
   if constexpr (WL) {
     for (int c = threadIdx.x; c < nv; c += TH) {
       float w[8];
@@ -273,6 +426,15 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_layernorm_bwd(const L
     __syncthreads();
   }
   auto one = [&](Row& cur, Row& nxt) {
+    int64_t row = first + group;
+    const bool valid = row < p.rows;
+    if (R > 1 && !valid) {  // whole wavefronts
+      row = p.rows - 1;
+      cur.mean = 0.0f;  // finite, whatever that row holds
+      cur.rstd = 0.0f;
+#pragma unroll
+      for (int g = 0; g < V; ++g) cur.dy[g].fill(0.0f), cur.z[g].fill(0.0f);
+    }
     const float rs = cur.rstd, mu = cur.mean;
     Raw8<DT> dr[V];
     if constexpr (RES) {
@@ -295,16 +457,19 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_layernorm_bwd(const L
       dot += in[g] ? d : 0.0f;
       sum += in[g] ? s : 0.0f;
     }
-    load(nxt, row + step);
+    load(nxt, first + step + group);
     dot = wave_sum(dot), sum = wave_sum(sum);
     if constexpr (TPR > 64) {
       float(&pt)[2][TH / 64] = part[flip];
-      flip ^= 1;  // the next row's sums go to the other slots: no wave still reads those
+      flip ^= 1;  // the next rows' sums go to the other slots: no wave still reads those
       if ((threadIdx.x & 63) == 0) pt[0][threadIdx.x >> 6] = dot, pt[1][threadIdx.x >> 6] = sum;
       __syncthreads();
       dot = 0.0f, sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < TPR / 64; ++i) dot += pt[0][i], sum += pt[1][i];
+      for (int i = 0; i < TPR / 64; ++i) {
+        dot += pt[0][group * (TPR / 64) + i];
+        sum += pt[1][group * (TPR / 64) + i];
+      }
     }
     dot *= rc, sum *= rc;
 #pragma unroll
@@ -317,13 +482,14 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_layernorm_bwd(const L
         d[e] = rs * (__builtin_fmaf(-xh, dot, cur.dy[g][e] * w[e]) - sum);
         if constexpr (RES) d[e] += dr[g][e];
       }
-      if (in[g]) store8<DT>(p.dx, row * p.lddx + 8 * cc[g], d);
+      if (in[g] && valid) store8<DT>(p.dx, row * p.lddx + 8 * cc[g], d);
     }
   };
-  for (; row < p.rows; row += step) {
+  // the same turns for every wavefront: the barriers are inside
+  for (; first < p.rows; first += step) {
     one(even, odd);
-    row += step;
-    if (row >= p.rows) break;
+    first += step;
+    if (first >= p.rows) break;
     one(odd, even);
   }
   // one row of column sums per workgroup
@@ -331,7 +497,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_layernorm_bwd(const L
                          p.pb ? p.pb + (int64_t)blockIdx.x * p.ldp : nullptr};
   if constexpr (R > 1) {
     // the workgroup's R row groups meet in LDS, one sum after the other
-    __shared__ float sum[R][V * 512];
+    __shared__ float sum[R][V * TPR * 8];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (!out[k]) continue;
@@ -339,7 +505,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_layernorm_bwd(const L
 #pragma unroll
       for (int g = 0; g < V; ++g)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[threadIdx.x / TPR][8 * (g * TPR + t) + e] = k ? db[g][e] : dw[g][e];
+        for (int e = 0; e < 8; ++e) sum[group][8 * (g * TPR + t) + e] = k ? db[g][e] : dw[g][e];
       __syncthreads();
       for (int c = threadIdx.x; c < p.cols; c += TH) {
         float a = 0.0f;
@@ -401,24 +567,26 @@ void launch_column_sums(const float* ws, int64_t parts, int64_t cols, int64_t sp
   hipLaunchKernelGGL(k_column_sums, dim3((unsigned)((cols + 63) / 64)), dim3(256), 0, st, ws, parts, cols, split, a, b);
 }
 
-template <int DT, int TPR, int V>
+template <int DT, int64_t COLS>
 static void launch_bwd(const LayerNormBwd& p, int64_t parts, hipStream_t st) {
-  const dim3 grid((unsigned)parts), block(TPR < 256 ? 256 : TPR);
-  if (p.dres) hipLaunchKernelGGL((k_layernorm_bwd<DT, TPR, V, true>), grid, block, 0, st, p);
-  else hipLaunchKernelGGL((k_layernorm_bwd<DT, TPR, V, false>), grid, block, 0, st, p);
+  constexpr BwdShape s = bwd_shape(COLS);
+  const dim3 grid((unsigned)parts), block(s.tpr * s.r);
+  if (p.dres) hipLaunchKernelGGL((k_layernorm_bwd<DT, s.tpr, s.v, s.r, true>), grid, block, 0, st, p);
+  else hipLaunchKernelGGL((k_layernorm_bwd<DT, s.tpr, s.v, s.r, false>), grid, block, 0, st, p);
 }
 
+// The shape of the smallest limit that holds the columns.
 template <int DT>
 static void dispatch_bwd(const LayerNormBwd& p, int64_t parts, hipStream_t st) {
   const int64_t c = p.cols;
-  if (c <= 64 * 8) launch_bwd<DT, 64, 1>(p, parts, st);
-  else if (c <= 64 * 8 * 2) launch_bwd<DT, 64, 2>(p, parts, st);
-  else if (c <= 64 * 8 * 4) launch_bwd<DT, 64, 4>(p, parts, st);
-  else if (c <= 256 * 8 * 2) launch_bwd<DT, 256, 2>(p, parts, st);
-  else if (c <= 256 * 8 * 4) launch_bwd<DT, 256, 4>(p, parts, st);
-  else if (c <= 512 * 8 * 4) launch_bwd<DT, 512, 4>(p, parts, st);
-  else if (c <= 1024 * 8 * 4) launch_bwd<DT, 1024, 4>(p, parts, st);
-  else launch_bwd<DT, 1024, 8>(p, parts, st);
+  if (c <= 512) launch_bwd<DT, 512>(p, parts, st);
+  else if (c <= 1024) launch_bwd<DT, 1024>(p, parts, st);
+  else if (c <= 2048) launch_bwd<DT, 2048>(p, parts, st);
+  else if (c <= 4096) launch_bwd<DT, 4096>(p, parts, st);
+  else if (c <= 8192) launch_bwd<DT, 8192>(p, parts, st);
+  else if (c <= 16384) launch_bwd<DT, 16384>(p, parts, st);
+  else if (c <= 32768) launch_bwd<DT, 32768>(p, parts, st);
+  else launch_bwd<DT, 65536>(p, parts, st);
 }
 
 int launch_layernorm_bwd(const LayerNormBwd& q, hipStream_t st) {
