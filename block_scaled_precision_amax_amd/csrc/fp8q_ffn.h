@@ -43,6 +43,20 @@ __device__ __forceinline__ float block_scale7(float amax, float eps) {
   return m / max_finite(FMT);
 }
 
+// fl32(1 / s) for s in [2^-80, 2^80] (scale_ok), in a third of the division's
+// instructions: the hardware's reciprocal is within one step, and one Newton
+// step whose residual is exact in an FMA rounds it correctly (equal to the IEEE
+// quotient for each of the 2^23 mantissas; powers of two only scale it).  Other
+// s take the division in encode4, which does not read it.
+__device__ __forceinline__ float recip(float s) {
+  const float r = __builtin_amdgcn_rcpf(s);
+  return __builtin_fmaf(__builtin_fmaf(-s, r, 1.0f), r, r);
+}
+
+// The larger of m and |x|, or NaN if one is (v_maximum3_f32: the magnitude
+// costs nothing, where an integer maximum takes an AND for each value).
+__device__ __forceinline__ float max_abs(float m, float x) { return __builtin_elementwise_maximum(m, __builtin_fabsf(x)); }
+
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
 // Eight elements of a row as loaded, and as fp32.

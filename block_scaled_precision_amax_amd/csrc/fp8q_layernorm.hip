@@ -66,13 +66,16 @@ struct Sum8<FP8Q_BF16> {
   }
 };
 
-// The codes of group c of a row, m the largest |y| bits of the lane's eight.
-__device__ __forceinline__ void store_codes(const LayerNormFwd& p, int64_t row, int c, const float (&y)[8], uint32_t m) {
-  const float amax = __uint_as_float(canon_abs_bits(row16_max(m)));
+// The codes of group c of a row.
+__device__ __forceinline__ void store_codes(const LayerNormFwd& p, int64_t row, int c, const float (&y)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = max_abs(m, y[e]);
+  const float amax = __uint_as_float(canon_abs_bits(row16_max(__float_as_uint(m))));
   const bool e4 = p.fmt == FP8Q_E4M3FN;
   const float s = e4 ? block_scale7<FP8Q_E4M3FN>(amax, p.qeps) : block_scale7<FP8Q_E5M2>(amax, p.qeps);
   const bool fast = scale_ok(s);
-  const float inv = 1.0f / s;
+  const float inv = recip(s);
   u32x2 q;
   if (e4)
     q = u32x2{encode4<FP8Q_E4M3FN>(y[0], y[1], y[2], y[3], s, inv, fast),
@@ -154,16 +157,12 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_layernorm_1x128(const
     __builtin_amdgcn_sched_barrier(0);
     const int c = cc[g];
     float y[8];
-    uint32_t m = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      y[e] = __builtin_fmaf(v[g][e] * rstd, w[g & 1][e], b[g & 1][e]);
-      m = max(m, abs_bits(y[e]));
-    }
+    for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(v[g][e] * rstd, w[g & 1][e], b[g & 1][e]);
     // the sum is stored in x's type; the norm goes on from the unrounded sum
     if (p.z) z[g].store(p.z, row * p.ldz + 8 * c);
     if (p.y) store8<DT>(p.y, row * p.ldy + 8 * c, y);
-    if (p.q) store_codes(p, row, c, y, m);
+    if (p.q) store_codes(p, row, c, y);
     __builtin_amdgcn_sched_barrier(0);
   }
   if (t == 0) {
@@ -238,15 +237,11 @@ __global__ __launch_bounds__(TPR) void k_layernorm_walk(const LayerNormFwd p) {
     for (int g = 0; g < V; ++g) {
       const int c = cc[g];
       float y[8];
-      uint32_t m = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        y[e] = __builtin_fmaf(v[g][e] * rstd, w[g][e], b[g][e]);
-        m = max(m, abs_bits(y[e]));
-      }
+      for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(v[g][e] * rstd, w[g][e], b[g][e]);
       if (p.z) z[g].store(p.z, row * p.ldz + 8 * c);
       if (p.y) store8<DT>(p.y, row * p.ldy + 8 * c, y);
-      if (p.q) store_codes(p, row, c, y, m);
+      if (p.q) store_codes(p, row, c, y);
     }
     if (t == 0) {
       if (p.mean) p.mean[row] = mean;

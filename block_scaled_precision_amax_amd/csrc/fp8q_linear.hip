@@ -79,11 +79,11 @@ __device__ __forceinline__ void finish8(const Proj& p, const Epilogue& e, int64_
   } else {
     // N is a multiple of 128: the sixteen lanes of a block are all here
     constexpr int QF = OUT - 2;
-    uint32_t m = 0;
+    float m = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = max(m, abs_bits(v[k]));
-    const float s = block_scale7<QF>(__uint_as_float(canon_abs_bits(row16_max(m))), p.eps);
-    const float inv = 1.0f / s;
+    for (int k = 0; k < 8; ++k) m = max_abs(m, v[k]);
+    const float s = block_scale7<QF>(__uint_as_float(canon_abs_bits(row16_max(__float_as_uint(m)))), p.eps);
+    const float inv = recip(s);
     const bool fast = scale_ok(s);
     const u32x2 q = {encode4<QF>(v[0], v[1], v[2], v[3], s, inv, fast), encode4<QF>(v[4], v[5], v[6], v[7], s, inv, fast)};
     __builtin_nontemporal_store(q, (u32x2*)((uint8_t*)p.out + row * p.ldo + col));

@@ -35,79 +35,121 @@ __global__ __launch_bounds__(512, 4) void k_linear_bwd(const LinearBwd p) {
   __shared__ __attribute__((aligned(16))) uint32_t tile[NH][128 * 32];
   __shared__ uint32_t cmax[NH][8][128];
   __shared__ float csum[8][128];
+  __shared__ int slow;  // a column's scale needs the division
   __shared__ float2 cs[NH][128];  // a column's scale and its reciprocal, column 8 cl + e at 16 e + cl
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int cl = tid & 15, rg = tid >> 4;
-  const int64_t nf = p.N / 128, nm = (p.M + 127) / 128;
   // Order of tiles: each XCD a contiguous part (ids go to the eight in turn),
   // and in it sixteen token blocks of a feature block after one another, whose
   // transposed pieces adjoin.
-  int64_t id = blockIdx.x;
+  const uint32_t nf = (uint32_t)(p.N / 128), nm = (uint32_t)((p.M + 127) / 128);  // fewer than 2^23 tiles
+  uint32_t id = blockIdx.x;
   if (nf * nm % 8 == 0) id = (id & 7) * (nf * nm / 8) + (id >> 3);
-  const int64_t grp = id / (16 * nf), r16 = id - grp * 16 * nf, gs = nm - grp * 16 < 16 ? nm - grp * 16 : 16;
-  const int64_t fb = r16 / gs, mb = grp * 16 + r16 % gs;
-  const int64_t f0 = fb * 128, m0 = mb * 128;
+  const uint32_t grp = id / (16 * nf), r16 = id - grp * 16 * nf, gs = nm - grp * 16 < 16 ? nm - grp * 16 : 16;
+  const uint32_t fb = r16 / gs, mb = grp * 16 + r16 % gs;
+  const int64_t f0 = (int64_t)fb * 128, m0 = (int64_t)mb * 128;
   const int64_t col = f0 + 8 * cl;
 
   float v[NH][4][8];  // d, h
   with_linear_act(p.act, [&](auto act) {
     constexpr int ACT = decltype(act)::value;
+    constexpr bool PRE = ACT != FP8Q_ACT_NONE || NH == 2;
+    Raw8<DC> dc[4];
+    Raw8<FP8Q_BF16> g[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      // rows past M read the last one, and their values count as zero
-      const bool in = m0 + 4 * rg + q < p.M;
-      const int64_t row = in ? m0 + 4 * rg + q : p.M - 1;
-      Raw8<DC> dc;
-      Raw8<FP8Q_BF16> g;
-      dc.load(p.dc, row * p.lddc + col);
-      if (ACT != FP8Q_ACT_NONE || NH == 2) g.load(p.pre, row * p.ldpre + col);
+      // rows past M read the last one; zeros for both make d and h zero
+      const int64_t at = m0 + 4 * rg + q, row = at < p.M ? at : p.M - 1;
+      dc[q].load(p.dc, row * p.lddc + col);
+      if constexpr (PRE) g[q].load(p.pre, row * p.ldpre + col);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (m0 + 4 * rg + q >= p.M) {
+        dc[q].fill(0.0f);
+        if constexpr (PRE) g[q].fill(0.0f);
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         float h = 0.0f;
-        const float d = ACT == FP8Q_ACT_NONE && NH == 1 ? dc[e] : linear_act_bwd<ACT>(dc[e], g[e], h);
-        v[0][q][e] = in ? d : 0.0f;
-        if constexpr (NH == 2) v[1][q][e] = in ? h : 0.0f;
+        if constexpr (PRE) v[0][q][e] = linear_act_bwd<ACT>(dc[q][e], g[q][e], h);
+        else v[0][q][e] = dc[q][e];
+        if constexpr (NH == 2) v[1][q][e] = h;
       }
     }
   });
 
-  // along features
+  // along features: four rows' scales, then their codes, by the quick quotient
+  // where every lane's scale allows it
+  {
+    float s[4], r[4];
+    bool ok = true;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int64_t row = m0 + 4 * rg + q;
-    if (row >= p.M) continue;  // 16 lanes share a row
-    const float(&x)[8] = v[0][q];
-    uint32_t m = 0;
+    for (int q = 0; q < 4; ++q) {
+      float m = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, abs_bits(x[e]));
-    const float s = block_scale7<FC>(__uint_as_float(canon_abs_bits(row16_max(m))), p.eps);
-    const float r = 1.0f / s;
-    const bool fast = scale_ok(s);
-    const u32x2 w = {encode4<FC>(x[0], x[1], x[2], x[3], s, r, fast), encode4<FC>(x[4], x[5], x[6], x[7], s, r, fast)};
-    __builtin_nontemporal_store(w, (u32x2*)(p.d + row * p.ldd + col));
-    if (cl == 0) p.ds[row * p.ld_ds + fb] = s;
+      for (int e = 0; e < 8; ++e) m = max_abs(m, v[0][q][e]);
+      s[q] = block_scale7<FC>(__uint_as_float(canon_abs_bits(row16_max(__float_as_uint(m)))), p.eps);
+      r[q] = recip(s[q]);
+      ok = ok && scale_ok(s[q]);
+    }
+    auto codes = [&](auto fast) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t row = m0 + 4 * rg + q;
+        const float(&x)[8] = v[0][q];
+        const bool f = decltype(fast)::value || scale_ok(s[q]);
+        const u32x2 w = {encode4<FC>(x[0], x[1], x[2], x[3], s[q], r[q], f),
+                         encode4<FC>(x[4], x[5], x[6], x[7], s[q], r[q], f)};
+        if (row < p.M) {  // 16 lanes share a row
+          __builtin_nontemporal_store(w, (u32x2*)(p.d + row * p.ldd + col));
+          if (cl == 0) p.ds[row * p.ld_ds + fb] = s[q];
+        }
+      }
+    };
+    if (__all(ok)) codes(std::true_type{});
+    else codes(std::false_type{});
   }
 
-  // along tokens
+  // along tokens.  The wavefront's four row groups meet in its registers: two
+  // exchanges of halves and of rows of 16 lanes, each joining two columns at once,
+  // leave lane group j with columns 2j and 2j + 1 of the eight.
+  auto join = [&](auto op, uint32_t(&x)[8]) {
+    uint32_t y[4];
 #pragma unroll
-  for (int k = 0; k < NH; ++k)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      uint32_t m = max(max(abs_bits(v[k][0][e]), abs_bits(v[k][1][e])), max(abs_bits(v[k][2][e]), abs_bits(v[k][3][e])));
-      m = max(m, (uint32_t)__shfl_xor((int)m, 16));
-      m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-      if (lane < 16) cmax[k][wave][16 * e + cl] = m;
+    for (int e = 0; e < 4; ++e) {
+      const auto t = __builtin_amdgcn_permlane32_swap(x[e], x[e + 4], false, false);
+      y[e] = op(t[0], t[1]);
     }
-  if (p.ws) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float a = (v[0][0][e] + v[0][1][e]) + (v[0][2][e] + v[0][3][e]);
-      a += __shfl_xor(a, 16);
-      a += __shfl_xor(a, 32);
-      if (lane < 16) csum[wave][16 * e + cl] = a;
+    for (int e = 0; e < 2; ++e) {
+      const auto t = __builtin_amdgcn_permlane16_swap(y[e], y[e + 2], false, false);
+      x[e] = op(t[0], t[1]);
     }
+  };
+  const int slot = 32 * (lane >> 4) + cl;  // column 8 cl + e at 16 e + cl
+  auto larger = [](uint32_t a, uint32_t b) { return max(a, b); };
+  auto added = [](uint32_t a, uint32_t b) { return __float_as_uint(__uint_as_float(a) + __uint_as_float(b)); };
+#pragma unroll
+  for (int k = 0; k < NH; ++k) {
+    uint32_t m[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      m[e] = __float_as_uint(max_abs(max_abs(max_abs(__builtin_fabsf(v[k][0][e]), v[k][1][e]), v[k][2][e]), v[k][3][e]));
+    join(larger, m);
+    cmax[k][wave][slot] = m[0];
+    cmax[k][wave][slot + 16] = m[1];
   }
+  if (p.ws) {
+    uint32_t a[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[e] = __float_as_uint((v[0][0][e] + v[0][1][e]) + (v[0][2][e] + v[0][3][e]));
+    join(added, a);
+    csum[wave][slot] = __uint_as_float(a[0]);
+    csum[wave][slot + 16] = __uint_as_float(a[1]);
+  }
+  if (tid == 0) slow = 0;
   __syncthreads();
   if (tid < 128 * NH) {
     const int k = tid >> 7, c = tid & 127, at = (c & 7) * 16 + (c >> 3);
@@ -116,7 +158,8 @@ __global__ __launch_bounds__(512, 4) void k_linear_bwd(const LinearBwd p) {
     for (int w = 0; w < 8; ++w) m = max(m, cmax[k][w][at]);
     const float amax = __uint_as_float(canon_abs_bits(m));
     const float s = k == 0 ? block_scale7<FC>(amax, p.eps) : block_scale7<FH>(amax, p.eps);
-    cs[k][at] = make_float2(s, 1.0f / s);
+    cs[k][at] = make_float2(s, recip(s));
+    if (!scale_ok(s)) slow = 1;
     if (k == 0) {
       if (p.dt_) p.dts[(f0 + c) * p.ld_dts + mb] = s;
     } else {
@@ -131,15 +174,19 @@ __global__ __launch_bounds__(512, 4) void k_linear_bwd(const LinearBwd p) {
   }
   if (!p.dt_ && NH == 1) return;
   __syncthreads();
+  auto codes_t = [&](auto fast) {
 #pragma unroll
-  for (int k = 0; k < NH; ++k)
+    for (int k = 0; k < NH; ++k)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float s = cs[k][16 * e + cl].x, r = cs[k][16 * e + cl].y;
-      const bool fast = scale_ok(s);
-      tile[k][tr_slot(8 * cl + e, rg)] = k == 0 ? encode4<FC>(v[k][0][e], v[k][1][e], v[k][2][e], v[k][3][e], s, r, fast)
-                                                : encode4<FH>(v[k][0][e], v[k][1][e], v[k][2][e], v[k][3][e], s, r, fast);
-    }
+      for (int e = 0; e < 8; ++e) {
+        const float s = cs[k][16 * e + cl].x, r = cs[k][16 * e + cl].y;
+        const bool f = decltype(fast)::value || scale_ok(s);
+        tile[k][tr_slot(8 * cl + e, rg)] = k == 0 ? encode4<FC>(v[k][0][e], v[k][1][e], v[k][2][e], v[k][3][e], s, r, f)
+                                                  : encode4<FH>(v[k][0][e], v[k][1][e], v[k][2][e], v[k][3][e], s, r, f);
+      }
+  };
+  if (slow == 0) codes_t(std::true_type{});
+  else codes_t(std::false_type{});
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < NH; ++k) {
