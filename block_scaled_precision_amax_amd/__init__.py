@@ -375,8 +375,9 @@ def fp8q_gemm_blockscaled_qt(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, gb, 
 
 def _same_dt(t, *others) -> int:
     """The element type of t, which the tensors among `others` must share."""
+    dtype = t.dtype
     for o in others:
-        if o is not None and not isinstance(o, int) and o.dtype != t.dtype:
+        if o is not None and o.__class__ is not int and o.dtype is not dtype:
             raise TypeError(f"these operands share one dtype, got {t.dtype} and {o.dtype}")
     return _dt(t)
 
@@ -447,36 +448,43 @@ def fp8q_gemm_blockscaled_few(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, gb,
 _get_device = None
 
 
-def _place(stream, *operands):
-    """The device of the operands that are tensors (-1: all are raw pointers) and the stream's handle.  A host tensor's
-    address, or one of another device, would fault in the kernel: both are refused."""
-    dev, first = -1, operands[0]
+def _place(operands) -> int:
+    """The device of the operands that are tensors (-1: all are raw pointers).  A host tensor's address, or one of another
+    device, would fault in the kernel: both are refused."""
+    dev = -1
     for t in operands:
-        if t is None or isinstance(t, int):
+        if t is None or t.__class__ is int:
             continue
         d = t.get_device()
-        if d < 0:
-            raise ValueError("this operand is not on a GPU")
-        if dev < 0:
-            dev, first = d, t
-        elif d != dev:
-            raise ValueError(f"these operands share one device, got cuda:{dev} and cuda:{d}")
-    return dev, _stream(stream, first)
+        if d != dev or d < 0:
+            if d < 0:
+                raise ValueError("this operand is not on a GPU")
+            if dev >= 0:
+                raise ValueError(f"these operands share one device, got cuda:{dev} and cuda:{d}")
+            dev = d
+    return dev
 
 
-def _on(dev, call):
-    """call() with `dev` as the current device, on which kernels are launched."""
-    global _get_device
+def _launch(fn, args, dev, stream) -> None:
+    """fn(*args, stream's handle) with `dev` as the current device, on which kernels are launched."""
+    global _get_device, _raw_stream
+    if dev < 0:  # raw pointers alone
+        _check(fn(*args, _stream(stream)))
+        return
     if _get_device is None:
         import torch
 
-        _get_device = torch._C._cuda_getDevice
-    if dev < 0 or _get_device() == dev:
-        return call()
-    import torch
+        _get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    handle = _raw_stream(dev) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
+    if _get_device() == dev:
+        rc = fn(*args, handle)
+    else:
+        import torch
 
-    with torch.cuda.device(dev):
-        return call()
+        with torch.cuda.device(dev):
+            rc = fn(*args, handle)
+    if rc:
+        _check(rc)
 
 
 def fp8q_layernorm_1x128(x, ldx, res, ldr, w, b, rows, cols, norm_eps, z, ldz, y, ldy, f, eps, q, ldq, scales, ld_s,
@@ -485,8 +493,7 @@ def fp8q_layernorm_1x128(x, ldx, res, ldr, w, b, rows, cols, norm_eps, z, ldz, y
     wdt = F32 if w is None and b is None else _same_dt(b if w is None else w, b)
     args = (_ptr(x), _same_dt(x, res, z, y), ldx, _ptr(res), ldr, _ptr(w), _ptr(b), wdt, rows, cols, norm_eps, _ptr(z), ldz,
             _ptr(y), ldy, f, eps, _codes(q), ldq, _f32(scales), ld_s, _f32(mean), _f32(rstd))
-    dev, handle = _place(stream, x, res, w, b, z, y, q, scales, mean, rstd)
-    _check(_on(dev, lambda: lib().fp8q_layernorm_1x128(*args, handle)))
+    _launch(lib().fp8q_layernorm_1x128, args, _place((x, res, w, b, z, y, q, scales, mean, rstd)), stream)
 
 
 def fp8q_layernorm_bwd_workspace(rows, cols) -> int:
@@ -497,8 +504,7 @@ def fp8q_layernorm_bwd(dy, lddy, z, ldz, w, mean, rstd, dres, lddr, rows, cols, 
                        ws_bytes=0, stream=None) -> None:
     args = (_ptr(dy), _same_dt(dy, z, dres, dx), lddy, _ptr(z), ldz, _ptr(w), F32 if w is None else _dt(w), _f32(mean),
             _f32(rstd), _ptr(dres), lddr, rows, cols, _ptr(dx), lddx, _f32(dw), _f32(db), _ptr(ws), ws_bytes)
-    dev, handle = _place(stream, dy, z, w, mean, rstd, dres, dx, dw, db, ws)
-    _check(_on(dev, lambda: lib().fp8q_layernorm_bwd(*args, handle)))
+    _launch(lib().fp8q_layernorm_bwd, args, _place((dy, z, w, mean, rstd, dres, dx, dw, db, ws)), stream)
 
 
 def fp8q_linear_blockscaled_workspace(fast, codes, M, N, K) -> int:
@@ -507,17 +513,14 @@ def fp8q_linear_blockscaled_workspace(fast, codes, M, N, K) -> int:
 
 def _linear(fn, fast, codes, args, sizes, ws, ws_bytes, stream, operands) -> None:
     """A linear layer's call: args up to its sizes; without `ws`, what it needs comes from torch's allocator."""
-    dev, handle = _place(stream, *operands, ws)
-
-    def call():
-        w, n = ws, ws_bytes
-        if w is None:
-            n = lib().fp8q_linear_blockscaled_workspace(fast, codes, *sizes)
-            if n:
-                w = _workspace(n, handle, stream, next((t for t in operands if t is not None and not isinstance(t, int)), 0))
-        return fn(*args, *sizes, _ptr(w), n, handle)
-
-    _check(_on(dev, call))
+    dev = _place((*operands, ws))
+    if ws is None:
+        # one device's answer for every device of its kind
+        ws_bytes = lib().fp8q_linear_blockscaled_workspace(fast, codes, *sizes)
+        if ws_bytes:
+            t = next((t for t in operands if t is not None and t.__class__ is not int), 0)
+            ws = _workspace(ws_bytes, _stream(stream, t), stream, t)
+    _launch(fn, (*args, *sizes, _ptr(ws), ws_bytes), dev, stream)
 
 
 def fp8q_linear_blockscaled(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, sB_sn, sB_skb, bias, act, res, ldr, C, ldc, pre,
@@ -559,5 +562,4 @@ def fp8q_linear_bwd_q(dC, lddc, pre, ldpre, act, fc, eps, Dq, lddq, Ds, ld_ds, D
                       ld_hst, dbias, M, N, ws=None, ws_bytes=0, stream=None) -> None:
     args = (_ptr(dC), _dt(dC), lddc, _bf16(pre), ldpre, act, fc, eps, _codes(Dq), lddq, _f32(Ds), ld_ds, _codes(Dt), lddt,
             _f32(Dst), ld_dst, fh, _codes(Ht), ldht, _f32(Hst), ld_hst, _f32(dbias), M, N, _ptr(ws), ws_bytes)
-    dev, handle = _place(stream, dC, pre, Dq, Ds, Dt, Dst, Ht, Hst, dbias, ws)
-    _check(_on(dev, lambda: lib().fp8q_linear_bwd_q(*args, handle)))
+    _launch(lib().fp8q_linear_bwd_q, args, _place((dC, pre, Dq, Ds, Dt, Dst, Ht, Hst, dbias, ws)), stream)
