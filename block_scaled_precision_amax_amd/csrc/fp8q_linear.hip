@@ -47,48 +47,89 @@ __device__ __forceinline__ void store_edge8(void* p, int64_t i, const float (&v)
   }
 }
 
-// Everything behind the sums of one row's columns col .. col + 7 (col a
-// multiple of eight, col < N): v are the sums, b their bias.  Sixteen
-// neighbouring lanes hold a block of 128 columns.
-template <int OUT>
-__device__ __forceinline__ void finish8(const Proj& p, const Epilogue& e, int64_t row, int64_t col, float (&v)[8],
-                                        const float (&b)[8]) {
+// Everything behind the sums of U rows' columns col .. col + 7 (col a multiple
+// of eight, col < N): v are the sums, b their bias, in[u] whether row u exists
+// (the same for the sixteen lanes that hold a block of 128 columns).  The rows
+// go side by side, so that one's long chain (exponential, reciprocal, block
+// maximum, quotient) fills the other's waits.
+template <int OUT, int ACT, int U>
+__device__ __forceinline__ void finish8(const Proj& p, const Epilogue& e, const int64_t (&row)[U], const bool (&in)[U],
+                                        int64_t col, float (&v)[U][8], const float (&b)[8]) {
   const int64_t left = p.N - col;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] += b[k];
-  if (e.pre) store_edge8<FP8Q_BF16>(e.pre, row * e.ldpre + col, v, left, e.vp);
-  with_linear_act(e.act, [&](auto act) {
+  for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = linear_act<decltype(act)::value>(v[k]);
-  });
+    for (int k = 0; k < 8; ++k) v[u][k] += b[k];
+  if (e.pre) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (in[u]) store_edge8<FP8Q_BF16>(e.pre, row[u] * e.ldpre + col, v[u], left, e.vp);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[u][k] = linear_act<ACT>(v[u][k]);
   if constexpr (OUT < 2) {
     if (e.res) {
-      const int64_t i = row * e.ldr + col;
       if (e.vr && left >= 8) {
-        Raw8<OUT> r;
-        r.load(e.res, i);
+        Raw8<OUT> r[U];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] += r[k];
+        for (int u = 0; u < U; ++u)
+          if (in[u]) r[u].load(e.res, row[u] * e.ldr + col);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[u][k] += r[u][k];
       } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k < left) v[k] += OUT == FP8Q_F32 ? ((const float*)e.res)[i + k] : bf_lo(((const uint16_t*)e.res)[i + k]);
+        for (int u = 0; u < U; ++u) {
+          const int64_t i = row[u] * e.ldr + col;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (in[u] && k < left)
+              v[u][k] += OUT == FP8Q_F32 ? ((const float*)e.res)[i + k] : bf_lo(((const uint16_t*)e.res)[i + k]);
+        }
       }
     }
-    store_edge8<OUT>(p.out, row * p.ldo + col, v, left, e.vo);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (in[u]) store_edge8<OUT>(p.out, row[u] * p.ldo + col, v[u], left, e.vo);
   } else {
     // N is a multiple of 128: the sixteen lanes of a block are all here
     constexpr int QF = OUT - 2;
-    float m = 0.0f;
+    float s[U], r[U];
+    bool ok = true;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = max_abs(m, v[k]);
-    const float s = block_scale7<QF>(__uint_as_float(canon_abs_bits(row16_max(__float_as_uint(m)))), p.eps);
-    const float inv = recip(s);
-    const bool fast = scale_ok(s);
-    const u32x2 q = {encode4<QF>(v[0], v[1], v[2], v[3], s, inv, fast), encode4<QF>(v[4], v[5], v[6], v[7], s, inv, fast)};
-    __builtin_nontemporal_store(q, (u32x2*)((uint8_t*)p.out + row * p.ldo + col));
-    if ((threadIdx.x & 15) == 0) p.scales[row * p.ld_s + (col >> 7)] = s;
+    for (int u = 0; u < U; ++u) {
+      float m = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = max_abs(m, v[u][k]);
+      s[u] = block_scale7<QF>(__uint_as_float(canon_abs_bits(row16_max(__float_as_uint(m)))), p.eps);
+      r[u] = recip(s[u]);
+      ok = ok && scale_ok(s[u]);
+    }
+    auto codes = [&](auto fast) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float(&x)[8] = v[u];
+        const bool f = decltype(fast)::value || scale_ok(s[u]);
+        const u32x2 q = {encode4<QF>(x[0], x[1], x[2], x[3], s[u], r[u], f), encode4<QF>(x[4], x[5], x[6], x[7], s[u], r[u], f)};
+        if (!in[u]) continue;
+        __builtin_nontemporal_store(q, (u32x2*)((uint8_t*)p.out + row[u] * p.ldo + col));
+        if ((threadIdx.x & 15) == 0) p.scales[row[u] * p.ld_s + (col >> 7)] = s[u];
+      }
+    };
+    if (__all(ok)) codes(std::true_type{});
+    else codes(std::false_type{});
   }
+}
+// One row, any activation.
+template <int OUT>
+__device__ __forceinline__ void finish8(const Proj& p, const Epilogue& e, int64_t row, int64_t col, float (&v)[1][8],
+                                        const float (&b)[8]) {
+  const int64_t rows[1] = {row};
+  const bool in[1] = {true};
+  with_linear_act(e.act, [&](auto act) { finish8<OUT, decltype(act)::value, 1>(p, e, rows, in, col, v, b); });
 }
 
 // Tiles of BM rows x 256 columns.  The sums of a whole tile pass through LDS as
@@ -140,8 +181,9 @@ __global__ __launch_bounds__(kThreads, 1) void k_linear(const Proj p, const floa
       }
       continue;
     }
-#pragma unroll
-    for (int h0 = 0; h0 < 2; h0 += AT_ONCE) {
+    // the half is a constant: indexed by a variable, the sums would leave the registers
+    auto drain = [&](auto first) {
+      constexpr int h0 = decltype(first)::value;
 #pragma unroll
       for (int h = h0; h < h0 + AT_ONCE; ++h)
 #pragma unroll
@@ -152,27 +194,36 @@ __global__ __launch_bounds__(kThreads, 1) void k_linear(const Proj p, const floa
             *(v4f*)(lds + (h - h0) * HALF + r * 512 + 16 * (c ^ (r & 15))) = acc[i][2 * h + j];
           }
       __syncthreads();
+      with_linear_act(ep.act, [&](auto act) {
+        constexpr int U = BM < 128 ? BM / 32 : 4;  // 16384 x 18432 x 7168 FP8-MFMA with GELU: 2136 us, one row at a time 2258
+        for (int h = h0; h < h0 + AT_ONCE; ++h) {
+          const int c = 2 * (tid & 15);
+          const int64_t col = n0 + 128 * h + 4 * c;
+          if (col >= N) continue;
+          float b[8];
+          load_bias8(ep, col, N, b);
+          for (int it = 0; it < BM / 32; it += U) {
+            int64_t row[U];
+            bool in[U];
+            float v[U][8];
 #pragma unroll
-      for (int h = h0; h < h0 + AT_ONCE; ++h) {
-        const int c = 2 * (tid & 15);
-        const int64_t col = n0 + 128 * h + 4 * c;
-        float b[8];
-        load_bias8(ep, col, N, b);
-        if (col < N) {
-#pragma unroll 2
-          for (int it = 0; it < BM / 32; ++it) {
-            const int r = it * 32 + (tid >> 4);
-            const int64_t row = m0 + r;
-            if (row >= M) break;
-            const uint8_t* at = lds + (h - h0) * HALF + r * 512;
-            const v4f x = *(const v4f*)(at + 16 * (c ^ (r & 15))), y = *(const v4f*)(at + 16 * ((c + 1) ^ (r & 15)));
-            float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-            finish8<OUT>(p, ep, row, col, v, b);
+            for (int u = 0; u < U; ++u) {
+              const int r = (it + u) * 32 + (tid >> 4);
+              row[u] = m0 + r;
+              in[u] = row[u] < M;
+              const uint8_t* at = lds + (h - h0) * HALF + r * 512;
+              const v4f x = *(const v4f*)(at + 16 * (c ^ (r & 15))), y = *(const v4f*)(at + 16 * ((c + 1) ^ (r & 15)));
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v[u][k] = x[k], v[u][4 + k] = y[k];
+            }
+            finish8<OUT, decltype(act)::value, U>(p, ep, row, in, col, v, b);
           }
         }
-      }
+      });
       __syncthreads();  // before the other half, or the next tile's copies
-    }
+    };
+    drain(std::integral_constant<int, 0>{});
+    if constexpr (AT_ONCE == 1) drain(std::integral_constant<int, 1>{});
   }
 }
 
@@ -193,14 +244,14 @@ __global__ __launch_bounds__(256) void k_linear_join(const Proj p, const Epilogu
   const int wave = 4 * (i / TI) + c / 32, reg = (i % TI) * TJ + 2 * h + (c / 16 & 1), lane = 16 * (c / 4 & 3) + lr;
   const float* w = p.ws + at * (BM * 256) + wave * (TI * TJ * 256) + reg * 256 + lane * 4;
   v4f x = *(const v4f*)w, y = *(const v4f*)(w + 64);
-#pragma unroll 4
+#pragma unroll 8
   for (int k = 1; k < t.parts; ++k) {
     w += t.rest * (BM * 256);
     const v4f u = *(const v4f*)w, z = *(const v4f*)(w + 64);
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] += u[e], y[e] += z[e];
   }
-  float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+  float v[1][8] = {{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]}};
   finish8<OUT>(p, ep, row, col, v, b);
 }
 
@@ -211,12 +262,12 @@ __global__ __launch_bounds__(256) void k_linear_finish(const Proj p, const Epilo
   const int64_t nb = p.N / 128, g = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);  // a row's 128 columns
   const int64_t row = g / nb, col = (g - row * nb) * 128 + 8 * (threadIdx.x & 15);
   if (row >= p.M) return;
-  float b[8], v[8];
+  float b[8], v[1][8];
   load_bias8(ep, col, p.N, b);
   Raw8<FP8Q_F32> x;
   x.load(p.ws, row * p.N + col);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] = x[k];
+  for (int k = 0; k < 8; ++k) v[0][k] = x[k];
   finish8<OUT>(p, ep, row, col, v, b);
 }
 
