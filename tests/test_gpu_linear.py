@@ -655,114 +655,49 @@ def test_explicit_streams(fq, gpu):
         assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))
 
 
-class Mlp:
-    """norm -> up (GELU, codes) -> down (residual) and back, on buffers of its own."""
+def example():
+    import importlib.util
+    import os
 
-    def __init__(self, fq, gpu, M, K, F, seed=0):
-        self.fq, self.M, self.K, self.F, self.Mp = fq, M, K, F, -(-M // 128) * 128
-        g = torch.Generator(device=gpu).manual_seed(seed)
-        rand = lambda *s, std=1.0: torch.randn(*s, generator=g, device=gpu) * std  # noqa: E731
-        self.w, self.b = 1 + rand(K, std=0.1), rand(K, std=0.1)
-        self.w1, self.b1 = rand(F, K, std=K ** -0.5), rand(F, std=0.3)
-        self.w2, self.b2 = rand(K, F, std=F ** -0.5), rand(K, std=0.3)
-        self.x, self.r, self.dy = (rand(M, K).bfloat16() for _ in range(3))
-        self.dy = self.dy * 1e-3
-        quant = {}
-        for n, m in (("1", self.w1), ("2", self.w2), ("1t", self.w1.t().contiguous()), ("2t", self.w2.t().contiguous())):
-            q, s = self.codes(*m.shape, 128)
-            fq.fp8q_quantize_128x128(m, m.shape[0], m.shape[1], m.shape[1], E4, EPS, q, m.shape[1], s, m.shape[1] // 128)
-            quant[n] = (q, s)
-        self.W = quant
-        bf = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device=gpu)  # noqa: E731
-        Mp = self.Mp
-        self.z, self.n, self.pre, self.y, self.dh, self.dn, self.dx = (bf(M, K), bf(M, K), bf(M, F), bf(M, K), bf(M, F), bf(M, K),
-                                                                       bf(M, K))
-        self.nq, self.hq, self.gq, self.dq = (self.codes(M, c) for c in (K, F, K, F))
-        self.gt, self.dt, self.ht, self.nt = (self.codes(c, Mp) for c in (K, F, F, K))
-        f4 = lambda n: torch.empty(n, device=gpu)  # noqa: E731
-        self.mean, self.rstd, self.dw, self.db, self.db1, self.db2 = f4(M), f4(M), f4(K), f4(K), f4(F), f4(K)
-        self.dw1, self.dw2 = torch.empty(F, K, device=gpu), torch.empty(K, F, device=gpu)
-        self.ws = f4(max(fq.fp8q_layernorm_bwd_workspace(M, K), fq.fp8q_linear_bwd_q_workspace(M, max(K, F))) // 4 + 4)
-        self.npad = torch.zeros(Mp, K, dtype=torch.bfloat16, device=gpu)
-
-    def codes(self, r, c, br=1):
-        return (torch.empty(r, c, dtype=torch.uint8, device="cuda"), torch.empty(-(-r // br), c // 128, device="cuda"))
-
-    def forward(self):
-        fq, M, K, F = self.fq, self.M, self.K, self.F
-        fq.fp8q_layernorm_1x128(self.x, K, self.r, K, self.w, self.b, M, K, NEPS, self.z, K, self.n, K, E4, EPS, self.nq[0], K,
-                                self.nq[1], K // 128, self.mean, self.rstd)
-        call(fq, self.nq[0], E4, self.nq[1], self.W["1"][0], E4, self.W["1"][1], self.b1, ERF, self.hq[0], M, F, K, True, None,
-             self.pre, q=(E4, self.hq[1]))
-        call(fq, self.hq[0], E4, self.hq[1], self.W["2"][0], E4, self.W["2"][1], self.b2, NONE, self.y, M, K, F, True, self.z)
-
-    def backward(self):
-        fq, M, K, F, Mp = self.fq, self.M, self.K, self.F, self.Mp
-        wsb = self.ws.numel() * 4
-
-        def prod(q, f, k, w, out):
-            fq.fp8q_gemm_blockscaled_fast(q[0], f, k, q[1], k // 128, 1, w[0], E4, k, w[1], fq.GRAN_128x128, k // 128, 1, out,
-                                          out.shape[1], M, out.shape[1], k)
-
-        def wgrad(a, b, out):
-            fq.fp8q_gemm_blockscaled_fast(a[0], E5, Mp, a[1], Mp // 128, 1, b[0], E4, Mp, b[1], fq.GRAN_1x128, Mp // 128, 1, out,
-                                          out.shape[1], out.shape[0], out.shape[1], Mp)
-
-        # the down layer: no activation, so no pre-activations and no output again
-        fq.fp8q_linear_bwd_q(self.dy, K, None, 0, NONE, E5, EPS, self.gq[0], K, self.gq[1], K // 128, self.gt[0], Mp, self.gt[1],
-                             Mp // 128, E4, None, 0, None, 0, self.db2, M, K, self.ws, wsb)
-        prod(self.gq, E5, K, self.W["2t"], self.dh)
-        fq.fp8q_linear_bwd_q(self.dh, F, self.pre, F, ERF, E5, EPS, self.dq[0], F, self.dq[1], F // 128, self.dt[0], Mp, self.dt[1],
-                             Mp // 128, E4, self.ht[0], Mp, self.ht[1], Mp // 128, self.db1, M, F, self.ws, wsb)
-        wgrad(self.gt, self.ht, self.dw2)
-        self.npad[:M] = self.n
-        fq.fp8q_quantize_1x128_t(self.npad, Mp, K, K, E4, EPS, self.nt[0], Mp, self.nt[1], Mp // 128)
-        wgrad(self.dt, self.nt, self.dw1)
-        prod(self.dq, E5, F, self.W["1t"], self.dn)
-        fq.fp8q_layernorm_bwd(self.dn, K, self.z, K, self.w, self.mean, self.rstd, self.dy, K, M, K, self.dx, K, self.dw, self.db,
-                              self.ws, wsb)
-
-    def step(self):
-        self.forward()
-        self.backward()
-        return [t.clone() for t in (self.y, self.dx, self.dw, self.db, self.dw1, self.db1, self.dw2, self.db2)]
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "mlp.py")
+    spec = importlib.util.spec_from_file_location("mlp_example", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
 
 
-def test_mlp_against_64_bits(fq, gpu):
-    """The four operators as a layer uses them: outputs and every gradient against the same layer in 64 bits."""
-    m = Mlp(fq, gpu, 150, 512, 1024)
-    got = m.step()
-    leaves = [t.double().requires_grad_() for t in (m.x, m.w, m.b, m.w1, m.b1, m.w2, m.b2)]
-    x, w, b, w1, b1, w2, b2 = leaves
-    z = x + m.r.double()
-    c = z - z.mean(1, keepdim=True)
-    n = c / torch.sqrt((c * c).mean(1, keepdim=True) + NEPS) * w + b
-    v = n @ w1.t() + b1
-    y = (v * torch.special.ndtr(v)) @ w2.t() + b2 + z
-    grads = torch.autograd.grad(y, leaves, m.dy.double())
-    # each operand's codes are off by up to 2^-4 (E4M3) or 2^-3 (E5M2) of a value, as independent errors of a third
-    # to a half of that root mean square; a product of two such operands, chained twice, stays within 15%
-    for a, r in zip(got, (y, *grads)):
-        assert float((a.double() - r.detach()).norm() / r.detach().norm()) <= 0.15
+@pytest.mark.parametrize("tokens,K,F", [(150, 512, 1024), (1, 128, 256), (300, 1024, 2048)])
+def test_mlp_against_64_bits(gpu, tokens, K, F):
+    """The operators as a layer uses them: outputs and every gradient against the same layer in 64 bits.  Each operand's
+    codes are off by up to 2^-4 (E4M3) or 2^-3 (E5M2) of a value, as independent errors of a third to a half of that root
+    mean square; a product of two such operands, chained twice, stays within 15%."""
+    res = example().main(tokens, K, F)
+    assert len(res) == 9 and max(res.values()) <= 0.15, res
 
 
 @pytest.mark.parametrize("M", [3, 150, 1100])
-def test_mlp_captured_in_a_graph(fq, gpu, M):
+def test_mlp_captured_in_a_graph(gpu, M):
     """A step captured once and replayed on changing inputs, eager work in between, equals the eager step bit for bit."""
-    m = Mlp(fq, gpu, M, 512, 1024)
-    m.step()
+    ex = example()
+    params, (x, r, dy) = ex.inputs(M, 512, 1024, gpu)
+    layer = ex.Mlp(*params)
+
+    def step():
+        y, saved = layer.forward(x, r)
+        return [y, *layer.backward(saved, dy), layer.token(x[:3], r[:3])]
+
+    step()
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        m.forward()
-        m.backward()
+        out = step()
     for i in range(4):
-        m.x.copy_(torch.randn(m.x.shape, generator=torch.Generator(gpu).manual_seed(i), device=gpu))
-        m.dy.mul_(0.5)
+        x.copy_(torch.randn(x.shape, generator=torch.Generator(gpu).manual_seed(i), device=gpu))
+        dy.mul_(0.5)
         graph.replay()
         torch.cuda.synchronize()
-        got = [t.clone() for t in (m.y, m.dx, m.dw, m.db, m.dw1, m.db1, m.dw2, m.db2)]
-        want = m.step()
+        got = [t.clone() for t in out]
+        want = step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
