@@ -135,6 +135,53 @@ def test_layernorm(fq, orc, gpu, rows, cols, dt):
         assert np.array_equal(q.cpu().numpy(), wq) and np.array_equal(s.cpu().numpy(), ws)
 
 
+@pytest.mark.parametrize("rows,cols,dt", [(2050, 4104, torch.float32), (2051, 8192, torch.float32), (4100, 8200, torch.bfloat16),
+                                          (4099, 16384, torch.float32), (4096, 9088, torch.bfloat16)])
+def test_layernorm_of_many_wide_rows(fq, gpu, rows, cols, dt):
+    """Rows walked by one workgroup a compute unit: against 64 bits, in place, codes as the quantizer makes them."""
+    codes = cols % 128 == 0
+    x = (W.activation(rows, cols, seed=2, factor=30.0, device=gpu, dtype=torch.float32) + 3).to(dt)
+    r = W.normal((rows, cols), seed=5, device=gpu, std=2.0, dtype=dt) if rows % 2 else None
+    w = 1 + W.normal((cols,), seed=6, device=gpu, std=0.1, dtype=torch.float32)
+    b = W.normal((cols,), seed=7, device=gpu, std=0.3, dtype=torch.float32) if rows != 2051 else None
+    x[7, 5] = float("nan")
+    z, y, q, s, mean, rstd = run_norm(fq, x, r, w, b, E4, pad=64, codes=codes)
+    keep = torch.arange(rows, device=gpu) != 7
+    assert y[7].isnan().all() and y[keep].isfinite().all()
+    for a in range(0, rows, 1024):
+        k = torch.arange(a, min(rows, a + 1024), device=gpu)
+        k = k[k != 7]
+        v, m, rs, yr, tm, trs, ty = norm_ref(x[k], None if r is None else r[k], w, b)
+        assert ((mean[k].double() - m).abs() <= tm).all() and ((rstd[k].double() - rs).abs() <= trs).all()
+        assert ((y[k].double() - yr).abs() <= ty + (BF * (yr.abs() + ty) if dt == torch.bfloat16 else 0)).all()
+    zf = (x.float() + (r.float() if r is not None else 0)).to(dt)
+    assert torch.equal(z[keep], zf[keep])
+    if codes and dt == torch.float32:
+        wq, wsc = torch.empty(rows, cols, dtype=torch.uint8, device=gpu), torch.empty(rows, cols // 128, device=gpu)
+        y = y.contiguous()
+        fq.fp8q_quantize_1x128(y, rows, cols, cols, E4, EPS, wq, cols, wsc, cols // 128)
+        assert torch.equal(q, wq) and torch.equal(s[keep], wsc[keep]) and s[7].isnan().all()
+    a = x.clone()
+    y2 = torch.empty_like(x)
+    fq.fp8q_layernorm_1x128(a, cols, r, cols, w, b, rows, cols, NEPS, a, cols, y2, cols, E4, EPS, None, 0, None, 0)
+    assert torch.equal(a[keep], zf[keep]) and torch.equal(y2[keep], y[:, :cols][keep])
+
+
+def test_layernorm_codes_of_extreme_blocks(fq, orc, gpu):
+    """Blocks whose scale leaves the quick quotient's range."""
+    cols = 640
+    x = torch.randn(6, cols, device=gpu)
+    w = torch.ones(cols, device=gpu)
+    w[128:256], w[256:384], w[384:512] = 1e30, 1e-35, 0.0
+    for eps in (1e-12, 1e-37):
+        for fmt in (E4, E5):
+            y, q, s = torch.empty_like(x), torch.empty(6, cols, dtype=torch.uint8, device=gpu), torch.empty(6, 5, device=gpu)
+            fq.fp8q_layernorm_1x128(x, cols, None, 0, w, None, 6, cols, NEPS, None, 0, y, cols, fmt, eps, q, cols, s, 5)
+            wq, wsc = torch.empty_like(q), torch.empty_like(s)
+            fq.fp8q_quantize_1x128(y, 6, cols, cols, fmt, eps, wq, cols, wsc, 5)
+            assert torch.equal(q, wq) and torch.equal(s, wsc)
+
+
 def test_layernorm_far_from_zero(fq, gpu):
     """Rows whose mean is a thousand times their spread: the variance is not lost."""
     x = 1000 + torch.randn(6, 2048, device=gpu, generator=torch.Generator(gpu).manual_seed(1))
@@ -203,7 +250,7 @@ def bwd_ref(dy, z, w, mean, rstd, dres):
 
 
 @pytest.mark.parametrize("rows,cols", [(1, 8), (3, 40), (1, 128), (3, 384), (2500, 128), (41, 1024), (700, 1608), (2300, 1920),
-                                       (700, 2304), (9, 7168), (1300, 4096), (5, 16384), (3, 18432), (2, 20008), (1, 65536)])
+                                       (700, 2304), (9, 7168), (1300, 4096), (701, 2504), (513, 4096), (5, 16384), (3, 18432), (2, 20008), (1, 65536)])
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
 def test_layernorm_bwd(fq, gpu, rows, cols, dt):
     pad = 64 if rows % 2 else 0
@@ -458,6 +505,114 @@ def test_linear_many_tiles(fq, gpu, M, N, K):
             assert torch.equal(q, wq) and torch.equal(s, ws)
 
 
+# Every way a call goes on 256 compute units (exact | FP8-MFMA): whole tiles of either height, one round and several, and
+# tiles in parts of K, alone and behind whole rounds; a few rows elsewhere.
+WAYS = [
+    (65, 256, 7168),     # low tiles in parts | low tiles in parts
+    (200, 18432, 4096),  # low tiles in parts behind a round | whole low tiles
+    (65, 9088, 512),     # whole low tiles | whole low tiles
+    (385, 18432, 512),   # two rounds of low tiles | whole tall tiles
+    (65, 18432, 7168),   # tall tiles in parts | low tiles in parts
+    (1000, 8960, 2048),  # tall tiles in parts behind a round | whole low tiles
+    (200, 18432, 512),   # whole tall tiles | whole low tiles
+    (3000, 4096, 512),   # two rounds of tall tiles | low tiles
+    (385, 18432, 7168),  # tall | low tiles in parts behind a round
+    (1000, 18432, 512),  # rounds of low or tall tiles, both
+    (1000, 18432, 4096), # tall | tall tiles in parts behind a round
+    (2049, 12928, 512),  # rounds | two rounds of tall tiles
+]
+
+
+@pytest.mark.parametrize("M,N,K", WAYS)
+@pytest.mark.parametrize("fast", [False, True])
+def test_linear_every_way(fq, gpu, M, N, K, fast):
+    """Formats, activations, biases, residuals and ragged columns in each; outputs against sampled rows, the other forms
+    against the fp32 one."""
+    i = WAYS.index((M, N, K))
+    fa, fb = (i // 2) % 2, i % 2
+    A, sA, B, sB = operands(gpu, M, N, K, fa, fb, 16 if i % 4 == 0 else 0, seed=i)
+    rows = torch.tensor(sorted({r for e in range(0, M, 64) for r in (e, e + 15, e + 63) if r < M} | {M - 1})[:40]
+                        + [M - 2, M - 1], device=gpu)
+    v, D = product(A[rows], fa, sA[rows], B, fb, sB, K)
+    for n, act in ((N, i % 5), (N - 3, (i + 1) % 5)):
+        bias = W.normal((n,), seed=3, device=gpu) if i % 3 else None
+        w = v[:, :n] + (bias.double() if bias is not None else 0)
+        res = W.normal((M, n), seed=5, device=gpu) if (i + n) % 2 else None
+        pre = torch.full((M, n + 1), 7.0, dtype=torch.bfloat16, device=gpu)
+        C = torch.full((M, n + 4), 7.0, device=gpu)
+        call(fq, A, fa, sA, B, fb, sB, bias, act, C, M, n, K, fast, res, pre)
+        tv = (2.0 ** -10 if fast else 1e-5) * D[:, :n] + 2 * U * w.abs()
+        want, _, ta, _ = act64(act, w)
+        if res is not None:
+            want = want + res[rows].double()
+        assert ((C[rows, :n].double() - want).abs() <= LIPSCHITZ * tv + 1.01 * ta + U * want.abs()).all()
+        assert ((pre[rows, :n].double() - w).abs() <= 1.01 * tv + BF * w.abs()).all()
+        assert C[:, :n].isfinite().all() and (C[:, n:] == 7).all() and (pre[:, n:] == 7).all()
+        # bf16: the same sums rounded once; the workspace of exactly the size asked for
+        Cb = torch.empty(M, n, dtype=torch.bfloat16, device=gpu)
+        nb = fq.fp8q_linear_blockscaled_workspace(int(fast), 0, M, n, K)
+        ws = torch.full((nb // 4 + 64,), 5.0, device=gpu)
+        call(fq, A, fa, sA, B, fb, sB, bias, act, Cb, M, n, K, fast, None if res is None else torch.zeros_like(Cb), ws=ws,
+             ws_bytes=nb)
+        C0 = torch.empty(M, n, device=gpu)
+        call(fq, A, fa, sA, B, fb, sB, bias, act, C0, M, n, K, fast)
+        assert (ws[nb // 4:] == 5).all() and torch.equal(Cb, C0.bfloat16())
+    # codes: what the quantizer makes of the fp32 output
+    bias = W.normal((N,), seed=3, device=gpu)
+    C = torch.empty(M, N, device=gpu)
+    call(fq, A, fa, sA, B, fb, sB, bias, i % 5, C, M, N, K, fast)
+    for fc in (E4, E5):
+        q, s = torch.empty(M, N, dtype=torch.uint8, device=gpu), torch.empty(M, N // 128, device=gpu)
+        wq, wsc = torch.empty_like(q), torch.empty_like(s)
+        fq.fp8q_quantize_1x128(C, M, N, N, fc, EPS, wq, N, wsc, N // 128)
+        call(fq, A, fa, sA, B, fb, sB, bias, i % 5, q, M, N, K, fast, q=(fc, s))
+        assert torch.equal(q, wq) and torch.equal(s, wsc)
+    # a NaN code spoils its row alone, blocks of zeros and NaN scales among it
+    A[M // 2, K - 1] = 0x7F
+    q, s = torch.empty(M, N, dtype=torch.uint8, device=gpu), torch.empty(M, N // 128, device=gpu)
+    wq, wsc = torch.empty_like(q), torch.empty_like(s)
+    C1 = torch.empty_like(C)
+    call(fq, A, fa, sA, B, fb, sB, bias, i % 5, C1, M, N, K, fast)
+    keep = torch.arange(M, device=gpu) != M // 2
+    assert C1[M // 2].isnan().all() and torch.equal(C1[keep], C[keep])
+    fq.fp8q_quantize_1x128(C1, M, N, N, E4, EPS, wq, N, wsc, N // 128)
+    call(fq, A, fa, sA, B, fb, sB, bias, i % 5, q, M, N, K, fast, q=(E4, s))
+    assert torch.equal(q, wq) and torch.equal(s[keep], wsc[keep]) and s[M // 2].isnan().all()
+
+
+def test_linear_extreme_scales_in_tiles(fq, gpu):
+    """Blocks whose scale leaves the quick quotient's range: all zeros, products near fp32's ends."""
+    M, N, K = 200, 18432, 512
+    A, sA, B, sB = operands(gpu, M, N, K, seed=3)
+    sA[1], sA[2], sA[3] = 0.0, 1e-30, 1e30
+    bias = torch.zeros(N, device=gpu)
+    C = torch.empty(M, N, device=gpu)
+    for fast in (False, True):
+        call(fq, A, E4, sA, B, E4, sB, bias, NONE, C, M, N, K, fast)
+        for fc in (E4, E5):
+            q, s = torch.empty(M, N, dtype=torch.uint8, device=gpu), torch.empty(M, N // 128, device=gpu)
+            wq, wsc = torch.empty_like(q), torch.empty_like(s)
+            fq.fp8q_quantize_1x128(C, M, N, N, fc, EPS, wq, N, wsc, N // 128)
+            call(fq, A, E4, sA, B, E4, sB, bias, NONE, q, M, N, K, fast, q=(fc, s))
+            assert torch.equal(q, wq) and torch.equal(s, wsc)
+
+
+def test_linear_far_rows_in_tiles(fq, gpu):
+    """Rows of the output, the residual and the pre-activations 2^27 bytes apart, past 2^32 in all, in the tiled kernel and
+    the join."""
+    for M, N, K in ((65, 9088, 512), (65, 256, 7168)):
+        ld = 1 << 26
+        buf, far = (torch.empty(M * ld, dtype=torch.bfloat16, device=gpu).view(M, ld)[:, :N] for _ in range(2))
+        A, sA, B, sB = operands(gpu, M, N, K, seed=6)
+        res = W.normal((M, N), seed=5, device=gpu, dtype=torch.bfloat16)
+        buf.copy_(res)
+        C, pre = torch.empty_like(res), torch.empty_like(res)
+        call(fq, A, E4, sA, B, E4, sB, None, GELU, C, M, N, K, True, res, pre)
+        call(fq, A, E4, sA, B, E4, sB, None, GELU, buf, M, N, K, True, buf, far)
+        assert torch.equal(buf, C) and torch.equal(far, pre)
+        del buf, far
+
+
 def test_linear_rows_do_not_touch_each_other(fq, gpu):
     """A NaN code spoils its own row alone, in every kernel."""
     for M, K in ((20, 256), (150, 256), (150, 4096), (400, 1024)):
@@ -617,6 +772,26 @@ def test_relu_passes_nothing_of_what_it_masks(fq, gpu):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_linear_bwd_codes_of_extreme_blocks(fq, gpu):
+    """Blocks of zeros, Inf, NaN and magnitudes whose scale leaves the quick quotient's range, along both dimensions: the
+    quantizers' codes, bit for bit; blocks without them too."""
+    M, N = 256, 384
+    for eps in (1e-12, 1e-37):
+        dC = torch.randn(M, N, device=gpu)
+        dC[:, 3], dC[:, 4], dC[:, 5], dC[9], dC[10], dC[11] = 1e30, 1e-34, 0.0, 1e-36, 0.0, 1e32
+        dC[3, 7], dC[200, 140] = float("nan"), float("inf")
+        for fc in (E4, E5):
+            D, Ds = torch.empty(M, N, dtype=torch.uint8, device=gpu), torch.empty(M, N // 128, device=gpu)
+            Dt, Dts = torch.empty(N, M, dtype=torch.uint8, device=gpu), torch.empty(N, M // 128, device=gpu)
+            fq.fp8q_linear_bwd_q(dC, N, None, 0, NONE, fc, eps, D, N, Ds, N // 128, Dt, M, Dts, M // 128, E4, None, 0, None, 0, None,
+                                 M, N)
+            q, s, qt, st = torch.empty_like(D), torch.empty_like(Ds), torch.empty_like(Dt), torch.empty_like(Dts)
+            fq.fp8q_quantize_1x128(dC, M, N, N, fc, eps, q, N, s, N // 128)
+            fq.fp8q_quantize_1x128_t(dC, M, N, N, fc, eps, qt, M, st, M // 128)
+            for a, b in ((D, q), (Dt, qt), (Ds.nan_to_num(7.0), s.nan_to_num(7.0)), (Dts.nan_to_num(7.0), st.nan_to_num(7.0))):
+                assert torch.equal(a, b)
+
+
 def test_linear_bwd_special_gradients(fq, gpu):
     """A NaN gradient marks its blocks and its column's sum alone; an Inf its block's scale."""
     M, N = 256, 256
@@ -633,14 +808,14 @@ def test_linear_bwd_special_gradients(fq, gpu):
 # ------------------------------------------------------------------ streams, graphs, far rows, the operators together
 def test_explicit_streams(fq, gpu):
     """Two streams at once, each with its own workspace from torch's allocator, against one after the other."""
-    M, N, K = 200, 512, 4096
+    M, N, K = 65, 256, 7168
     ops = [operands(gpu, M, N, K, seed=s) for s in (1, 2)]
     bias = W.normal((N,), seed=3, device=gpu)
 
     def run(o, stream):
         A, sA, B, sB = o
         outs = []
-        for m in (5, M):
+        for m in (5, M):  # a few rows; tiles in parts of K
             q, s = torch.empty(m, N, dtype=torch.uint8, device=gpu), torch.empty(m, N // 128, device=gpu)
             call(fq, A, E4, sA, B, E4, sB, bias, GELU, q, m, N, K, q=(E4, s), stream=stream)
             outs += [q, s]
