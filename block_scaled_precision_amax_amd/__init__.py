@@ -445,44 +445,46 @@ def fp8q_gemm_blockscaled_few(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, gb,
 
 
 
+_native = None
 _get_device = None
 
 
-def _place(operands) -> int:
-    """The device of the operands that are tensors (-1: all are raw pointers).  A host tensor's address, or one of another
-    device, would fault in the kernel: both are refused."""
-    dev = -1
-    for t in operands:
-        if t is None or t.__class__ is int:
-            continue
-        d = t.get_device()
-        if d != dev or d < 0:
-            if d < 0:
-                raise ValueError("this operand is not on a GPU")
-            if dev >= 0:
-                raise ValueError(f"these operands share one device, got cuda:{dev} and cuda:{d}")
-            dev = d
-    return dev
-
-
-def _launch(fn, args, dev, stream) -> None:
-    """fn(*args, stream's handle) with `dev` as the current device, on which kernels are launched."""
-    global _get_device, _raw_stream
-    if dev < 0:  # raw pointers alone
-        _check(fn(*args, _stream(stream)))
-        return
-    if _get_device is None:
+def _entries():
+    """The module that marshals the calls below (csrc/fp8q_binding.cpp): pointers, fixed types and devices are read and
+    checked there."""
+    global _native, _get_device, _raw_stream
+    if _native is None:
         import torch
 
+        lib()
+        try:
+            from . import _fp8q_call as m
+        except ImportError as e:
+            raise ImportError(f"{e}: build it with `python -m block_scaled_precision_amax_amd.build`") from e
+        m.types((torch.float32,), (torch.bfloat16, torch.int16, torch.uint16),
+                (torch.uint8, torch.int8, torch.float8_e4m3fn, torch.float8_e5m2))
         _get_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-    handle = _raw_stream(dev) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
-    if _get_device() == dev:
-        rc = fn(*args, handle)
-    else:
-        import torch
+        _native = m
+    return _native
 
-        with torch.cuda.device(dev):
-            rc = fn(*args, handle)
+
+def _launch(fn, stream, t, *args) -> None:
+    """fn(device of t, *args, stream's handle) with that device as the current one, on which kernels are launched.  A host
+    tensor's address, or one of another device, would fault in the kernel: fn refuses both."""
+    if t.__class__ is int:  # a raw pointer: what the tensors say, else the current device
+        t = next((a for a in args if hasattr(a, "get_device")), None)
+    dev = -1 if t is None else t.get_device()
+    if dev < 0:
+        rc = fn(-1, *args, _stream(stream) if t is None else 0)
+    else:
+        handle = _raw_stream(dev) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
+        if _get_device() == dev:
+            rc = fn(dev, *args, handle)
+        else:
+            import torch
+
+            with torch.cuda.device(dev):
+                rc = fn(dev, *args, handle)
     if rc:
         _check(rc)
 
@@ -491,9 +493,8 @@ def fp8q_layernorm_1x128(x, ldx, res, ldr, w, b, rows, cols, norm_eps, z, ldz, y
                          mean=None, rstd=None, stream=None) -> None:
     """w and b, of one dtype, may each be None (ones, zeros)."""
     wdt = F32 if w is None and b is None else _same_dt(b if w is None else w, b)
-    args = (_ptr(x), _same_dt(x, res, z, y), ldx, _ptr(res), ldr, _ptr(w), _ptr(b), wdt, rows, cols, norm_eps, _ptr(z), ldz,
-            _ptr(y), ldy, f, eps, _codes(q), ldq, _f32(scales), ld_s, _f32(mean), _f32(rstd))
-    _launch(lib().fp8q_layernorm_1x128, args, _place((x, res, w, b, z, y, q, scales, mean, rstd)), stream)
+    _launch((_native or _entries()).fp8q_layernorm_1x128, stream, x, x, _same_dt(x, res, z, y), ldx, res, ldr, w, b, wdt, rows,
+            cols, norm_eps, z, ldz, y, ldy, f, eps, q, ldq, scales, ld_s, mean, rstd)
 
 
 def fp8q_layernorm_bwd_workspace(rows, cols) -> int:
@@ -502,56 +503,59 @@ def fp8q_layernorm_bwd_workspace(rows, cols) -> int:
 
 def fp8q_layernorm_bwd(dy, lddy, z, ldz, w, mean, rstd, dres, lddr, rows, cols, dx, lddx, dw=None, db=None, ws=None,
                        ws_bytes=0, stream=None) -> None:
-    args = (_ptr(dy), _same_dt(dy, z, dres, dx), lddy, _ptr(z), ldz, _ptr(w), F32 if w is None else _dt(w), _f32(mean),
-            _f32(rstd), _ptr(dres), lddr, rows, cols, _ptr(dx), lddx, _f32(dw), _f32(db), _ptr(ws), ws_bytes)
-    _launch(lib().fp8q_layernorm_bwd, args, _place((dy, z, w, mean, rstd, dres, dx, dw, db, ws)), stream)
+    _launch((_native or _entries()).fp8q_layernorm_bwd, stream, dy, dy, _same_dt(dy, z, dres, dx), lddy, z, ldz, w,
+            F32 if w is None else _dt(w), mean, rstd, dres, lddr, rows, cols, dx, lddx, dw, db, ws, ws_bytes)
 
 
 def fp8q_linear_blockscaled_workspace(fast, codes, M, N, K) -> int:
     return lib().fp8q_linear_blockscaled_workspace(fast, codes, M, N, K)
 
 
-def _linear(fn, fast, codes, args, sizes, ws, ws_bytes, stream, operands) -> None:
-    """A linear layer's call: args up to its sizes; without `ws`, what it needs comes from torch's allocator."""
-    dev = _place((*operands, ws))
-    if ws is None:
-        # one device's answer for every device of its kind
-        ws_bytes = lib().fp8q_linear_blockscaled_workspace(fast, codes, *sizes)
-        if ws_bytes:
-            t = next((t for t in operands if t is not None and t.__class__ is not int), 0)
-            ws = _workspace(ws_bytes, _stream(stream, t), stream, t)
-    _launch(fn, (*args, *sizes, _ptr(ws), ws_bytes), dev, stream)
+def _linear_workspace(fast, codes, M, N, K, stream, t):
+    """What a call needs, from torch's allocator."""
+    n = (_lib or lib()).fp8q_linear_blockscaled_workspace(fast, codes, M, N, K)
+    if not n:
+        return None, 0
+    if t.__class__ is not int and t.get_device() < 0:
+        return 0, n  # a host tensor: the call refuses it
+    return _workspace(n, _stream(stream, t), stream, t), n
 
 
 def fp8q_linear_blockscaled(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, sB_sn, sB_skb, bias, act, res, ldr, C, ldc, pre,
                             ldpre, M, N, K, ws=None, ws_bytes=0, stream=None) -> None:
     """Without `ws`, the workspace of a call of few tiles comes from torch's allocator; so in the forms below."""
-    args = (_codes(A), fa, lda, _f32(sA), sA_sm, sA_skb, _codes(B), fb, ldb, _f32(sB), sB_sn, sB_skb, _ptr(bias),
-            F32 if bias is None else _dt(bias), act, _ptr(res), ldr, _ptr(C), _same_dt(C, res), ldc, _bf16(pre), ldpre)
-    _linear(lib().fp8q_linear_blockscaled, 0, 0, args, (M, N, K), ws, ws_bytes, stream, (A, sA, B, sB, bias, res, C, pre))
+    if ws is None:
+        ws, ws_bytes = _linear_workspace(0, 0, M, N, K, stream, A)
+    _launch((_native or _entries()).fp8q_linear_blockscaled, stream, A, A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, sB_sn,
+            sB_skb, bias, F32 if bias is None else _dt(bias), act, res, ldr, C, _same_dt(C, res), ldc, pre, ldpre, M, N, K, ws,
+            ws_bytes)
 
 
 def fp8q_linear_blockscaled_fast(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, sB_sn, sB_skb, bias, act, res, ldr, C, ldc,
                                  pre, ldpre, M, N, K, ws=None, ws_bytes=0, stream=None) -> None:
-    args = (_codes(A), fa, lda, _f32(sA), sA_sm, sA_skb, _codes(B), fb, ldb, _f32(sB), sB_sn, sB_skb, _ptr(bias),
-            F32 if bias is None else _dt(bias), act, _ptr(res), ldr, _ptr(C), _same_dt(C, res), ldc, _bf16(pre), ldpre)
-    _linear(lib().fp8q_linear_blockscaled_fast, 1, 0, args, (M, N, K), ws, ws_bytes, stream,
-            (A, sA, B, sB, bias, res, C, pre))
+    if ws is None:
+        ws, ws_bytes = _linear_workspace(1, 0, M, N, K, stream, A)
+    _launch((_native or _entries()).fp8q_linear_blockscaled_fast, stream, A, A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB,
+            sB_sn, sB_skb, bias, F32 if bias is None else _dt(bias), act, res, ldr, C, _same_dt(C, res), ldc, pre, ldpre, M, N,
+            K, ws, ws_bytes)
 
 
 def fp8q_linear_blockscaled_q(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, sB_sn, sB_skb, bias, act, fc, eps, Cq, ldcq, Cs,
                               ld_cs, pre, ldpre, M, N, K, ws=None, ws_bytes=0, stream=None) -> None:
-    args = (_codes(A), fa, lda, _f32(sA), sA_sm, sA_skb, _codes(B), fb, ldb, _f32(sB), sB_sn, sB_skb, _ptr(bias),
-            F32 if bias is None else _dt(bias), act, fc, eps, _codes(Cq), ldcq, _f32(Cs), ld_cs, _bf16(pre), ldpre)
-    _linear(lib().fp8q_linear_blockscaled_q, 0, 1, args, (M, N, K), ws, ws_bytes, stream, (A, sA, B, sB, bias, Cq, Cs, pre))
+    if ws is None:
+        ws, ws_bytes = _linear_workspace(0, 1, M, N, K, stream, A)
+    _launch((_native or _entries()).fp8q_linear_blockscaled_q, stream, A, A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, sB_sn,
+            sB_skb, bias, F32 if bias is None else _dt(bias), act, fc, eps, Cq, ldcq, Cs, ld_cs, pre, ldpre, M, N, K, ws,
+            ws_bytes)
 
 
 def fp8q_linear_blockscaled_q_fast(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, sB_sn, sB_skb, bias, act, fc, eps, Cq,
                                    ldcq, Cs, ld_cs, pre, ldpre, M, N, K, ws=None, ws_bytes=0, stream=None) -> None:
-    args = (_codes(A), fa, lda, _f32(sA), sA_sm, sA_skb, _codes(B), fb, ldb, _f32(sB), sB_sn, sB_skb, _ptr(bias),
-            F32 if bias is None else _dt(bias), act, fc, eps, _codes(Cq), ldcq, _f32(Cs), ld_cs, _bf16(pre), ldpre)
-    _linear(lib().fp8q_linear_blockscaled_q_fast, 1, 1, args, (M, N, K), ws, ws_bytes, stream,
-            (A, sA, B, sB, bias, Cq, Cs, pre))
+    if ws is None:
+        ws, ws_bytes = _linear_workspace(1, 1, M, N, K, stream, A)
+    _launch((_native or _entries()).fp8q_linear_blockscaled_q_fast, stream, A, A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB,
+            sB_sn, sB_skb, bias, F32 if bias is None else _dt(bias), act, fc, eps, Cq, ldcq, Cs, ld_cs, pre, ldpre, M, N, K, ws,
+            ws_bytes)
 
 
 def fp8q_linear_bwd_q_workspace(M, N) -> int:
@@ -560,6 +564,5 @@ def fp8q_linear_bwd_q_workspace(M, N) -> int:
 
 def fp8q_linear_bwd_q(dC, lddc, pre, ldpre, act, fc, eps, Dq, lddq, Ds, ld_ds, Dt, lddt, Dst, ld_dst, fh, Ht, ldht, Hst,
                       ld_hst, dbias, M, N, ws=None, ws_bytes=0, stream=None) -> None:
-    args = (_ptr(dC), _dt(dC), lddc, _bf16(pre), ldpre, act, fc, eps, _codes(Dq), lddq, _f32(Ds), ld_ds, _codes(Dt), lddt,
-            _f32(Dst), ld_dst, fh, _codes(Ht), ldht, _f32(Hst), ld_hst, _f32(dbias), M, N, _ptr(ws), ws_bytes)
-    _launch(lib().fp8q_linear_bwd_q, args, _place((dC, pre, Dq, Ds, Dt, Dst, Ht, Hst, dbias, ws)), stream)
+    _launch((_native or _entries()).fp8q_linear_bwd_q, stream, dC, dC, _dt(dC), lddc, pre, ldpre, act, fc, eps, Dq, lddq, Ds,
+            ld_ds, Dt, lddt, Dst, ld_dst, fh, Ht, ldht, Hst, ld_hst, dbias, M, N, ws, ws_bytes)

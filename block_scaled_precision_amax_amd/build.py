@@ -1,6 +1,8 @@
 """Builds libfp8q.so (the HIP kernels and the C ABI) for gfx950 with hipcc,
-and libfp8q_stream.so, the streaming-bandwidth reference the benchmark sets
-the quantizers against (not part of the library's ABI).
+libfp8q_stream.so, the streaming-bandwidth reference the benchmark sets
+the quantizers against (not part of the library's ABI), and, with the host
+compiler, _fp8q_call.so, the Python binding's marshalling of the calls whose
+latency counts.
 
 Each csrc/*.hip is compiled to an object in parallel, then linked into the
 package directory, where the Python binding loads it.  Flags:
@@ -14,12 +16,14 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(os.path.dirname(HERE), "_build")
 LIB = os.path.join(HERE, "libfp8q.so")
 STREAM_LIB = os.path.join(HERE, "libfp8q_stream.so")
+CALL_LIB = os.path.join(HERE, "_fp8q_call.so")
 ARCH = os.environ.get("FP8Q_ARCH", "gfx950")
 
 SOURCES = ["fp8q_api.hip", "fp8q_quant.hip", "fp8q_gemm.hip", "fp8q_norm.hip", "fp8q_few.hip",
@@ -64,9 +68,24 @@ def _link(objs: list[str], lib: str) -> None:
     os.replace(tmp, lib)
 
 
+def _binding() -> None:
+    """The host-side module, linked against the library beside it."""
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("no host C++ compiler found (set CXX)")
+    tmp = CALL_LIB + ".tmp"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+           "-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "fp8q_binding.cpp"), "-L" + HERE,
+           "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"host compiler failed for fp8q_binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALL_LIB)
+
+
 def build(extra: list[str] | None = None, save_temps: bool = False) -> str:
-    """Compile every HIP source and link libfp8q.so and libfp8q_stream.so.
-    Always recompiles."""
+    """Compile every HIP source and link libfp8q.so and libfp8q_stream.so, then
+    the binding's module.  Always recompiles."""
     os.makedirs(BUILD, exist_ok=True)
     extra = list(extra or [])
     if save_temps:
@@ -76,6 +95,7 @@ def build(extra: list[str] | None = None, save_temps: bool = False) -> str:
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
     _link(objs[:len(SOURCES)], LIB)
     _link(objs[len(SOURCES):], STREAM_LIB)
+    _binding()
     return LIB
 
 
