@@ -9,6 +9,20 @@
 // with the epilogue behind their last block, where the tiles that do not fill a
 // round of the compute units may have K cut into parts: their sums go to a
 // workspace and a second kernel joins them, with the same epilogue.
+//
+// What bounds it, measured:
+//   1 x 18432 x 7168, GELU, codes: HBM, 132 MB of weight in 23 us of k_few, 4.6
+//     for the epilogue's launch;
+//   48 x 7168 x 18432 with residual, exact: 30.5 us in 9 parts of K (the weight at
+//     4.4 TB/s and 12 MB of sums out), 7.5 to join them;
+//   1023 x 9000 x 4096, GELU, exact fp32: 96 us + 7.4: 1.57 us a block of K (1.45 at
+//     the rate of a large bf16 product), but 32 of the 288 tiles are left after a
+//     round, and neither round's epilogue has anything beside it;
+//   16384 x 18432 x 7168, erf GELU, codes and pre-activations, exact: 3900 us
+//     (to 4040), 1110 TFLOP/s: the decode takes the vector ALU's slots, and after some
+//     milliseconds the clock falls (2.0 us a block of K);
+//   8192 x 7168 x 18432 with residual, FP8-MFMA: 955 us + 28 to join the last
+//     128 tiles, 2240 TFLOP/s, LDS and matrix issue, clock.
 #include "fp8q_tiles.h"
 
 namespace fp8q {
@@ -48,15 +62,19 @@ __device__ __forceinline__ void store_edge8(void* p, int64_t i, const float (&v)
 }
 
 // The residual of U rows' columns col .. col + 7, where whole pieces can be
-// loaded; asked for before the sums are at hand, so that it comes beside them
-// (8192 x 8192 x 2048 FP8-MFMA with GELU and pre-activations: 217 us, loaded
-// where it is added 221).
+// loaded.  A bf16 one is asked for before the sums are read back, so that it
+// comes beside them (8192 x 8192 x 2048 FP8-MFMA with GELU and pre-activations:
+// 198 us, loaded where it is added 204; 1024 x 8192 x 4096 exact 66.7 against 68).
+// An fp32 one holds twice the registers and is loaded where it is added: early, a
+// large product gains 2 % and one of a few rounds, with or without it, loses 1 to 2.
 template <int OUT>
 using Res8 = Raw8<OUT == FP8Q_F32 ? FP8Q_F32 : FP8Q_BF16>;
+template <int OUT>
+constexpr bool kEarly = OUT == FP8Q_BF16;
 template <int OUT, int U>
 __device__ __forceinline__ void load_res8(const Epilogue& e, const int64_t (&row)[U], const bool (&in)[U], int64_t col,
                                           int64_t N, Res8<OUT> (&r)[U]) {
-  if (OUT >= 2 || !e.res || !e.vr || N - col < 8) return;
+  if (!e.res || !e.vr || N - col < 8) return;
 #pragma unroll
   for (int u = 0; u < U; ++u)
     if (in[u]) r[u].load(e.res, row[u] * e.ldr + col);
@@ -69,7 +87,7 @@ __device__ __forceinline__ void load_res8(const Epilogue& e, const int64_t (&row
 // maximum, quotient) fills the other's waits.
 template <int OUT, int ACT, int U>
 __device__ __forceinline__ void finish8(const Proj& p, const Epilogue& e, const int64_t (&row)[U], const bool (&in)[U],
-                                        int64_t col, float (&v)[U][8], const float (&b)[8], const Res8<OUT> (&res)[U]) {
+                                        int64_t col, float (&v)[U][8], const float (&b)[8], Res8<OUT> (&res)[U]) {
   const int64_t left = p.N - col;
 #pragma unroll
   for (int u = 0; u < U; ++u)
@@ -87,6 +105,7 @@ __device__ __forceinline__ void finish8(const Proj& p, const Epilogue& e, const 
   if constexpr (OUT < 2) {
     if (e.res) {
       if (e.vr && left >= 8) {
+        if constexpr (!kEarly<OUT>) load_res8<OUT>(e, row, in, col, p.N, res);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -137,7 +156,7 @@ __device__ __forceinline__ void finish8(const Proj& p, const Epilogue& e, const 
 // One row, any activation.
 template <int OUT>
 __device__ __forceinline__ void finish8(const Proj& p, const Epilogue& e, int64_t row, int64_t col, float (&v)[1][8],
-                                        const float (&b)[8], const Res8<OUT> (&res)[1]) {
+                                        const float (&b)[8], Res8<OUT> (&res)[1]) {
   const int64_t rows[1] = {row};
   const bool in[1] = {true};
   with_linear_act(e.act, [&](auto act) { finish8<OUT, decltype(act)::value, 1>(p, e, rows, in, col, v, b, res); });
@@ -220,7 +239,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_linear(const Proj p, const floa
             Res8<OUT> res[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) row[u] = m0 + (it + u) * 32 + (tid >> 4), in[u] = row[u] < M;
-            load_res8<OUT>(ep, row, in, col, N, res);
+            if constexpr (kEarly<OUT>) load_res8<OUT>(ep, row, in, col, N, res);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
               const int r = (it + u) * 32 + (tid >> 4);
@@ -268,7 +287,7 @@ __global__ __launch_bounds__(256) void k_linear_join(const Proj p, const Epilogu
   const int64_t rows[1] = {row};
   const bool in[1] = {true};
   Res8<OUT> res[1];
-  load_res8<OUT>(ep, rows, in, col, p.N, res);
+  if constexpr (kEarly<OUT>) load_res8<OUT>(ep, rows, in, col, p.N, res);
   float v[1][8] = {{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]}};
   finish8<OUT>(p, ep, row, col, v, b, res);
 }
@@ -286,7 +305,8 @@ __global__ __launch_bounds__(256) void k_linear_finish(const Proj p, const Epilo
   x.load(p.ws, row * p.N + col);
 #pragma unroll
   for (int k = 0; k < 8; ++k) v[0][k] = x[k];
-  finish8<OUT>(p, ep, row, col, v, b, {});
+  Res8<OUT> none[1];
+  finish8<OUT>(p, ep, row, col, v, b, none);
 }
 
 // How a call goes, and its cost in nanoseconds.  Measured, the codes of either

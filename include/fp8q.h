@@ -508,7 +508,7 @@ int fp8q_layernorm_1x128(const void* x, fp8q_dtype dt, int64_t ldx, const void* 
                          int64_t ld_s, float* mean, float* rstd, void* stream);
 
 /* Bytes of workspace fp8q_layernorm_bwd needs for the gradients of weight and
- * bias (at most 4096 bytes per column; 0 for sizes it refuses). */
+ * bias (at most 2048 bytes per column; 0 for sizes it refuses). */
 int64_t fp8q_layernorm_bwd_workspace(int64_t rows, int64_t cols);
 
 /* Gradients of fp8q_layernorm_1x128 (the quantization passed straight
