@@ -830,6 +830,41 @@ def test_explicit_streams(fq, gpu):
         assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))
 
 
+def test_calls_from_several_threads(fq, gpu):
+    """Calls release the interpreter's lock: four threads, each on a stream of its own, with refused calls in between,
+    against one after the other; a refusal's text is its thread's."""
+    from concurrent.futures import ThreadPoolExecutor
+
+    M, N, K = 65, 256, 2048
+    ops = [operands(gpu, M, N, K, seed=s) for s in range(4)]
+    bias = W.normal((N,), seed=3, device=gpu)
+
+    def run(i, stream):
+        A, sA, B, sB = ops[i]
+        q, s = torch.empty(M, N, dtype=torch.uint8, device=gpu), torch.empty(M, N // 128, device=gpu)
+        call(fq, A, E4, sA, B, E4, sB, bias, GELU, q, M, N, K, q=(E4, s), stream=stream)
+        return q, s
+
+    want = [run(i, None) for i in range(4)]
+    torch.cuda.synchronize()
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        got = []
+        for k in range(20):
+            got.append(run(i, stream))
+            cols = 8 * (1000 + i) + 1
+            with pytest.raises(fq.Fp8qError, match=str(cols)):
+                fq.fp8q_layernorm_1x128(bias, N, None, 0, None, None, 1, cols, 1e-5, None, 0, bias, cols, 0, 1e-12, None, 0, None,
+                                        0, stream=stream)
+        stream.synchronize()
+        return got
+
+    with ThreadPoolExecutor(4) as ex:
+        for got, w in zip(ex.map(work, range(4)), want):
+            assert all(torch.equal(a, b) for g in got for a, b in zip(g, w))
+
+
 def example():
     import importlib.util
     import os
