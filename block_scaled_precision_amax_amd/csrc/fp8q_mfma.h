@@ -104,7 +104,9 @@ __device__ __forceinline__ float activation(float g) {
 //
 // Where an activation passes nothing on (ReLU's negative side) its gradient is
 // 0 whatever arrives, Inf and NaN included; NaN pre-activations stay NaN.
-// linear_act gives act(g); linear_act_bwd dc * act'(g), and h = act(g).
+// linear_act gives act(g); linear_act_bwd dc * act'(g), and h = act(g).  The
+// derivative's second term, g p', is 0 at both ends but Inf * 0 if formed from an
+// infinite g, so it is formed from g clamped to where p has long been 0 or 1.
 __device__ __forceinline__ float normal_cdf(float g, float& e) {
   const float a = __builtin_fabsf(g), t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3f, a, 1.0f));
   e = __builtin_amdgcn_exp2f(g * g * -0.72134752044448170f);
@@ -142,17 +144,17 @@ __device__ __forceinline__ float linear_act_bwd(float dc, float g, float& h) {
     h = g * p;
     return dc * (d == 0.0f ? p : __builtin_fmaf(g, d, p));  // g may be Inf where the density is 0
   } else if constexpr (ACT == FP8Q_ACT_SILU) {
-    const float p = sigmoid(g);
+    const float p = sigmoid(g);  // NaN where g is, whatever the clamp gives there
     h = g * p;
-    return dc * __builtin_fmaf(h, 1.0f - p, p);
+    return dc * __builtin_fmaf(__builtin_amdgcn_fmed3f(g, -128.0f, 128.0f) * p, 1.0f - p, p);
   } else {
-    // p = sigmoid(2 k), k = c (g + a g^3): p' = p (1 - p) 2 c (1 + 3 a g^2).  Beyond 16 p is 0 or 1, and the clamp
-    // keeps the square finite
+    // p = sigmoid(2 k), k = c (g + a g^3): p' = p (1 - p) 2 c (1 + 3 a g^2).  Beyond 16 p is 0 or 1; the clamp
+    // keeps a NaN
     constexpr float c2 = 2.0f * 0.7978845608028654f, a = 0.044715f, l = -1.4426950408889634f;
-    const float x = __builtin_amdgcn_fmed3f(g, -16.0f, 16.0f), x2 = x * x;
+    const float x = __builtin_elementwise_minimum(__builtin_elementwise_maximum(g, -16.0f), 16.0f), x2 = x * x;
     const float p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * __builtin_fmaf(x2, l * c2 * a, l * c2)));
     h = g * p;
-    return dc * __builtin_fmaf(h * (1.0f - p), __builtin_fmaf(x2, 3.0f * a * c2, c2), p);
+    return dc * __builtin_fmaf(x * p * (1.0f - p), __builtin_fmaf(x2, 3.0f * a * c2, c2), p);
   }
 }
 // f with the activation as a constant: the choice is made once around a
