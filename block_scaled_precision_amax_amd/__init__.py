@@ -444,7 +444,6 @@ def fp8q_gemm_blockscaled_few(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, gb,
                                            sB_sn, sB_skb, _ptr(C), _dt(C), ldc, M, N, K, _stream(stream, A)))
 
 
-
 _native = None
 _get_device = None
 
@@ -468,23 +467,27 @@ def _entries():
     return _native
 
 
-def _launch(fn, stream, t, *args) -> None:
+def _launch(fn, stream, t, *args, plan=None) -> None:
     """fn(device of t, *args, stream's handle) with that device as the current one, on which kernels are launched.  A host
-    tensor's address, or one of another device, would fault in the kernel: fn refuses both."""
-    if t.__class__ is int:  # a raw pointer: what the tensors say, else the current device
+    tensor's address, or one of another device, would fault in the kernel: fn refuses both.  With `plan`, the linear
+    layer's (fast, codes, M, N, K), the workspace that the call needs on that device follows the arguments."""
+    if t.__class__ is int or t is None:  # a raw pointer: what the tensors say, else the current device
         t = next((a for a in args if hasattr(a, "get_device")), None)
     dev = -1 if t is None else t.get_device()
-    if dev < 0:
-        rc = fn(-1, *args, _stream(stream) if t is None else 0)
-    else:
-        handle = _raw_stream(dev) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
-        if _get_device() == dev:
-            rc = fn(dev, *args, handle)
-        else:
-            import torch
+    if dev >= 0 and _get_device() != dev:
+        import torch
 
-            with torch.cuda.device(dev):
-                rc = fn(dev, *args, handle)
+        with torch.cuda.device(dev):
+            return _launch(fn, stream, t, *args, plan=plan)
+    if dev >= 0:
+        handle = _raw_stream(dev) if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
+    else:
+        handle = _stream(stream) if t is None else 0
+    if plan is not None:
+        n = (_lib or lib()).fp8q_linear_blockscaled_workspace(*plan)
+        # none for a host tensor, which fn refuses
+        args += (_workspace(n, handle, stream, 0 if t is None else t) if n and (dev >= 0 or t is None) else None, n)
+    rc = fn(dev, *args, handle)
     if rc:
         _check(rc)
 
@@ -511,51 +514,40 @@ def fp8q_linear_blockscaled_workspace(fast, codes, M, N, K) -> int:
     return lib().fp8q_linear_blockscaled_workspace(fast, codes, M, N, K)
 
 
-def _linear_workspace(fast, codes, M, N, K, stream, t):
-    """What a call needs, from torch's allocator."""
-    n = (_lib or lib()).fp8q_linear_blockscaled_workspace(fast, codes, M, N, K)
-    if not n:
-        return None, 0
-    if t.__class__ is not int and t.get_device() < 0:
-        return 0, n  # a host tensor: the call refuses it
-    return _workspace(n, _stream(stream, t), stream, t), n
+def _linear(fn, stream, A, plan, ws, ws_bytes, *args) -> None:
+    if ws is None:
+        _launch(fn, stream, A, *args, plan=plan)
+    else:
+        _launch(fn, stream, A, *args, ws, ws_bytes)
 
 
 def fp8q_linear_blockscaled(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, sB_sn, sB_skb, bias, act, res, ldr, C, ldc, pre,
                             ldpre, M, N, K, ws=None, ws_bytes=0, stream=None) -> None:
-    """Without `ws`, the workspace of a call of few tiles comes from torch's allocator; so in the forms below."""
-    if ws is None:
-        ws, ws_bytes = _linear_workspace(0, 0, M, N, K, stream, A)
-    _launch((_native or _entries()).fp8q_linear_blockscaled, stream, A, A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, sB_sn,
-            sB_skb, bias, F32 if bias is None else _dt(bias), act, res, ldr, C, _same_dt(C, res), ldc, pre, ldpre, M, N, K, ws,
-            ws_bytes)
+    """Without `ws`, what workspace the call needs comes from torch's allocator; so in the forms below."""
+    _linear((_native or _entries()).fp8q_linear_blockscaled, stream, A, (0, 0, M, N, K), ws, ws_bytes, A, fa, lda, sA, sA_sm,
+            sA_skb, B, fb, ldb, sB, sB_sn, sB_skb, bias, F32 if bias is None else _dt(bias), act, res, ldr, C, _same_dt(C, res),
+            ldc, pre, ldpre, M, N, K)
 
 
 def fp8q_linear_blockscaled_fast(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, sB_sn, sB_skb, bias, act, res, ldr, C, ldc,
                                  pre, ldpre, M, N, K, ws=None, ws_bytes=0, stream=None) -> None:
-    if ws is None:
-        ws, ws_bytes = _linear_workspace(1, 0, M, N, K, stream, A)
-    _launch((_native or _entries()).fp8q_linear_blockscaled_fast, stream, A, A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB,
-            sB_sn, sB_skb, bias, F32 if bias is None else _dt(bias), act, res, ldr, C, _same_dt(C, res), ldc, pre, ldpre, M, N,
-            K, ws, ws_bytes)
+    _linear((_native or _entries()).fp8q_linear_blockscaled_fast, stream, A, (1, 0, M, N, K), ws, ws_bytes, A, fa, lda, sA,
+            sA_sm, sA_skb, B, fb, ldb, sB, sB_sn, sB_skb, bias, F32 if bias is None else _dt(bias), act, res, ldr, C,
+            _same_dt(C, res), ldc, pre, ldpre, M, N, K)
 
 
 def fp8q_linear_blockscaled_q(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, sB_sn, sB_skb, bias, act, fc, eps, Cq, ldcq, Cs,
                               ld_cs, pre, ldpre, M, N, K, ws=None, ws_bytes=0, stream=None) -> None:
-    if ws is None:
-        ws, ws_bytes = _linear_workspace(0, 1, M, N, K, stream, A)
-    _launch((_native or _entries()).fp8q_linear_blockscaled_q, stream, A, A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, sB_sn,
-            sB_skb, bias, F32 if bias is None else _dt(bias), act, fc, eps, Cq, ldcq, Cs, ld_cs, pre, ldpre, M, N, K, ws,
-            ws_bytes)
+    _linear((_native or _entries()).fp8q_linear_blockscaled_q, stream, A, (0, 1, M, N, K), ws, ws_bytes, A, fa, lda, sA, sA_sm,
+            sA_skb, B, fb, ldb, sB, sB_sn, sB_skb, bias, F32 if bias is None else _dt(bias), act, fc, eps, Cq, ldcq, Cs, ld_cs,
+            pre, ldpre, M, N, K)
 
 
 def fp8q_linear_blockscaled_q_fast(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, sB_sn, sB_skb, bias, act, fc, eps, Cq,
                                    ldcq, Cs, ld_cs, pre, ldpre, M, N, K, ws=None, ws_bytes=0, stream=None) -> None:
-    if ws is None:
-        ws, ws_bytes = _linear_workspace(1, 1, M, N, K, stream, A)
-    _launch((_native or _entries()).fp8q_linear_blockscaled_q_fast, stream, A, A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB,
-            sB_sn, sB_skb, bias, F32 if bias is None else _dt(bias), act, fc, eps, Cq, ldcq, Cs, ld_cs, pre, ldpre, M, N, K, ws,
-            ws_bytes)
+    _linear((_native or _entries()).fp8q_linear_blockscaled_q_fast, stream, A, (1, 1, M, N, K), ws, ws_bytes, A, fa, lda, sA,
+            sA_sm, sA_skb, B, fb, ldb, sB, sB_sn, sB_skb, bias, F32 if bias is None else _dt(bias), act, fc, eps, Cq, ldcq, Cs,
+            ld_cs, pre, ldpre, M, N, K)
 
 
 def fp8q_linear_bwd_q_workspace(M, N) -> int:

@@ -1,0 +1,91 @@
+"""The binding of the layer norm and the linear layer without a GPU: what it asks of the library and of torch, on which
+device and stream, with both replaced by recorders."""
+import contextlib
+import types
+
+import pytest
+import torch
+
+
+class Operand:
+    """A tensor of the second device, as far as the binding looks."""
+
+    dtype, device = torch.bfloat16, torch.device("cuda", 1)
+
+    def get_device(self):
+        return 1
+
+
+@pytest.fixture
+def two_devices(fq, monkeypatch):
+    """Device 0 current, operands on device 1; the library answers 256 bytes of workspace on device 0 and 512 on device 1."""
+    r = types.SimpleNamespace(current=0, asked=[], given=[], called=[])
+
+    @contextlib.contextmanager
+    def device(d):
+        before, r.current = r.current, d
+        try:
+            yield
+        finally:
+            r.current = before
+
+    def ask(fast, codes, M, N, K):
+        r.asked.append((r.current, fast, codes, M, N, K))
+        return 256 << r.current
+
+    def entry(name):
+        def f(dev, *args):
+            r.called.append((r.current, name, dev, args))
+            return 0
+        return f
+
+    def workspace(n, handle, stream, t):
+        r.given.append((n, handle, r.current if isinstance(t, int) else t.get_device()))
+        return "workspace of %d" % n
+
+    names = ("fp8q_linear_blockscaled", "fp8q_linear_blockscaled_fast", "fp8q_linear_blockscaled_q",
+             "fp8q_linear_blockscaled_q_fast")
+    fq.lib()
+    monkeypatch.setattr(fq, "_lib", types.SimpleNamespace(fp8q_linear_blockscaled_workspace=ask))
+    monkeypatch.setattr(fq, "_native", types.SimpleNamespace(**{n: entry(n) for n in names}))
+    monkeypatch.setattr(fq, "_get_device", lambda: r.current)
+    monkeypatch.setattr(fq, "_raw_stream", lambda d: 1000 + d)
+    monkeypatch.setattr(fq, "_workspace", workspace)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: types.SimpleNamespace(cuda_stream=1000 + r.current))
+    return r
+
+
+def forms(fq, A, t, **kw):
+    """Every form of the linear layer: its name, whether it is the FP8-MFMA one and leaves codes, and a call of it."""
+    a = (A, 0, 128, t, 1, 1, t, 0, 128, t, 1, 1, None, fq.ACT_NONE)
+    for name in ("fp8q_linear_blockscaled", "fp8q_linear_blockscaled_fast"):
+        yield name, int(name.endswith("fast")), 0, lambda f=getattr(fq, name): f(*a, None, 0, t, 8, None, 0, 3, 8, 128, **kw)
+    for name in ("fp8q_linear_blockscaled_q", "fp8q_linear_blockscaled_q_fast"):
+        yield name, int(name.endswith("fast")), 1, lambda f=getattr(fq, name): f(*a, 0, 1e-12, t, 128, t, 1, None, 0, 3, 128, 128,
+                                                                                **kw)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("stream", [None, 77])
+def test_the_workspace_is_asked_for_and_taken_where_the_operands_lie(fq, two_devices, raw, stream):
+    """A's own device, or with a raw pointer for A that of the first operand that is a tensor."""
+    t = Operand()
+    for name, fast, codes, call in forms(fq, 0x10000 if raw else t, t, stream=stream):
+        call()
+        N = 128 if codes else 8
+        handle = stream or 1001
+        assert two_devices.asked.pop() == (1, fast, codes, 3, N, 128)
+        assert two_devices.given.pop() == (512, handle, 1)
+        current, called, dev, args = two_devices.called.pop()
+        assert (current, called, dev) == (1, name, 1) and args[-3:] == ("workspace of 512", 512, handle)
+        assert not (two_devices.asked or two_devices.given or two_devices.called) and two_devices.current == 0
+
+
+def test_a_workspace_that_is_given_is_not_asked_for(fq, two_devices):
+    t = Operand()
+    for name, _, _, call in forms(fq, t, t, ws=t, ws_bytes=99):
+        call()
+        current, called, dev, args = two_devices.called.pop()
+        assert (current, called, dev) == (1, name, 1) and args[-3:] == (t, 99, 1001)
+        assert not (two_devices.asked or two_devices.given)
