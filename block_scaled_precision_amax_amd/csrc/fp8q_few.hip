@@ -45,9 +45,12 @@ static constexpr int kScaleBlocks = 160;
 
 // Eight wavefronts share the K blocks of a group of columns: 16 of g and the
 // same 16 of u (GLU, NJ = 2), or 16 NJ columns.  RT tiles of 16 rows.  OUT:
-// FP8Q_F32 or FP8Q_BF16.
-template <int FA, int FB, int GB, bool GLU, int OUT, int NJ, int RT>
-__global__ __launch_bounds__(64 * kWaves) void k_few(const Proj p, const Epilogue ep) {
+// FP8Q_F32 or FP8Q_BF16.  E: Epilogue for a linear layer, else Nothing (a plain
+// product that asks at run time for the parts of an epilogue takes 22.13 us
+// instead of 22.02 at one row of 7168 x 18432, 36.56 instead of 36.43 at 48).
+struct Nothing {};
+template <int FA, int FB, int GB, bool GLU, int OUT, int NJ, int RT, typename E>
+__global__ __launch_bounds__(64 * kWaves) void k_few(const Proj p, const E ep) {
   constexpr bool H16 = FA == FP8Q_E5M2 || FB == FP8Q_E5M2;
   constexpr int NS = GB == FP8Q_GRAN_1x128 ? 4 : 1;  // B scales of a lane's four columns
   using V8 = typename Op<H16>::v8;
@@ -210,8 +213,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_few(const Proj p, const Epilogu
     });
   }
   using T = std::conditional_t<OUT == FP8Q_F32, float, uint16_t>;
-  if constexpr (!GLU) {
-    // a linear layer's epilogue; four columns a lane, whatever their alignment
+  if constexpr (std::is_same_v<E, Epilogue>) {
+    // four columns a lane, whatever their alignment
     if (ep.bias) {
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
@@ -249,16 +252,16 @@ __global__ __launch_bounds__(64 * kWaves) void k_few(const Proj p, const Epilogu
     if (col + 16 * j < p.N) store_row4((T*)p.out + row * p.ldo + col + 16 * j, o[j], p.N - col - 16 * j, vec);
 }
 
-template <int FA, int FB, int GB, bool GLU, int OUT, int NJ, int RT>
-static void launch_rt(const Proj& p, const Epilogue& e, hipStream_t st) {
+template <int FA, int FB, int GB, bool GLU, int OUT, int NJ, int RT, typename E>
+static void launch_rt(const Proj& p, const E& e, hipStream_t st) {
   constexpr int COLS = GLU ? 16 : 16 * NJ, ROWS = 16 * RT;
-  hipLaunchKernelGGL((k_few<FA, FB, GB, GLU, OUT, NJ, RT>),
+  hipLaunchKernelGGL((k_few<FA, FB, GB, GLU, OUT, NJ, RT, E>),
                      dim3((unsigned)((p.N + COLS - 1) / COLS), (unsigned)((p.M + ROWS - 1) / ROWS)), dim3(64 * kWaves), 0,
                      st, p, e);
 }
 
-template <int FA, int FB, int GB, bool GLU, int OUT>
-static void launch_m(const Proj& p, const Epilogue& e, hipStream_t st) {
+template <int FA, int FB, int GB, bool GLU, int OUT, typename E>
+static void launch_m(const Proj& p, const E& e, hipStream_t st) {
   // a plain product of more than 16 rows shares each tile of A among 32
   // columns; beyond 64 rows, equal groups of up to 64 each read the weight
   const int64_t groups = (p.M + 63) / 64, rows = (p.M + groups - 1) / groups;
@@ -268,26 +271,22 @@ static void launch_m(const Proj& p, const Epilogue& e, hipStream_t st) {
   else launch_rt<FA, FB, GB, GLU, OUT, 2, 4>(p, e, st);
 }
 
-template <int FA, int FB>
-static void launch_f(const Proj& p, const Epilogue& e, hipStream_t st) {
-  constexpr int BLK = FP8Q_GRAN_128x128;
-  const bool f32 = p.out_dt == FP8Q_F32;
-  if (p.B1) {
-    if (f32) launch_m<FA, FB, BLK, true, FP8Q_F32>(p, e, st);
-    else launch_m<FA, FB, BLK, true, FP8Q_BF16>(p, e, st);
-  } else if (p.gb == FP8Q_GRAN_1x128) {
-    if (f32) launch_m<FA, FB, FP8Q_GRAN_1x128, false, FP8Q_F32>(p, e, st);
-    else launch_m<FA, FB, FP8Q_GRAN_1x128, false, FP8Q_BF16>(p, e, st);
-  } else {
-    if (f32) launch_m<FA, FB, BLK, false, FP8Q_F32>(p, e, st);
-    else launch_m<FA, FB, BLK, false, FP8Q_BF16>(p, e, st);
-  }
+template <int FA, int FB, int GB, bool GLU, typename E>
+static void launch_out(const Proj& p, const E& e, hipStream_t st) {
+  if (p.out_dt == FP8Q_F32) launch_m<FA, FB, GB, GLU, FP8Q_F32>(p, e, st);
+  else launch_m<FA, FB, GB, GLU, FP8Q_BF16>(p, e, st);
 }
 
-int launch_few(const Proj& p, const Epilogue* ep, const char* what, hipStream_t st) {
-  Epilogue e = {};
-  e.act = FP8Q_ACT_NONE;
-  if (ep) e = *ep;
+template <int FA, int FB>
+static void launch_f(const Proj& p, const Epilogue* e, hipStream_t st) {
+  constexpr int BLK = FP8Q_GRAN_128x128;
+  if (e) launch_out<FA, FB, BLK, false>(p, *e, st);
+  else if (p.B1) launch_out<FA, FB, BLK, true>(p, Nothing{}, st);
+  else if (p.gb == FP8Q_GRAN_1x128) launch_out<FA, FB, FP8Q_GRAN_1x128, false>(p, Nothing{}, st);
+  else launch_out<FA, FB, BLK, false>(p, Nothing{}, st);
+}
+
+int launch_few(const Proj& p, const Epilogue* e, const char* what, hipStream_t st) {
   if (p.fa == FP8Q_E4M3FN && p.fb == FP8Q_E4M3FN) launch_f<0, 0>(p, e, st);
   else if (p.fa == FP8Q_E5M2 && p.fb == FP8Q_E4M3FN) launch_f<1, 0>(p, e, st);
   else if (p.fa == FP8Q_E4M3FN) launch_f<0, 1>(p, e, st);

@@ -209,7 +209,7 @@ struct Epilogue {
 };
 // Rows the product of a few rows takes at most.
 static constexpr int64_t kFewRows = 64;
-// e (nullable, plain products only): a linear layer's epilogue.
+// e (nullable; plain products with 128x128 B scales only): a linear layer's epilogue.
 int launch_few(const Proj& p, const Epilogue* e, const char* what, hipStream_t st);
 // The linear layer: p.out as out_dt, or codes and p.scales; p.ws as the workspace.
 int launch_linear(const Proj& p, const Epilogue& e, bool fast, const char* what, hipStream_t st);
