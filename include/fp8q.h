@@ -544,7 +544,8 @@ int fp8q_layernorm_bwd(const void* dy, fp8q_dtype dt, int64_t lddy, const void* 
  * SiLU and both GELUs give NaN at -Inf.
  * ws: ws_bytes >= fp8q_linear_blockscaled_workspace, 16-B aligned,
  * overwritten; NULL where that is 0.  Calls in flight must not share it.
- * The order of every sum is fixed by M, N and K alone.
+ * The order of every sum is fixed by M, N, K, exact or _fast, and the device's
+ * number of compute units: the same bits every call.
  * K % 128 == 0 (else FP8Q_ESHAPE); M, N >= 1; alignment as the GEMM; C, res
  * and pre aligned to their elements.  A and B each span less than 4 GiB (else
  * FP8Q_ESHAPE), in the forms below too. */
@@ -584,8 +585,11 @@ int fp8q_linear_blockscaled_q_fast(const uint8_t* A, fp8q_format fa, int64_t lda
                                    int64_t ws_bytes, void* stream);
 
 /* Bytes of workspace the linear layer's forms need: `fast` (0 or 1) for the
- * _fast forms, `codes` for the _q forms.  0 for many rows, and for sizes they
- * refuse.  The answer holds on the device that is current when it is asked. */
+ * _fast forms, `codes` for the _q forms.  Ask for any size: 4*M*N for the codes
+ * of a few rows, and of few rows or many the tiles that do not fill a round of
+ * the device's compute units may leave partial sums, less than 4 MiB for each
+ * compute unit in all.  0 where neither happens, and for sizes they refuse.  The
+ * answer holds on the device that is current when it is asked. */
 int64_t fp8q_linear_blockscaled_workspace(int fast, int codes, int64_t M, int64_t N, int64_t K);
 
 /* Bytes of workspace fp8q_linear_bwd_q needs for the bias's gradient: 4*N for

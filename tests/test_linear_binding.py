@@ -89,3 +89,29 @@ def test_a_workspace_that_is_given_is_not_asked_for(fq, two_devices):
         current, called, dev, args = two_devices.called.pop()
         assert (current, called, dev) == (1, name, 1) and args[-3:] == (t, 99, 1001)
         assert not (two_devices.asked or two_devices.given)
+
+
+def test_linear_workspace_of_any_size(fq):
+    """Many rows may need one too, and a call without it is refused; bounded as the header says."""
+    import random
+
+    w = fq.fp8q_linear_blockscaled_workspace
+    M, N, K = 8192, 7168, 18432
+    need = w(1, 0, M, N, K)
+    assert need > 0 and w(1, 1, M, N, K) == need
+    p = 0x10000  # never dereferenced
+    args = lambda ws, n: (p, 0, K, p, K // 128, 1, p, 0, K, p, K // 128, 1, None, 0, fq.ACT_NONE, None, 0, p, fq.BF16, N, None, 0,  # noqa: E731
+                          M, N, K, ws, n, None)
+    for ws, n in ((None, 0), (None, need), (p, need - 1)):
+        assert fq.lib().fp8q_linear_blockscaled_fast(*args(ws, n)) == fq.EINVAL
+        assert str(need) in fq.lib().fp8q_last_error().decode()
+    assert fq.lib().fp8q_linear_blockscaled_fast(*args(p + 8, need)) == fq.EALIGN
+    rng = random.Random(1)
+    units = torch.cuda.get_device_properties(0).multi_processor_count if torch.cuda.is_available() else 256
+    for _ in range(4000):
+        M, N, K = (max(1, round(2 ** rng.uniform(0, 15))) for _ in range(3))
+        N, K = -(-N // 128) * 128, -(-K // 128) * 128
+        for fast in (0, 1):
+            for codes in (0, 1):
+                n = w(fast, codes, M, N, K)
+                assert n == codes * 4 * M * N or 0 <= n < units << 22, (fast, codes, M, N, K, n)
