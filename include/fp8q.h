@@ -501,7 +501,9 @@ int fp8q_gemm_blockscaled_few(const uint8_t* A, fp8q_format fa, int64_t lda, con
  * norm_eps > 0; every pointer and row 16-B aligned (scales, mean, rstd 4-B).
  * A row that holds an Inf or a NaN gives NaN throughout (codes 0x7F, NaN
  * scales); where the fp32 sum of squares overflows (distances from the mean
- * whose root sum of squares passes 1.8e19) rstd is 0 and y is b.  At most 2^31-1 rows. */
+ * whose root sum of squares passes 1.8e19) rstd is 0 and y is b; where a sum of
+ * the row's own values passes fp32's largest, its mean is not finite and y is
+ * NaN throughout, as for an Inf.  At most 2^31-1 rows. */
 int fp8q_layernorm_1x128(const void* x, fp8q_dtype dt, int64_t ldx, const void* res, int64_t ldr, const void* w,
                          const void* b, fp8q_dtype wdt, int64_t rows, int64_t cols, float norm_eps, void* z, int64_t ldz,
                          void* y, int64_t ldy, fp8q_format f, float eps, uint8_t* q, int64_t ldq, float* scales,

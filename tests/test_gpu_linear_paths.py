@@ -3,7 +3,7 @@ import pytest
 import torch
 
 from block_scaled_precision_amax_amd import workloads as W
-from test_gpu_linear import E4, E5, EPS, ERF, GELU, NONE, RELU, SILU, U, act64, bwd_call, check_codes
+from test_gpu_linear import E4, E5, EPS, ERF, GELU, NONE, RELU, SILU, U, act64, bwd_call, check_codes, run_norm
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +52,26 @@ def test_an_infinite_pre_activation_spoils_nothing(fq, gpu, act):
     pre[130, 200] = INF
     got = bwd_call(fq, dC, pre, act, E5, E4, M, N, want_h=False)
     assert all(a is None or torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------------ layer norm
+@pytest.mark.parametrize("rows,cols", [(4, 512), (4, 2304), (2052, 8192)])
+def test_layernorm_of_rows_whose_sums_overflow(fq, gpu, rows, cols):
+    """Finite rows near fp32's largest value: where only the squares overflow the bias is left, where the sum itself does
+    the row is NaN as if it held an Inf, and the other rows know nothing of it."""
+    x = torch.randn(rows, cols, device=gpu, generator=torch.Generator(gpu).manual_seed(3))
+    b = torch.linspace(-1, 1, cols, device=gpu)
+    want = run_norm(fq, x, None, None, b, E4)
+    bad = x.clone()
+    bad[0] = 1e38
+    bad[1] = torch.tensor([1e38, -1e38], device=gpu).repeat(cols // 2)  # every partial sum of a pair is 0
+    bad[3] = -3e38
+    z, y, q, s, mean, rstd = run_norm(fq, bad, None, None, b, E4)
+    assert torch.equal(z, bad)
+    for i, sign in ((0, INF), (3, -INF)):
+        assert mean[i] == sign and rstd[i] == 0
+        assert y[i].isnan().all() and (q[i] == 0x7F).all() and s[i].isnan().all()
+    assert mean[1] == 0 and rstd[1] == 0 and torch.equal(y[1], b)
+    keep = torch.arange(rows, device=gpu) > 3
+    keep[2] = True
+    assert all(torch.equal(a[keep], c[keep]) for a, c in zip((z, y, q, s, mean, rstd), want))
