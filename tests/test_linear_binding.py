@@ -115,3 +115,9 @@ def test_linear_workspace_of_any_size(fq):
             for codes in (0, 1):
                 n = w(fast, codes, M, N, K)
                 assert n == codes * 4 * M * N or 0 <= n < units << 22, (fast, codes, M, N, K, n)
+
+
+def test_layernorm_bwd_workspace_is_at_most_2048_bytes_a_column(fq):
+    for cols in (8, 128, 1608, 4096, 16384, 65536):
+        assert max(fq.fp8q_layernorm_bwd_workspace(r, cols) for r in (1, 255, 256, 257, 513, 1025, 70000, (1 << 31) - 1)) \
+            == 2048 * cols
