@@ -25,6 +25,13 @@
 
 namespace fp8q {
 
+// The tiles of one launch: `count` from number `first` of the ntm x ntn tile
+// grid, or (halves) both halves of count / 2 tiles of twice this height.
+struct Part {
+  int64_t ntm, ntn, first, count;
+  bool halves;
+};
+
 // A BM x 128 tile of T through LDS: `put` is called for the lane's 4-column
 // pieces, then whole rows leave 16 bytes a lane.  Chunk c of row r sits in
 // slot c ^ (r & 15), so the sixteen rows of a write fall on different banks.
@@ -183,6 +190,32 @@ __global__ __launch_bounds__(kThreads, 1) void k_glu(const Proj p, const float* 
     __syncthreads();  // the epilogue's LDS reads precede the next tile's copies
   }
 }
+
+// How a product of ntn tile columns is cut, and what it costs in thousandths
+// of a microsecond per K block.  A round of up to a tile per compute unit takes
+// 1.4 us a block with tall tiles (256 rows FP8-MFMA, 128 exact) and 0.85 with
+// low ones (half the rows) while few units work, 1.7 and 1.05 when all do.
+// So: whole rounds of tall tiles, and the rest, if it is at most half a
+// round, as a second launch of its halves; or low tiles throughout.
+//   exact 1023 x 9000 x 4096 (568 tall tiles): 163 us in three rounds, 146 in
+//   two and a round of halves; fast 128 x 18432 x 7168: 94 us tall, 75 low.
+struct Cut {
+  bool low;       // low tiles throughout
+  int64_t tall;   // tall tiles, then
+  int64_t split;  // tall tiles taken as halves
+  int64_t cost;
+};
+static Cut cut_tiles(int64_t M, int64_t rows, int64_t ntn, int64_t launch_cost) {
+  const int64_t cu = grid_size(), tiles = (M + rows - 1) / rows * ntn;
+  const int64_t low = 850 * ((((M + rows / 2 - 1) / (rows / 2)) * ntn + cu - 1) / cu);
+  const int64_t full = tiles / cu, rest = tiles - full * cu;
+  const bool split = full > 0 && rest > 0 && 2 * rest <= cu && 850 + launch_cost < 1360;
+  const int64_t tall = 1360 * full + (rest == 0 ? 0 : split ? 850 + launch_cost : 1360);
+  if (low < tall) return {true, 0, 0, low};
+  return {false, split ? full * cu : tiles, split ? rest : 0, tall};
+}
+// A second launch costs about 3 us.
+static int64_t second_launch(int64_t K) { return 3000 * 128 / K; }
 
 template <int FA, int FB, int OUT, bool FAST, int TI, bool GLU>
 static void launch_part(const Proj& p, const Part& t, hipStream_t st) {

@@ -1,6 +1,6 @@
-// Tiles of block-scaled FP8 products: their shape, the loop over K that fills
-// a tile's accumulators, and how a product is cut into tiles.  Shared by the
-// gated projection (fp8q_glu.hip) and the linear layer (fp8q_linear.hip).
+// Tiles of block-scaled FP8 products: their shape and the loop over K that
+// fills a tile's accumulators.  Shared by the gated projection (fp8q_glu.hip)
+// and the linear layer (fp8q_linear.hip).
 //
 // fast: 256 rows (or 128), v_mfma_scale_f32_16x16x128_f8f6f4 on the codes;
 // exact: 128 rows (or 64), codes decoded to bf16 / f16 without loss and
@@ -17,13 +17,6 @@ using namespace ffn;
 static constexpr int BK = 128;
 static constexpr int kThreads = 512;
 static constexpr int TJ = 4;
-
-// The tiles of one launch: `count` from number `first` of the ntm x ntn tile
-// grid, or (halves) both halves of count / 2 tiles of twice this height.
-struct Part {
-  int64_t ntm, ntn, first, count;
-  bool halves;
-};
 
 template <bool FAST, int TI_>
 struct Shape {
@@ -319,31 +312,5 @@ static int64_t grid_size() {
   const int64_t g = device_cu_count() / 8 * 8;
   return g < 8 ? 8 : g;
 }
-
-// How a product of ntn tile columns is cut, and what it costs in thousandths
-// of a microsecond per K block.  A round of up to a tile per compute unit takes
-// 1.4 us a block with tall tiles (256 rows FP8-MFMA, 128 exact) and 0.85 with
-// low ones (half the rows) while few units work, 1.7 and 1.05 when all do.
-// So: whole rounds of tall tiles, and the rest, if it is at most half a
-// round, as a second launch of its halves; or low tiles throughout.
-//   exact 1023 x 9000 x 4096 (568 tall tiles): 163 us in three rounds, 146 in
-//   two and a round of halves; fast 128 x 18432 x 7168: 94 us tall, 75 low.
-struct Cut {
-  bool low;       // low tiles throughout
-  int64_t tall;   // tall tiles, then
-  int64_t split;  // tall tiles taken as halves
-  int64_t cost;
-};
-static Cut cut_tiles(int64_t M, int64_t rows, int64_t ntn, int64_t launch_cost) {
-  const int64_t cu = grid_size(), tiles = (M + rows - 1) / rows * ntn;
-  const int64_t low = 850 * ((((M + rows / 2 - 1) / (rows / 2)) * ntn + cu - 1) / cu);
-  const int64_t full = tiles / cu, rest = tiles - full * cu;
-  const bool split = full > 0 && rest > 0 && 2 * rest <= cu && 850 + launch_cost < 1360;
-  const int64_t tall = 1360 * full + (rest == 0 ? 0 : split ? 850 + launch_cost : 1360);
-  if (low < tall) return {true, 0, 0, low};
-  return {false, split ? full * cu : tiles, split ? rest : 0, tall};
-}
-// A second launch costs about 3 us.
-static int64_t second_launch(int64_t K) { return 3000 * 128 / K; }
 
 }  // namespace fp8q
