@@ -27,7 +27,8 @@ CALL_LIB = os.path.join(HERE, "_fp8q_call.so")
 ARCH = os.environ.get("FP8Q_ARCH", "gfx950")
 
 SOURCES = ["fp8q_api.hip", "fp8q_quant.hip", "fp8q_gemm.hip", "fp8q_norm.hip", "fp8q_few.hip",
-           "fp8q_glu.hip", "fp8q_glu_bwd.hip", "fp8q_layernorm.hip", "fp8q_linear.hip", "fp8q_linear_bwd.hip"]
+           "fp8q_glu.hip", "fp8q_glu_bwd.hip", "fp8q_layernorm.hip", "fp8q_linear.hip", "fp8q_linear_e4m3_e4m3.hip",
+           "fp8q_linear_e4m3_e5m2.hip", "fp8q_linear_e5m2_e4m3.hip", "fp8q_linear_e5m2_e5m2.hip", "fp8q_linear_bwd.hip"]
 STREAM_SOURCES = ["fp8q_stream.hip"]
 
 COMMON = [

@@ -1,6 +1,6 @@
 // Tiles of block-scaled FP8 products: their shape and the loop over K that
 // fills a tile's accumulators.  Shared by the gated projection (fp8q_glu.hip)
-// and the linear layer (fp8q_linear.hip).
+// and the linear layer (fp8q_linear.h).
 //
 // fast: 256 rows (or 128), v_mfma_scale_f32_16x16x128_f8f6f4 on the codes;
 // exact: 128 rows (or 64), codes decoded to bf16 / f16 without loss and
