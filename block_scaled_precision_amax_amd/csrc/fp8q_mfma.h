@@ -148,13 +148,14 @@ __device__ __forceinline__ float linear_act_bwd(float dc, float g, float& h) {
     h = g * p;
     return dc * __builtin_fmaf(__builtin_amdgcn_fmed3f(g, -128.0f, 128.0f) * p, 1.0f - p, p);
   } else {
-    // p = sigmoid(2 k), k = c (g + a g^3): p' = p (1 - p) 2 c (1 + 3 a g^2).  Beyond 16 p is 0 or 1; the clamp
-    // keeps a NaN
+    // p = sigmoid(2 k), k = c (g + a g^3): p' = p (1 - p) 2 c (1 + 3 a g^2).  Beyond 16 p is 0 or 1.  The exponent
+    // has g itself, which leaves p a NaN where the clamp does not
     constexpr float c2 = 2.0f * 0.7978845608028654f, a = 0.044715f, l = -1.4426950408889634f;
-    const float x = __builtin_elementwise_minimum(__builtin_elementwise_maximum(g, -16.0f), 16.0f), x2 = x * x;
-    const float p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * __builtin_fmaf(x2, l * c2 * a, l * c2)));
+    const float x = __builtin_amdgcn_fmed3f(g, -16.0f, 16.0f), x2 = x * x;
+    const float p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * __builtin_fmaf(x2, l * c2 * a, l * c2)));
+    const float q = x * p;
     h = g * p;
-    return dc * __builtin_fmaf(x * p * (1.0f - p), __builtin_fmaf(x2, 3.0f * a * c2, c2), p);
+    return dc * __builtin_fmaf(__builtin_fmaf(-q, p, q), __builtin_fmaf(x2, 3.0f * a * c2, c2), p);
   }
 }
 // f with the activation as a constant: the choice is made once around a
