@@ -53,6 +53,10 @@ bool valid_dt(int dt) { return dt == FP8Q_F32 || dt == FP8Q_BF16; }
 bool valid_fmt(int f) { return f == FP8Q_E4M3FN || f == FP8Q_E5M2; }
 int64_t esize(int dt) { return dt == FP8Q_F32 ? 4 : 2; }
 hipStream_t S(void* s) { return (hipStream_t)s; }
+// Whether rows of K bytes, ld >= K >= 1 bytes apart, span less than 4 GiB: the
+// kernels' per-lane operand offsets have 32 bits.  The product is not formed,
+// it may pass 64.
+bool under_4gib(int64_t rows, int64_t ld, int64_t K) { return K <= 0xFFFFFFFFll && rows - 1 <= (0xFFFFFFFFll - K) / ld; }
 
 // Shared checks of the two block quantizers.
 int check_block_quant(const char* fn, const void* x, int dt, int64_t rows, int64_t cols, int64_t ldx,
@@ -119,9 +123,7 @@ int check_proj(const char* fn, const uint8_t* A, int fa, int64_t lda, const floa
   if (!aligned(A, 16) || !aligned(B0, 16) || !aligned(B1, 16) || lda % 16 != 0 || ldb % 16 != 0)
     return fail(FP8Q_EALIGN, "%s: the operands and their leading dimensions must be 16-byte aligned", fn);
   if (!aligned(sA, 4) || !aligned(s0, 4) || !aligned(s1, 4)) return fail(FP8Q_EALIGN, "%s: misaligned scales", fn);
-  // per-lane operand offsets are 32-bit
-  if ((M - 1) * lda + K > 0xFFFFFFFFll || (N - 1) * ldb + K > 0xFFFFFFFFll)
-    return fail(FP8Q_ESHAPE, "%s: an operand spans 4 GiB or more", fn);
+  if (!under_4gib(M, lda, K) || !under_4gib(N, ldb, K)) return fail(FP8Q_ESHAPE, "%s: an operand spans 4 GiB or more", fn);
   return FP8Q_OK;
 }
 // Shared checks of the linear layer's forms, C aside.
@@ -402,10 +404,10 @@ static int gemm_entry(const char* fn, const uint8_t* A, int fa, int64_t lda, con
     return fail(FP8Q_EALIGN, "%s: A, B and their leading dimensions must be 16-byte aligned", fn);
   if (!aligned(sA, 4) || !aligned(sB, 4) || !aligned(C, out_dt == FP8Q_F32 ? 4 : 2))
     return fail(FP8Q_EALIGN, "%s: misaligned scales or C", fn);
+  if (!under_4gib(M, lda, K) || !under_4gib(N, ldb, K)) return fail(FP8Q_ESHAPE, "%s: an operand spans 4 GiB or more", fn);
   // both kernels compute every element by the same instructions in the same
   // order; the tiles' heights alone differ
-  if (fast && gb == FP8Q_GRAN_128x128 && gemm_fast_cut(M, N, K) && (M - 1) * lda + K <= 0xFFFFFFFFll &&
-      (N - 1) * ldb + K <= 0xFFFFFFFFll) {
+  if (fast && gb == FP8Q_GRAN_128x128 && gemm_fast_cut(M, N, K)) {
     Proj p = make_proj(A, fa, lda, sA, sA_sm, sA_skb, B, nullptr, fb, ldb, sB, nullptr, gb, sB_sn, sB_skb, M, N, K);
     p.out = C, p.ldo = ldc, p.out_dt = out_dt;
     return launch_gemm_fast_cut(p, fn, S(stream));
@@ -442,6 +444,7 @@ int fp8q_gemm_blockscaled_q(const uint8_t* A, fp8q_format fa, int64_t lda, const
   if (!aligned(A, 16) || !aligned(B, 16) || lda % 16 != 0 || ldb % 16 != 0)
     return fail(FP8Q_EALIGN, "%s: A, B and their leading dimensions must be 16-byte aligned", fn);
   if (!aligned(sA, 4) || !aligned(sB, 4) || !aligned(Cs, 4)) return fail(FP8Q_EALIGN, "%s: misaligned scales", fn);
+  if (!under_4gib(M, lda, K) || !under_4gib(N, ldb, K)) return fail(FP8Q_ESHAPE, "%s: an operand spans 4 GiB or more", fn);
   return launch_gemm_q(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, gb, sB_sn, sB_skb, fc, eps, Cq, ldcq, Cs,
                        ld_cs, M, N, K, S(stream));
 }
@@ -471,6 +474,7 @@ int fp8q_gemm_blockscaled_qt(const uint8_t* A, fp8q_format fa, int64_t lda, cons
     return fail(FP8Q_EALIGN, "%s: A, B, Cqt and their leading dimensions must be 16-byte aligned", fn);
   if (!aligned(sA, 4) || !aligned(sB, 4) || !aligned(Cst, 4) || (Cs && !aligned(Cs, 4)))
     return fail(FP8Q_EALIGN, "%s: misaligned scales", fn);
+  if (!under_4gib(M, lda, K) || !under_4gib(N, ldb, K)) return fail(FP8Q_ESHAPE, "%s: an operand spans 4 GiB or more", fn);
   return launch_gemm_qt(A, fa, lda, sA, sA_sm, sA_skb, B, fb, ldb, sB, gb, sB_sn, sB_skb, fc, eps, Cqt, ldcqt, Cst,
                         ld_cst, Cq, ldcq, Cs, ld_cs, M, N, K, S(stream));
 }
@@ -490,6 +494,7 @@ int fp8q_gemm_mx(const uint8_t* A, fp8q_format fa, int64_t lda, const uint8_t* s
   if (!aligned(sA, 4) || !aligned(sB, 4) || ld_sa % 4 != 0 || ld_sb % 4 != 0 ||
       !aligned(C, out_dt == FP8Q_F32 ? 4 : 2))
     return fail(FP8Q_EALIGN, "%s: scale rows must be 4-byte aligned; C aligned to its element", fn);
+  if (!under_4gib(M, lda, K) || !under_4gib(N, ldb, K)) return fail(FP8Q_ESHAPE, "%s: an operand spans 4 GiB or more", fn);
   return launch_gemm_mx(A, fa, lda, sA, ld_sa, B, fb, ldb, sB, ld_sb, C, out_dt, ldc, M, N, K, S(stream));
 }
 
@@ -732,7 +737,7 @@ int fp8q_linear_blockscaled_q_fast(const uint8_t* A, fp8q_format fa, int64_t lda
 
 int64_t fp8q_linear_blockscaled_workspace(int fast, int codes, int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0 || K <= 0 || K % 128 != 0 || (codes && N % 128 != 0)) return 0;
-  if ((M - 1) * K + K > 0xFFFFFFFFll || (N - 1) * K + K > 0xFFFFFFFFll) return 0;
+  if (!under_4gib(M, K, K) || !under_4gib(N, K, K)) return 0;
   return linear_workspace(fast != 0, codes != 0, M, N, K);
 }
 

@@ -1,6 +1,5 @@
-"""The binding of the layer norm and the linear layer without a GPU: what it asks of the library and of torch, on which
-device and stream, with both replaced by recorders."""
-import contextlib
+"""The layer norm and the linear layer without a GPU: what the binding asks of the library and of torch, on which device and
+stream (with both replaced by recorders), workspaces, and refusals of sizes that overflow."""
 import types
 
 import pytest
@@ -121,3 +120,51 @@ def test_layernorm_bwd_workspace_is_at_most_2048_bytes_a_column(fq):
     for cols in (8, 128, 1608, 4096, 16384, 65536):
         assert max(fq.fp8q_layernorm_bwd_workspace(r, cols) for r in (1, 255, 256, 257, 513, 1025, 70000, (1 << 31) - 1)) \
             == 2048 * cols
+
+
+SPANS = [dict(M=(1 << 57) + 128), dict(N=(1 << 57) + 128), dict(M=(1 << 62) + 128), dict(M=(1 << 33) + 128, lda=1 << 31),
+         dict(N=(1 << 29) + 128, ldb=1 << 35), dict(K=(1 << 63) - 128, lda=(1 << 63) - 16, ldb=(1 << 63) - 16)]
+
+
+@pytest.mark.parametrize("kw", SPANS)
+@pytest.mark.parametrize("form", ["linear", "linear_fast", "linear_q", "linear_q_fast", "gemm", "gemm_fast", "gemm_q", "gemm_qt",
+                                  "gemm_mx", "gemm_few", "glu", "glu_fast", "glu_q"])
+def test_spans_that_pass_64_bits_are_refused(fq, form, kw):
+    """The 4 GiB limit holds where the span itself overflows 64 bits and comes out small."""
+    p, far, L = 0x10000, 1 << 60, fq.lib()  # p is never dereferenced
+    c = dict(dict(M=128, N=128, K=128, lda=128, ldb=128), **kw)
+    M, N, K = c["M"], c["N"], c["K"]
+    if form == "gemm_few":
+        M = min(M, 64)
+    a, b, d, ld = (p, 0, c["lda"], p, 1, 1), (p, 0, c["ldb"], p), (M, N, K), max(N, M, 128)
+    g, ep = (fq.GRAN_128x128, 1, 1), (None, 0, fq.ACT_NONE)
+    glu = (*a, p, p, 0, c["ldb"], p, p, 1, 1, fq.ACT_SILU)
+    rc = {
+        "linear": lambda: L.fp8q_linear_blockscaled(*a, *b, 1, 1, *ep, None, 0, p, 0, ld, None, 0, *d, p, far, None),
+        "linear_fast": lambda: L.fp8q_linear_blockscaled_fast(*a, *b, 1, 1, *ep, None, 0, p, 0, ld, None, 0, *d, p, far, None),
+        "linear_q": lambda: L.fp8q_linear_blockscaled_q(*a, *b, 1, 1, *ep, 0, 1e-12, p, ld, p, ld, None, 0, *d, p, far, None),
+        "linear_q_fast": lambda: L.fp8q_linear_blockscaled_q_fast(*a, *b, 1, 1, *ep, 0, 1e-12, p, ld, p, ld, None, 0, *d, p, far,
+                                                                  None),
+        "gemm": lambda: L.fp8q_gemm_blockscaled(*a, *b, *g, p, 0, ld, *d, None),
+        "gemm_fast": lambda: L.fp8q_gemm_blockscaled_fast(*a, *b, *g, p, 0, ld, *d, None),
+        "gemm_q": lambda: L.fp8q_gemm_blockscaled_q(*a, *b, *g, 0, 1e-12, p, ld, p, ld, *d, None),
+        "gemm_qt": lambda: L.fp8q_gemm_blockscaled_qt(*a, *b, *g, 0, 1e-12, p, ld, p, ld, None, 0, None, 0, *d, None),
+        "gemm_mx": lambda: L.fp8q_gemm_mx(*a[:4], far, *b, far, p, 0, ld, *d, None),
+        "gemm_few": lambda: L.fp8q_gemm_blockscaled_few(*a, *b, *g, p, 0, ld, *d, None),
+        "glu": lambda: L.fp8q_glu_blockscaled(*glu, p, 0, ld, None, 0, *d, None),
+        "glu_fast": lambda: L.fp8q_glu_blockscaled_fast(*glu, p, 0, ld, None, 0, *d, None),
+        "glu_q": lambda: L.fp8q_glu_blockscaled_q(*glu, 0, 1e-12, p, ld, p, ld, None, 0, *d, p, far, None),
+    }[form]()
+    if form == "gemm_few" and "M" in kw and "lda" not in kw:
+        return  # at most 64 rows: nothing overflows
+    assert rc == fq.ESHAPE, fq.lib().fp8q_last_error().decode()
+    assert "4 GiB" in fq.lib().fp8q_last_error().decode()
+
+
+def test_no_workspace_for_sizes_whose_span_passes_64_bits(fq):
+    w = fq.fp8q_linear_blockscaled_workspace
+    for fast in (0, 1):
+        for codes in (0, 1):
+            for M, N, K in (((1 << 57) + 1, 128, 128), (16, 1 << 57, 128), (16, 128, 1 << 62), (16, (1 << 62) + 128, 128),
+                            (16, 128, (1 << 63) - 128), ((1 << 63) - 1, 128, 128), (17, 1 << 59, 128)):
+                assert w(fast, codes, M, N, K) == 0, (M, N, K)
