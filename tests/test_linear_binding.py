@@ -1,5 +1,6 @@
 """The layer norm and the linear layer without a GPU: what the binding asks of the library and of torch, on which device and
 stream (with both replaced by recorders), workspaces, and refusals of sizes that overflow."""
+import contextlib
 import types
 
 import pytest
