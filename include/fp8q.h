@@ -612,7 +612,8 @@ int64_t fp8q_linear_bwd_q_workspace(int64_t M, int64_t N);
  *     next layer's weight gradient;
  *   dbias (nullable): N fp32, overwritten; sums in an order fixed by M and N.
  * Mp is M rounded up to a multiple of 128: the padding is written as zero
- * codes, so any M can be reduced over.  fc: format of D; eps the amax clamp.
+ * codes (0x7F in a block that holds a NaN, as its scale is one), so any M can
+ * be reduced over.  fc: format of D; eps the amax clamp.
  * ReLU's gradient is 0 where pre <= 0, whatever dC holds there.  Where pre is
  * +Inf or -Inf, act' is its limit, 1 or 0 (none: 1), and H what the forward gives:
  * +Inf stays, -Inf is 0 for ReLU and NaN for SiLU and both GELUs.
