@@ -17,7 +17,7 @@
 // registers, and not mean(v^2) - mean^2, which loses it where a row lies far
 // from zero.
 //   16384 x 7168 bf16 with residual: forward to z, codes and statistics
-//   (826 MB) 150 us, gradients (940 MB) 156 us, where an elementwise pass that
+//   (826 MB) 151 us, gradients (940 MB) 157 us, where an elementwise pass that
 //   moves 6.19 TB/s takes 133 and 152.
 //   One row of 7168: 4.5 us, the latency of two loads (the row, then weight and
 //   bias), two sums across the workgroup and the stores.

@@ -11,18 +11,23 @@
 // workspace and a second kernel joins them, with the same epilogue.
 //
 // What bounds it, measured:
-//   1 x 18432 x 7168, GELU, codes: HBM, 132 MB of weight in 23 us of k_few, 4.6
+//   1 x 18432 x 7168, GELU, codes: HBM, 132 MB of weight in 22.6 us of k_few, 4
 //     for the epilogue's launch;
-//   48 x 7168 x 18432 with residual, exact: 30.5 us in 9 parts of K (the weight at
-//     4.4 TB/s and 12 MB of sums out), 7.5 to join them;
-//   1023 x 9000 x 4096, GELU, exact fp32: 96 us + 7.4: 1.57 us a block of K (1.45 at
-//     the rate of a large bf16 product), but 32 of the 288 tiles are left after a
-//     round, and neither round's epilogue has anything beside it;
-//   16384 x 18432 x 7168, erf GELU, codes and pre-activations, exact: 3900 us
-//     (to 4040), 1110 TFLOP/s: the decode takes the vector ALU's slots, and after some
-//     milliseconds the clock falls (2.0 us a block of K);
-//   8192 x 7168 x 18432 with residual, FP8-MFMA: 955 us + 28 to join the last
-//     128 tiles, 2240 TFLOP/s, LDS and matrix issue, clock.
+//   48 x 7168 x 18432 with residual, exact: 28 us in 9 parts of K (the weight at
+//     4.7 TB/s and 12 MB of sums out), 7 to join them;
+//   1023 x 9000 x 4096, GELU, exact fp32: 89 to 91 us + 7: 40 blocks of K (the round's 32,
+//     and 8 for the 32 tiles left after it, in 4 parts) at 1.5 to 1.6 us; the rest is
+//     two starts and a tile's epilogue with nothing beside them;
+//   16384 x 18432 x 7168, erf GELU, codes and pre-activations, exact: 3950 to 4160
+//     us, 1040 to 1100 TFLOP/s.  By the slope over K 3.9 ms are blocks of K, 1.92 us
+//     each where a single round of tiles takes 1.67 (the decode takes the vector
+//     ALU's slots, and a long run the clock) and the plain product with codes 1.80;
+//     0.27 are the 36 rounds' epilogues with the matrix cores idle, 7.5 us a tile,
+//     1.6 of them without bias, activation and pre-activations;
+//   the same on FP8-MFMA: 2140 to 2230 us, 1.8 to 2.1 us a block of K and 21 a
+//     tile's epilogue, 10 without those three; fp32 instead of codes 2235 to 2260;
+//   8192 x 7168 x 18432 with residual, FP8-MFMA: 938 to 969 us + 28 to join the
+//     last 128 tiles, 2180 to 2240 TFLOP/s, LDS and matrix issue, clock.
 #include "fp8q_linear.h"
 
 namespace fp8q {
@@ -81,7 +86,9 @@ __global__ __launch_bounds__(256) void k_linear_finish(const Proj p, const Epilo
 // operand in HBM:
 //   a block of K of a tile, all compute units at work: exact 1050 (64 rows) and
 //   1680 (128), FP8-MFMA 980 (128) and 1600 (256); its start and end 2500 and
-//   5000; a join 4000 and its bytes, written and read, at 4 TB/s;
+//   5000, of outputs without activation (with one and the pre-activations kept
+//   7500 exact and 21000 FP8-MFMA, which every way of tiles pays); a join 4000 and
+//   its bytes, written and read, at 4 TB/s;
 //   a workgroup of the few-row kernel, a block of K: 80 with 16 rows and columns,
 //   85 + 44 for each 16 rows with 32 columns; its start and end 1500.
 // A round is a workgroup per compute unit.

@@ -9,11 +9,11 @@
 // 128 tokens for the bias and, recomputed, the codes of h^T along tokens (the
 // operand of the next layer's weight gradient).  Nothing wide is written: 4
 // bytes are read and 3 written per element (bf16, h asked for).
-//   8192 x 18432, GELU, h asked for: 1.07 GB in 212 us + 5 for the bias's sum
-//   (5.1 TB/s; 173 us at an elementwise pass's 6.19): the vector ALU is busy
+//   8192 x 18432, GELU, h asked for: 1.07 GB in 213 to 221 us + 5 for the bias's
+//   sum (4.9 TB/s; 173 us at an elementwise pass's 6.19): the vector ALU is busy
 //   88 % of it, some 43 instructions an element for the activation with its
 //   derivative and three quantized outputs.  1000 x 4096 ReLU fp32 without h:
-//   9.8 + 2.3 us (33 MB, 5.4 us): one turn of latency and the second launch.
+//   9.7 + 1.6 us (33 MB, 5.4 us): one turn of latency and the second launch.
 //
 // A workgroup of 512 threads takes 128 tokens x 128 features, so both kinds
 // of block lie inside it.  Thread (rg, cl) holds tokens 4rg .. 4rg + 3 and

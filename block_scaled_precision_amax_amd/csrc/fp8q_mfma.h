@@ -97,7 +97,7 @@ __device__ __forceinline__ float activation(float g) {
 // g * P(g) with P the normal distribution function.  For a = |g| and
 // Q(a) = 1 - P(a): Q = exp(-a^2/2) t poly(t), t = 1 / (1 + 0.3 a), where the
 // polynomial is fitted to Q exp(a^2/2) / t for 0 <= a <= 14 (relative error
-// 2^-22.7, least maximum; Q is 0 in fp32 from 13.2 on), and P(g) = Q for g < 0, 1 - Q
+// 2^-22.4, constants rounded to fp32; Q is 0 in fp32 from 13.2 on), and P(g) = Q for g < 0, 1 - Q
 // otherwise, so neither tail cancels.  With the hardware's exponential and
 // reciprocal Q is off by (1.5 g^2 + 16) 2^-24 of its value: g^2 log2(e)/2 is
 // rounded twice and its constant once, the rest are a dozen roundings.
