@@ -202,3 +202,25 @@ def test_tiles_of_every_pair_of_formats(fq, gpu, fa, fb):
             f = fq.fp8q_linear_blockscaled_fast if fast else fq.fp8q_linear_blockscaled
             f(A, fa, K, sA, K // 128, 1, B, fb, K, sB, K // 128, 1, None, NONE, None, 0, C, N, None, 0, M, N, K)
             assert ((C.double() - v).abs() <= (2.0 ** -10 if fast else 1e-5) * D).all()
+
+
+def test_raw_pointers_without_a_workspace(fq, gpu):
+    """A's address alone, and addresses throughout: the workspace comes from the device at hand; few rows and parts of K."""
+    for M, N, K in ((3, 256, 512), (65, 256, 7168)):
+        A, sA, B, sB = operands(gpu, M, N, K, seed=M)
+        bias = W.normal((N,), seed=3, device=gpu)
+        outs = []
+        for p in (lambda t: t, lambda t: t.data_ptr() if t is A else t, lambda t: t.data_ptr() if t is not bias else t):
+            q, s = torch.zeros(M, N, dtype=torch.uint8, device=gpu), torch.zeros(M, N // 128, device=gpu)
+            fq.fp8q_linear_blockscaled_q(p(A), E4, K, p(sA), K // 128, 1, p(B), E4, K, p(sB), K // 128, 1, p(bias), GELU, E4, EPS,
+                                         p(q), N, p(s), N // 128, None, 0, M, N, K)
+            outs.append((q, s))
+        q, s = torch.zeros(M, N, dtype=torch.uint8, device=gpu), torch.zeros(M, N // 128, device=gpu)
+        a = [t.data_ptr() for t in (A, sA, B, sB, q, s)]
+        fq.fp8q_linear_blockscaled_q(a[0], E4, K, a[1], K // 128, 1, a[2], E4, K, a[3], K // 128, 1, None, GELU, E4, EPS, a[4], N,
+                                     a[5], N // 128, None, 0, M, N, K)
+        q2, s2 = torch.zeros_like(q), torch.zeros_like(s)
+        fq.fp8q_linear_blockscaled_q(A, E4, K, sA, K // 128, 1, B, E4, K, sB, K // 128, 1, None, GELU, E4, EPS, q2, N, s2, N // 128,
+                                     None, 0, M, N, K)
+        assert torch.equal(q, q2) and torch.equal(s, s2)
+        assert all(torch.equal(o[0], outs[0][0]) and torch.equal(o[1], outs[0][1]) for o in outs)
